@@ -51,7 +51,13 @@ enum {
   MOE_LORA_ERR_WORKSPACE = -5    /* workspace missing or too small                      */
 };
 
-typedef enum { MOE_LORA_F32 = 0, MOE_LORA_BF16 = 1, MOE_LORA_FP8_E4M3 = 2 } moe_lora_dtype;
+typedef enum {
+  MOE_LORA_F32 = 0,
+  MOE_LORA_BF16 = 1,
+  MOE_LORA_FP8_E4M3 = 2,
+  MOE_LORA_U8 = 3,  /* bytes, copied as they are (moe_lora_permute) */
+  MOE_LORA_MX4 = 4  /* e2m1 codes and e8m0 scales (moe_lora_mx4_gemm) */
+} moe_lora_dtype;
 
 /* Human-readable text of a status code (static storage, never NULL). */
 const char* moe_lora_status_str(int status);
@@ -154,6 +160,23 @@ int moe_lora_align(int32_t num_tokens, int32_t top_k, int32_t num_experts, int32
                    const int32_t* adapter_enabled, int32_t* sorted_pair_ids, int32_t* tile_expert,
                    int32_t* tile_lora, int32_t* expert_tile_offsets, int32_t* num_rows_padded,
                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_lora_align_pair_rows -- moe_lora_align that also writes the inverse of
+ * sorted_pair_ids:
+ *   pair_rows  [num_tokens, top_k] out  the row of each pair, or -1 for a pair
+ *                                   without one (its expert id is outside [0,
+ *                                   num_experts): under expert parallelism, an
+ *                                   expert of another rank).
+ * The other outputs, the workspace and the errors are those of moe_lora_align.
+ */
+int moe_lora_align_pair_rows(int32_t num_tokens, int32_t top_k, int32_t num_experts,
+                             int32_t num_loras, int32_t block_m, const int32_t* topk_ids,
+                             const int32_t* token_lora_mapping, const int32_t* adapter_enabled,
+                             int32_t* sorted_pair_ids, int32_t* tile_expert, int32_t* tile_lora,
+                             int32_t* expert_tile_offsets, int32_t* num_rows_padded,
+                             int32_t* pair_rows, void* workspace, size_t workspace_bytes,
+                             void* stream);
 
 /*
  * Device-side precondition checks (MOE_LORA_DEBUG builds, libmoe_lora_debug.so).
@@ -387,6 +410,127 @@ int moe_lora_dense_forward(const moe_lora_dense_args* args, void* stream);
  * Measurement only. */
 int moe_lora_dense_forward_events(const moe_lora_dense_args* args, void* stream,
                                   void* const* events);
+
+/*
+ * Rows in expert order and back.  With r(t, j) = pair_rows[t * top_k + j] of
+ * moe_lora_align_pair_rows (-1: the pair has no row, and takes no part):
+ *
+ *   moe_lora_permute             rows[r(t, j)] = x[t]
+ *   moe_lora_permute_backward    dx[t] = sum_j d_rows[r(t, j)]
+ *   moe_lora_unpermute           y[t] = sum_j w_tj * rows[r(t, j)]
+ *   moe_lora_unpermute_backward  d_rows[r(t, j)] = w_tj * dy[t],
+ *                                d_weights[t, j] = dy[t] . rows[r(t, j)]
+ *
+ *   x, dy, dx, y       [num_tokens, hidden]
+ *   rows, d_rows       [num_rows, hidden]  num_rows: rows that the buffer holds,
+ *                                          normally the capacity of the layout.
+ *   sorted_pair_ids, num_rows_padded, pair_rows: the layout.
+ *   topk_weights, d_weights [num_tokens, top_k] fp32.
+ *
+ * Sums over j are fp32, in ascending j, rounded once.  A token none of whose
+ * pairs has a row gets zeros; d_weights is 0 for a pair without a row.  Padding
+ * rows of rows / d_rows before *num_rows_padded are set to zero, rows behind it
+ * are left as they were; entries of pair_rows outside [0, num_rows) count as -1.
+ * What the pads of an input hold is never read.  There are no atomics: results
+ * do not change from run to run.  Inputs and outputs must not overlap.
+ *
+ * dtype is the type of the rows: F32 or BF16 (moe_lora_permute, whose x has it
+ * too, copies U8 as well: `hidden` bytes a row, for the codes and scales of MX4
+ * rows).  The tokens' type is given apart; the two may differ.  Any hidden from 1
+ * to 2^24 and any pointer aligned to its element works; rows of a multiple of 16
+ * bytes at 16-byte aligned addresses are moved 16 bytes at a time.
+ * num_tokens * top_k < 2^30, num_rows < 2^31 (else MOE_LORA_ERR_UNSUPPORTED).
+ *
+ * topk_weights NULL stands for ones (d_weights must then be NULL).  d_weights NULL
+ * skips it, and rows is then not read and may be NULL.
+ */
+int moe_lora_permute(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t dtype,
+                     int64_t num_rows, const void* x, const int32_t* sorted_pair_ids,
+                     const int32_t* pair_rows, const int32_t* num_rows_padded, void* rows,
+                     void* stream);
+int moe_lora_permute_backward(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t dtype,
+                              int32_t out_dtype, int64_t num_rows, const void* d_rows,
+                              const int32_t* pair_rows, void* dx, void* stream);
+int moe_lora_unpermute(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t dtype,
+                       int32_t out_dtype, int64_t num_rows, const void* rows,
+                       const int32_t* pair_rows, const float* topk_weights, void* y, void* stream);
+int moe_lora_unpermute_backward(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t dtype,
+                                int32_t dy_dtype, int64_t num_rows, const void* dy,
+                                const void* rows, const int32_t* sorted_pair_ids,
+                                const int32_t* pair_rows, const int32_t* num_rows_padded,
+                                const float* topk_weights, void* d_rows, float* d_weights,
+                                void* stream);
+
+/*
+ * MX4: 4-bit microscaled values (the OCP microscaling format with e2m1 elements).
+ * A matrix [num_rows, cols] is stored as
+ *   codes   [num_rows, cols / 2]   e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is
+ *                                  the sign), the even column in the low half;
+ *   scales  [num_rows, cols / 32]  e8m0 scale of 32 neighbouring columns: byte b
+ *                                  stands for 2^(b - 127), 255 for NaN.
+ * cols is a multiple of 32, at most 2^24.
+ *
+ * moe_lora_mx4_quantize: b = max(floor(log2(largest magnitude of the block)) - 2
+ * + 127, 0); codes round to nearest, ties to the even code, magnitudes past 6 to 6.
+ * A block that holds an infinity or a NaN gets the scale NaN and codes 0.  Codes
+ * and scales are exact: the same on every device.
+ *   num_rows_used  device int32, or NULL: rows from *num_rows_used on are skipped
+ *                  and their outputs left as they were (num_rows_padded of align).
+ * moe_lora_mx4_dequantize: code times scale, exact in fp32 and in bf16 (a magnitude
+ * past the largest finite value is an infinity).
+ * dtype (of x / out): F32 or BF16.  x, out and codes 16-byte aligned.
+ */
+int moe_lora_mx4_quantize(int64_t num_rows, int32_t cols, int32_t dtype, const void* x,
+                          const int32_t* num_rows_used, uint8_t* codes, uint8_t* scales,
+                          void* stream);
+int moe_lora_mx4_dequantize(int64_t num_rows, int32_t cols, int32_t dtype, const uint8_t* codes,
+                            const uint8_t* scales, void* out, void* stream);
+
+/*
+ * moe_lora_mx4_gemm -- products with MX4 weights, of rows in expert order or of
+ * all rows with one weight:
+ *
+ *   y[m, n] = sum_k x[m, k] W_e[n, k],   e = tile_expert[m / block_m]
+ *   out = y, or with silu_mul (out_features = 2 I; rows [0, I) of W are gate, [I, 2I)
+ *   up, as in w_gate_up)  out[m, i] = SiLU(y[m, i]) * y[m, I + i].
+ *
+ *   x        [num_rows, in_features] BF16, or MX4: codes [num_rows, in_features / 2]
+ *            with x_scale [num_rows, in_features / 32].
+ *   w        [num_experts, out_features, in_features / 2] codes,
+ *   w_scale  [num_experts, out_features, in_features / 32] scales.
+ *   tile_expert [num_rows / block_m] of moe_lora_align for this block_m; num_rows is a
+ *            multiple of block_m.  Rows of tiles whose entry is outside [0,
+ *            num_experts) (-1 past the end) are left as they were.  NULL: one weight
+ *            (num_experts == 1) for every row, any num_rows.
+ *   out      [num_rows, out_features] (silu_mul: out_features / 2), BF16 or F32.
+ *
+ * MX4 x goes through the matrix cores' own 4-bit products, BF16 x multiplies the
+ * weights expanded to bf16 (exactly, but for 4 and 6 under a scale byte of 253 or
+ * more, which are infinities there); sums are fp32, rounded once.  A row's result
+ * depends on that row alone: what padding rows hold reaches no other row.
+ * A workgroup covers rows of one tile_expert entry, so block_m is also the most
+ * rows that share one read of a weight: 16 for a few rows per expert, up to 256
+ * for many (a multiple of 64 at least from 64 rows per expert on).
+ * in_features: a multiple of 32; out_features: of 16 (32 with silu_mul); both at
+ * most 2^24; num_rows / 16 * out_features / 64 < 2^24 (else
+ * MOE_LORA_ERR_UNSUPPORTED).  x, w and out 16-byte aligned.  No workspace.
+ */
+typedef struct moe_lora_mx4_gemm_args {
+  size_t struct_size; /* sizeof(moe_lora_mx4_gemm_args) */
+  int32_t x_dtype;    /* MOE_LORA_BF16 or MOE_LORA_MX4 */
+  int32_t out_dtype;  /* MOE_LORA_BF16 or MOE_LORA_F32 */
+  int64_t num_rows;
+  int32_t out_features, in_features, num_experts, block_m;
+  int32_t silu_mul;
+  const void* x;
+  const uint8_t* x_scale;
+  const uint8_t* w;
+  const uint8_t* w_scale;
+  const int32_t* tile_expert;
+  void* out;
+} moe_lora_mx4_gemm_args;
+
+int moe_lora_mx4_gemm(const moe_lora_mx4_gemm_args* args, void* stream);
 
 #ifdef __cplusplus
 }

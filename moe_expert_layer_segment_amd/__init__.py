@@ -14,7 +14,16 @@ from .binding import (  # noqa: F401
     moe_lora_forward,
     moe_lora_forward_workspace_bytes,
     moe_lora_info,
+    moe_lora_mx4_dequantize,
+    moe_lora_mx4_gemm,
+    moe_lora_mx4_quantize,
+    moe_lora_permute,
+    moe_lora_permute_backward,
     moe_lora_route,
+    moe_lora_unpermute,
+    moe_lora_unpermute_backward,
+    mx4_block_m,
     run_dense,
     run_layer,
+    run_mx4_layer,
 )

@@ -19,7 +19,7 @@ LIB_PATH = os.environ.get("MOE_LORA_LIB") or os.path.join(_PKG, "lib", "libmoe_l
 DEBUG_LIB_PATH = os.path.join(_PKG, "lib", "libmoe_lora_debug.so")
 
 OK, ERR_INVALID, ERR_UNDERCOVER, ERR_UNSUPPORTED, ERR_HIP, ERR_WORKSPACE = 0, -1, -2, -3, -4, -5
-DTYPE_F32, DTYPE_BF16, DTYPE_FP8_E4M3 = 0, 1, 2
+DTYPE_F32, DTYPE_BF16, DTYPE_FP8_E4M3, DTYPE_U8, DTYPE_MX4 = 0, 1, 2, 3, 4
 _FP8_TORCH = (torch.uint8, torch.float8_e4m3fn)   # one-byte e4m3 codes
 FORWARD_STAGES = ("plan", "shrink_gate_up", "gate_up_gemm", "shrink_down", "down_gemm", "combine")
 
@@ -90,6 +90,27 @@ def _load(path: str) -> ctypes.CDLL:
     L.moe_lora_align.restype = ctypes.c_int
     L.moe_lora_align.argtypes = ([ctypes.c_int32] * 5 + [ctypes.c_void_p] * 9 +
                                  [ctypes.c_size_t, ctypes.c_void_p])
+    L.moe_lora_align_pair_rows.restype = ctypes.c_int
+    L.moe_lora_align_pair_rows.argtypes = ([ctypes.c_int32] * 5 + [ctypes.c_void_p] * 10 +
+                                           [ctypes.c_size_t, ctypes.c_void_p])
+    L.moe_lora_permute.restype = ctypes.c_int
+    L.moe_lora_permute.argtypes = [ctypes.c_int32] * 4 + [ctypes.c_int64] + [ctypes.c_void_p] * 6
+    L.moe_lora_permute_backward.restype = ctypes.c_int
+    L.moe_lora_permute_backward.argtypes = ([ctypes.c_int32] * 5 + [ctypes.c_int64] +
+                                            [ctypes.c_void_p] * 4)
+    L.moe_lora_unpermute.restype = ctypes.c_int
+    L.moe_lora_unpermute.argtypes = [ctypes.c_int32] * 5 + [ctypes.c_int64] + [ctypes.c_void_p] * 5
+    L.moe_lora_unpermute_backward.restype = ctypes.c_int
+    L.moe_lora_unpermute_backward.argtypes = ([ctypes.c_int32] * 5 + [ctypes.c_int64] +
+                                              [ctypes.c_void_p] * 9)
+    L.moe_lora_mx4_quantize.restype = ctypes.c_int
+    L.moe_lora_mx4_quantize.argtypes = ([ctypes.c_int64] + [ctypes.c_int32] * 2 +
+                                        [ctypes.c_void_p] * 5)
+    L.moe_lora_mx4_dequantize.restype = ctypes.c_int
+    L.moe_lora_mx4_dequantize.argtypes = ([ctypes.c_int64] + [ctypes.c_int32] * 2 +
+                                          [ctypes.c_void_p] * 4)
+    L.moe_lora_mx4_gemm.restype = ctypes.c_int
+    L.moe_lora_mx4_gemm.argtypes = [ctypes.POINTER(Mx4GemmArgs), ctypes.c_void_p]
     L.moe_lora_forward_workspace_bytes.restype = ctypes.c_size_t
     L.moe_lora_forward_workspace_bytes.argtypes = [ctypes.POINTER(ForwardArgs)]
     L.moe_lora_forward.restype = ctypes.c_int
@@ -236,8 +257,12 @@ def moe_lora_align_workspace_bytes(num_tokens, top_k, num_experts, num_loras, bl
 def moe_lora_align(topk_ids: torch.Tensor, token_lora_mapping: torch.Tensor,
                    adapter_enabled: Optional[torch.Tensor], num_experts: int, num_loras: int,
                    block_m: int = 16, out: Optional[Dict[str, torch.Tensor]] = None,
-                   workspace: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
-    """Bucket (token, expert) pairs by (expert, adapter); returns the align outputs."""
+                   workspace: Optional[torch.Tensor] = None,
+                   pair_rows: bool = False) -> Dict[str, torch.Tensor]:
+    """Bucket (token, expert) pairs by (expert, adapter); returns the align outputs.
+
+    ``pair_rows``: also write ``pair_rows`` (int32 [T * k], the row of each pair or
+    -1), which moe_lora_permute and moe_lora_unpermute need."""
     dev = topk_ids.device
     T, k = topk_ids.shape
     _need(topk_ids, "topk_ids", torch.int32)
@@ -252,6 +277,10 @@ def moe_lora_align(topk_ids: torch.Tensor, token_lora_mapping: torch.Tensor,
             tile_lora=torch.empty(max(cap // block_m, 1), dtype=torch.int32, device=dev),
             expert_tile_offsets=torch.empty(num_experts + 1, dtype=torch.int32, device=dev),
             num_rows_padded=torch.empty(1, dtype=torch.int32, device=dev))
+    if pair_rows:
+        if "pair_rows" not in out:
+            out["pair_rows"] = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)
+        _need(out["pair_rows"], "pair_rows", torch.int32, dev, T * k)
     for name, n in (("sorted_pair_ids", cap), ("tile_expert", cap // block_m),
                     ("tile_lora", cap // block_m), ("expert_tile_offsets", num_experts + 1),
                     ("num_rows_padded", 1)):
@@ -260,13 +289,15 @@ def moe_lora_align(topk_ids: torch.Tensor, token_lora_mapping: torch.Tensor,
     if workspace is None:
         workspace = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", torch.uint8, dev, wsb)
-    st = lib().moe_lora_align(T, k, num_experts, num_loras, block_m, _ptr(topk_ids),
-                              _ptr(token_lora_mapping),
-                              _ptr(adapter_enabled) if num_loras > 0 else None,
-                              _ptr(out["sorted_pair_ids"]), _ptr(out["tile_expert"]),
-                              _ptr(out["tile_lora"]), _ptr(out["expert_tile_offsets"]),
-                              _ptr(out["num_rows_padded"]), _ptr(workspace), workspace.numel(),
-                              _stream())
+    args = [T, k, num_experts, num_loras, block_m, _ptr(topk_ids), _ptr(token_lora_mapping),
+            _ptr(adapter_enabled) if num_loras > 0 else None, _ptr(out["sorted_pair_ids"]),
+            _ptr(out["tile_expert"]), _ptr(out["tile_lora"]), _ptr(out["expert_tile_offsets"]),
+            _ptr(out["num_rows_padded"])]
+    if pair_rows:
+        st = lib().moe_lora_align_pair_rows(*args, _ptr(out["pair_rows"]), _ptr(workspace),
+                                            workspace.numel(), _stream())
+    else:
+        st = lib().moe_lora_align(*args, _ptr(workspace), workspace.numel(), _stream())
     _check(st, "moe_lora_align")
     out["capacity"] = cap
     out["block_m"] = block_m
@@ -582,3 +613,362 @@ def run_dense(inputs: dict, out0: int, block_m: int = 16, with_lora: bool = True
     return moe_lora_dense_forward(inputs["x"], inputs["w"], out0, al, ranks if L > 0 else None,
                                   inputs["scaling"] if L > 0 else None, pools,
                                   out_dtype=out_dtype)
+
+
+# ---------------------------------------------------------------------------
+# rows in expert order
+# ---------------------------------------------------------------------------
+_ROW_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _row_dtype(t, name, also=()):
+    dtype = t if isinstance(t, torch.dtype) else t.dtype
+    if dtype in _ROW_DTYPES:
+        return _ROW_DTYPES[dtype]
+    if dtype in also:
+        return DTYPE_U8
+    raise TypeError(f"unsupported dtype of {name}: {dtype}")
+
+
+def _rows_layout(align_out, top_k, dev, num_rows=None):
+    """(tokens, rows of the layout) after checking its arrays."""
+    if "pair_rows" not in align_out:
+        raise ValueError("the layout has no pair_rows (moe_lora_align(..., pair_rows=True))")
+    pr = align_out["pair_rows"]
+    _need(pr, "pair_rows", torch.int32, dev)
+    cap = int(align_out["capacity"])
+    _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, cap)
+    _need(align_out["num_rows_padded"], "num_rows_padded", torch.int32, dev, 1)
+    if top_k <= 0 or (cap > 0 and pr.numel() % top_k):
+        raise ValueError("pair_rows is not [T, top_k]")
+    if num_rows is not None and num_rows != cap:
+        raise ValueError(f"the layout has {cap} rows, got {num_rows}")
+    return (pr.numel() // top_k if cap > 0 else 0), cap
+
+
+def _apart(out, *inputs):
+    """Outputs must not share memory with inputs."""
+    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for t in inputs:
+        if t is not None and t.numel() and lo < t.data_ptr() + t.numel() * t.element_size() \
+                and t.data_ptr() < hi:
+            raise ValueError("an output overlaps an input")
+
+
+def _matrix(t, name, dev=None):
+    _need(t, name, None, dev)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+
+
+def _on(t: torch.Tensor):
+    """The device of ``t`` as the current one, and that device's current stream."""
+    return torch.cuda.device(t.device)
+
+
+def moe_lora_permute(x: torch.Tensor, align_out: Dict[str, torch.Tensor], top_k: int,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows of x [T, H] copied to expert order: rows [capacity, H] of x's dtype
+    (float32, bfloat16, or uint8 for MX4 codes and scales).
+
+    Padding rows before ``num_rows_padded`` are zero; rows behind it are left as
+    they are in ``out`` (undefined when it is not given).  ``align_out`` comes from
+    moe_lora_align with ``pair_rows=True``."""
+    _matrix(x, "x")
+    dt = _row_dtype(x, "x", (torch.uint8,))
+    T, cap = _rows_layout(align_out, top_k, x.device)
+    if x.shape[0] != T:
+        raise ValueError(f"x has {x.shape[0]} rows, the layout {T} tokens")
+    H = x.shape[1]
+    if out is None:
+        out = torch.empty((cap, H), dtype=x.dtype, device=x.device)
+    _need(out, "out", x.dtype, x.device)
+    if tuple(out.shape) != (cap, H):
+        raise ValueError(f"out must be {(cap, H)}, got {tuple(out.shape)}")
+    _apart(out, x)
+    with _on(x):
+        _check(lib().moe_lora_permute(T, top_k, H, dt, cap, _ptr(x),
+                                      _ptr(align_out["sorted_pair_ids"]),
+                                      _ptr(align_out["pair_rows"]),
+                                      _ptr(align_out["num_rows_padded"]), _ptr(out), _stream()),
+               "moe_lora_permute")
+    return out
+
+
+def moe_lora_permute_backward(d_rows: torch.Tensor, align_out: Dict[str, torch.Tensor], top_k: int,
+                              dx: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
+    """Gradient of moe_lora_permute: dx [T, H], the sum of each token's rows of
+    ``d_rows`` (fp32 sums; ``out_dtype`` defaults to the rows' dtype)."""
+    _matrix(d_rows, "d_rows")
+    T, cap = _rows_layout(align_out, top_k, d_rows.device, d_rows.shape[0])
+    H = d_rows.shape[1]
+    if dx is None:
+        dx = torch.empty((T, H), dtype=out_dtype or d_rows.dtype, device=d_rows.device)
+    _token_out(dx, "dx", T, H, d_rows, out_dtype)
+    with _on(d_rows):
+        _check(lib().moe_lora_permute_backward(T, top_k, H, _row_dtype(d_rows, "d_rows"),
+                                               _row_dtype(dx, "dx"), cap, _ptr(d_rows),
+                                               _ptr(align_out["pair_rows"]), _ptr(dx), _stream()),
+               "moe_lora_permute_backward")
+    return dx
+
+
+def _token_out(t, name, T, H, rows, out_dtype):
+    _need(t, name, out_dtype, rows.device)
+    if tuple(t.shape) != (T, H):
+        raise ValueError(f"{name} must be {(T, H)}, got {tuple(t.shape)}")
+    _apart(t, rows)
+
+
+def _pair_weights(w, T, top_k, dev, name="topk_weights"):
+    _need(w, name, torch.float32, dev)
+    if w.numel() != T * top_k:
+        raise ValueError(f"{name} must be [{T}, {top_k}], got {tuple(w.shape)}")
+
+
+def moe_lora_unpermute(rows: torch.Tensor, align_out: Dict[str, torch.Tensor], top_k: int,
+                       topk_weights: Optional[torch.Tensor] = None,
+                       y: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
+    """y [T, H] = the sum over a token's top_k pairs of weight times row (fp32,
+    in pair order, rounded once; no weights: ones).  Pairs without a row take no
+    part.  ``out_dtype`` defaults to the rows' dtype."""
+    _matrix(rows, "rows")
+    T, cap = _rows_layout(align_out, top_k, rows.device, rows.shape[0])
+    H = rows.shape[1]
+    if topk_weights is not None:
+        _pair_weights(topk_weights, T, top_k, rows.device)
+    if y is None:
+        y = torch.empty((T, H), dtype=out_dtype or rows.dtype, device=rows.device)
+    _token_out(y, "y", T, H, rows, out_dtype)
+    with _on(rows):
+        _check(lib().moe_lora_unpermute(T, top_k, H, _row_dtype(rows, "rows"), _row_dtype(y, "y"),
+                                        cap, _ptr(rows), _ptr(align_out["pair_rows"]),
+                                        _ptr(topk_weights), _ptr(y), _stream()),
+               "moe_lora_unpermute")
+    return y
+
+
+def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
+                                align_out: Dict[str, torch.Tensor], top_k: int,
+                                topk_weights: Optional[torch.Tensor] = None,
+                                d_rows: Optional[torch.Tensor] = None,
+                                d_weights: Optional[torch.Tensor] = None,
+                                rows_dtype=None):
+    """Gradients of moe_lora_unpermute: (d_rows [capacity, H], d_weights [T, top_k]).
+
+    ``rows`` are the forward's rows, needed for d_weights; with ``rows=None`` (or
+    without weights) d_weights is None, and d_rows takes ``rows_dtype`` (default
+    dy's).  Padding rows of d_rows are zero, rows behind ``num_rows_padded`` are
+    left as they are."""
+    _matrix(dy, "dy")
+    dev = dy.device
+    T, cap = _rows_layout(align_out, top_k, dev)
+    H = dy.shape[1]
+    if dy.shape[0] != T:
+        raise ValueError(f"dy has {dy.shape[0]} rows, the layout {T} tokens")
+    if rows is not None:
+        _need(rows, "rows", rows_dtype, dev)
+        if tuple(rows.shape) != (cap, H):
+            raise ValueError(f"rows must be {(cap, H)}, got {tuple(rows.shape)}")
+    if topk_weights is not None:
+        _pair_weights(topk_weights, T, top_k, dev)
+    dt = rows.dtype if rows is not None else rows_dtype or dy.dtype
+    if d_rows is None:
+        d_rows = torch.empty((cap, H), dtype=dt, device=dev)
+    _need(d_rows, "d_rows", dt, dev)
+    if tuple(d_rows.shape) != (cap, H):
+        raise ValueError(f"d_rows must be {(cap, H)}, got {tuple(d_rows.shape)}")
+    _apart(d_rows, dy, rows, topk_weights)
+    if rows is None or topk_weights is None:
+        if d_weights is not None:
+            raise ValueError("d_weights needs rows and topk_weights")
+    elif d_weights is None:
+        d_weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    if d_weights is not None:
+        _pair_weights(d_weights, T, top_k, dev, "d_weights")
+        _apart(d_weights, dy, rows, topk_weights, d_rows)
+    with _on(dy):
+        _check(lib().moe_lora_unpermute_backward(
+            T, top_k, H, _row_dtype(dt, "rows"), _row_dtype(dy, "dy"), cap, _ptr(dy), _ptr(rows),
+            _ptr(align_out["sorted_pair_ids"]), _ptr(align_out["pair_rows"]),
+            _ptr(align_out["num_rows_padded"]), _ptr(topk_weights), _ptr(d_rows), _ptr(d_weights),
+            _stream()), "moe_lora_unpermute_backward")
+    return d_rows, d_weights
+
+
+# ---------------------------------------------------------------------------
+# MX4: 4-bit values in blocks of 32 under a power-of-two scale
+# ---------------------------------------------------------------------------
+class Mx4GemmArgs(ctypes.Structure):
+    """Mirror of ``moe_lora_mx4_gemm_args``."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("x_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+        ("num_rows", ctypes.c_int64),
+        ("out_features", ctypes.c_int32), ("in_features", ctypes.c_int32),
+        ("num_experts", ctypes.c_int32), ("block_m", ctypes.c_int32),
+        ("silu_mul", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p),
+        ("w", ctypes.c_void_p), ("w_scale", ctypes.c_void_p),
+        ("tile_expert", ctypes.c_void_p), ("out", ctypes.c_void_p),
+    ]
+
+
+def _mx4_pair(codes, scales, name, dev=None):
+    """Checks codes [.., K / 2] and scales [.., K / 32]; returns K."""
+    _need(codes, f"{name} codes", torch.uint8, dev)
+    _need(scales, f"{name} scales", torch.uint8, codes.device)
+    if codes.dim() < 1 or codes.shape[-1] % 16 or \
+            tuple(scales.shape) != (*codes.shape[:-1], codes.shape[-1] // 16):
+        raise ValueError(f"{name} must be codes [.., K/2] and scales [.., K/32], got "
+                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+    return 2 * codes.shape[-1]
+
+
+def moe_lora_mx4_quantize(x: torch.Tensor, num_rows_used: Optional[torch.Tensor] = None,
+                          codes: Optional[torch.Tensor] = None,
+                          scales: Optional[torch.Tensor] = None):
+    """(codes uint8 [.., K/2], scales uint8 [.., K/32]) of x [.., K], K a multiple of
+    32, float32 or bfloat16.
+
+    ``num_rows_used``: device int32 [1]; rows of x (all leading axes together) from
+    it on are skipped, their outputs left as they are (``num_rows_padded`` of
+    moe_lora_align)."""
+    _need(x, "x")
+    dt = _row_dtype(x, "x")
+    K = x.shape[-1] if x.dim() else 0
+    if K <= 0 or K % 32:
+        raise ValueError("the last axis of x must be a multiple of 32")
+    lead, dev = tuple(x.shape[:-1]), x.device
+    if codes is None:
+        codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=dev)
+    _mx4_pair(codes, scales, "the output", dev)
+    if tuple(codes.shape) != (*lead, K // 2):
+        raise ValueError(f"codes must be {(*lead, K // 2)}, got {tuple(codes.shape)}")
+    if num_rows_used is not None:
+        _need(num_rows_used, "num_rows_used", torch.int32, dev, 1)
+    _apart(codes, x, scales)
+    _apart(scales, x)
+    with _on(x):
+        _check(lib().moe_lora_mx4_quantize(x.numel() // K, K, dt, _ptr(x), _ptr(num_rows_used),
+                                           _ptr(codes), _ptr(scales), _stream()),
+               "moe_lora_mx4_quantize")
+    return codes, scales
+
+
+def moe_lora_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor,
+                            out: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
+    """The values [.., K] that MX4 codes and scales stand for (bfloat16 unless
+    ``out_dtype`` or ``out`` says float32)."""
+    K = _mx4_pair(codes, scales, "x")
+    shape = (*codes.shape[:-1], K)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=codes.device)
+    _need(out, "out", out_dtype, codes.device)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
+    _apart(out, codes, scales)
+    if K == 0:
+        return out
+    with _on(codes):
+        _check(lib().moe_lora_mx4_dequantize(out.numel() // K, K, _row_dtype(out, "out"),
+                                             _ptr(codes), _ptr(scales), _ptr(out), _stream()),
+               "moe_lora_mx4_dequantize")
+    return out
+
+
+def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                      x_scales: Optional[torch.Tensor] = None,
+                      align_out: Optional[Dict[str, torch.Tensor]] = None, silu_mul: bool = False,
+                      out: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
+    """x W^T with MX4 weights; ``silu_mul``: SiLU(gate) * up of the two halves of the
+    output columns.
+
+    ``align_out`` None: w_codes [N, K/2], w_scales [N, K/32], x [M, K] of any M.
+    Otherwise w_codes [E, N, K/2], w_scales [E, N, K/32] and x [capacity, K] in
+    expert order (moe_lora_permute); rows behind the last used tile are left as they
+    are in ``out`` (undefined when it is not given).
+    x: bfloat16, or MX4 codes [M, K/2] with ``x_scales`` [M, K/32].  ``out`` /
+    ``out_dtype``: bfloat16 (the default) or float32."""
+    K = _mx4_pair(w_codes, w_scales, "w")
+    dev = w_codes.device
+    if w_codes.dim() != (2 if align_out is None else 3):
+        raise ValueError("w_codes must be [N, K/2], or [E, N, K/2] with align_out")
+    E, N = (1 if align_out is None else w_codes.shape[0]), w_codes.shape[-2]
+    if x_scales is None:
+        _need(x, "x", torch.bfloat16, dev)
+        xk = x.shape[-1] if x.dim() == 2 else -1
+    else:
+        xk = _mx4_pair(x, x_scales, "x", dev) if x.dim() == 2 else -1
+    if x.dim() != 2 or xk != K:
+        raise ValueError(f"x {tuple(x.shape)} does not match weights of {K} columns")
+    M, a = x.shape[0], Mx4GemmArgs()
+    if align_out is not None:
+        a.block_m = int(align_out["block_m"])
+        if a.block_m <= 0 or M % a.block_m:
+            raise ValueError("x must hold whole tiles of block_m rows")
+        _need(align_out["tile_expert"], "tile_expert", torch.int32, dev, M // a.block_m)
+        a.tile_expert = align_out["tile_expert"].data_ptr()
+        if M == 0:
+            a.tile_expert = None
+    cols = N // 2 if silu_mul else N
+    if out is None:
+        out = torch.empty((M, cols), dtype=out_dtype or torch.bfloat16, device=dev)
+    _need(out, "out", out_dtype, dev)
+    if tuple(out.shape) != (M, cols):
+        raise ValueError(f"out must be {(M, cols)}, got {tuple(out.shape)}")
+    _apart(out, x, x_scales, w_codes, w_scales)
+    if M == 0:
+        return out
+    a.struct_size = ctypes.sizeof(Mx4GemmArgs)
+    a.x_dtype = DTYPE_BF16 if x_scales is None else DTYPE_MX4
+    a.out_dtype = _row_dtype(out, "out")
+    a.num_rows, a.out_features, a.in_features, a.num_experts = M, N, K, E
+    a.silu_mul = int(bool(silu_mul))
+    a.x, a.w, a.w_scale, a.out = (x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+                                  out.data_ptr())
+    a.x_scale = None if x_scales is None else x_scales.data_ptr()
+    with _on(x):
+        _check(lib().moe_lora_mx4_gemm(ctypes.byref(a), _stream()), "moe_lora_mx4_gemm")
+    return out
+
+
+def mx4_block_m(num_tokens: int, top_k: int, num_experts: int) -> int:
+    """The block_m of moe_lora_align that suits moe_lora_mx4_gemm: about the rows an
+    expert gets, so that its weights are read once without many padding rows."""
+    per = num_tokens * top_k / num_experts
+    return 16 if per <= 24 else 32 if per <= 48 else 64 if per <= 128 else 128 if per <= 512 else 256
+
+
+def run_mx4_layer(inputs: dict, activations: str = "bf16", block_m: Optional[int] = None,
+                  out_dtype=None) -> torch.Tensor:
+    """The MoE layer without adapters on MX4 expert weights: align -> permute ->
+    gate_up product with SiLU * up -> down product -> unpermute.
+
+    ``inputs``: x [T, H] bfloat16, topk_ids, topk_weights, and the weights
+    w_gate_up_mx4, w_down_mx4, each a (codes, scales) pair of moe_lora_mx4_quantize.
+    ``activations``: "bf16", or "mx4" to quantise x and the activations between the
+    products as well."""
+    if activations not in ("bf16", "mx4"):
+        raise ValueError("activations must be 'bf16' or 'mx4'")
+    x, ids, w = inputs["x"], inputs["topk_ids"], inputs["topk_weights"]
+    T, k = ids.shape
+    gu, down = inputs["w_gate_up_mx4"], inputs["w_down_mx4"]
+    E = gu[0].shape[0]
+    if block_m is None:
+        block_m = mx4_block_m(T, k, E)
+    slots = torch.full((max(T, 1),), -1, dtype=torch.int32, device=x.device)
+    al = moe_lora_align(ids, slots, None, E, 0, block_m, pair_rows=True)
+    if activations == "mx4":
+        codes, scales = moe_lora_mx4_quantize(x)
+        act = moe_lora_mx4_gemm(moe_lora_permute(codes, al, k), *gu,
+                                x_scales=moe_lora_permute(scales, al, k), align_out=al,
+                                silu_mul=True)
+        codes, scales = moe_lora_mx4_quantize(act, al["num_rows_padded"])
+        z = moe_lora_mx4_gemm(codes, *down, x_scales=scales, align_out=al, out_dtype=torch.float32)
+    else:
+        act = moe_lora_mx4_gemm(moe_lora_permute(x, al, k), *gu, align_out=al, silu_mul=True)
+        z = moe_lora_mx4_gemm(act, *down, align_out=al, out_dtype=torch.float32)
+    return moe_lora_unpermute(z, al, k, w, out_dtype=out_dtype or x.dtype)

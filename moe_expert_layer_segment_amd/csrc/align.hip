@@ -11,7 +11,8 @@
 //                 to block_m; exclusive scan over keys; tile counts per expert.
 //   3. scatter -- one thread per output row and per pair: pairs go to
 //                 bucket offset + chunk prefix + rank; pads, tile tables and the
-//                 unused tail are filled by binary search over bucket starts.
+//                 unused tail are filled by binary search over bucket starts.  The
+//                 row of each pair is written too when the caller asks for it.
 // Every output word up to the capacity is written.
 #include "moe_lora.h"
 #include "common.hpp"
@@ -239,15 +240,21 @@ align_scatter_kernel(int P, int k, int E, int L, int K, int BM, int64_t cap, int
                      const int32_t* __restrict__ enabled, const int32_t* __restrict__ ws_rank,
                      const int32_t* __restrict__ ws_off, const int32_t* __restrict__ ws_bstart,
                      const int32_t* __restrict__ ws_btotal, int32_t* __restrict__ sorted_ids,
-                     int32_t* __restrict__ tile_expert, int32_t* __restrict__ tile_lora) {
+                     int32_t* __restrict__ tile_expert, int32_t* __restrict__ tile_lora,
+                     int32_t* __restrict__ pair_rows) {
   const int64_t i = (int64_t)blockIdx.x * kScatterThreads + threadIdx.x;
   if (i < P) {
     int key = pair_key((int)i, k, E, L, topk_ids, mapping, enabled);
+    int row = -1;
     if (key >= 0) {
       // the key's first row + the key's pairs in earlier chunks + the rank in this chunk
       int64_t pos = (int64_t)ws_bstart[key] + ws_off[(i / chunk_pairs) * K + key] + ws_rank[i];
-      if (pos >= 0 && pos < cap) sorted_ids[pos] = (int32_t)i;
+      if (pos >= 0 && pos < cap) {
+        sorted_ids[pos] = (int32_t)i;
+        row = (int)pos;
+      }
     }
+    if (pair_rows) pair_rows[i] = row;
   }
   if (i < cap) {
     const int rows = ws_bstart[K];
@@ -275,8 +282,8 @@ align_scatter_kernel(int P, int k, int E, int L, int K, int BM, int64_t cap, int
 hipError_t launch_align(int32_t T, int32_t k, int32_t E, int32_t L, int32_t BM,
                         const int32_t* topk_ids, const int32_t* mapping, const int32_t* enabled,
                         int32_t* sorted_ids, int32_t* tile_expert, int32_t* tile_lora,
-                        int32_t* expert_tile_offsets, int32_t* num_rows_padded, void* workspace,
-                        uint32_t* debug_word, hipStream_t stream) {
+                        int32_t* expert_tile_offsets, int32_t* num_rows_padded, int32_t* pair_rows,
+                        void* workspace, uint32_t* debug_word, hipStream_t stream) {
   const int64_t P = (int64_t)T * k;
   const int64_t K = (int64_t)E * (L + 1);
   const AlignWs w = align_ws_layout(P, K);
@@ -302,7 +309,7 @@ hipError_t launch_align(int32_t T, int32_t k, int32_t E, int32_t L, int32_t BM,
     hipLaunchKernelGGL(align_scatter_kernel, dim3((unsigned)ceil_div(n, kScatterThreads)),
                        dim3(kScatterThreads), 0, stream, (int)P, k, E, L, (int)K, BM, cap,
                        align_chunk_pairs(P, K), topk_ids, mapping, enabled, ws_rank, ws_cnt,
-                       ws_bstart, ws_btotal, sorted_ids, tile_expert, tile_lora);
+                       ws_bstart, ws_btotal, sorted_ids, tile_expert, tile_lora, pair_rows);
   }
   return hipGetLastError();
 }

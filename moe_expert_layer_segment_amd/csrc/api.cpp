@@ -81,11 +81,12 @@ size_t moe_lora_align_workspace_bytes(int32_t num_tokens, int32_t top_k, int32_t
   return align_ws_layout((int64_t)num_tokens * top_k, (int64_t)num_experts * ((int64_t)num_loras + 1)).bytes;
 }
 
-int moe_lora_align(int32_t num_tokens, int32_t top_k, int32_t num_experts, int32_t num_loras,
-                   int32_t block_m, const int32_t* topk_ids, const int32_t* token_lora_mapping,
-                   const int32_t* adapter_enabled, int32_t* sorted_pair_ids, int32_t* tile_expert,
-                   int32_t* tile_lora, int32_t* expert_tile_offsets, int32_t* num_rows_padded,
-                   void* workspace, size_t workspace_bytes, void* stream) {
+static int align_impl(int32_t num_tokens, int32_t top_k, int32_t num_experts, int32_t num_loras,
+                      int32_t block_m, const int32_t* topk_ids, const int32_t* token_lora_mapping,
+                      const int32_t* adapter_enabled, int32_t* sorted_pair_ids,
+                      int32_t* tile_expert, int32_t* tile_lora, int32_t* expert_tile_offsets,
+                      int32_t* num_rows_padded, int32_t* pair_rows, void* workspace,
+                      size_t workspace_bytes, void* stream) {
   if (num_tokens < 0 || top_k <= 0 || num_experts <= 0 || num_loras < 0 || bad_block_m(block_m))
     return MOE_LORA_ERR_INVALID;
   if (top_k > num_experts) return MOE_LORA_ERR_INVALID;
@@ -100,8 +101,33 @@ int moe_lora_align(int32_t num_tokens, int32_t top_k, int32_t num_experts, int32
   if (!workspace || workspace_bytes < need) return MOE_LORA_ERR_WORKSPACE;
   return hip_status(launch_align(num_tokens, top_k, num_experts, num_loras, block_m, topk_ids,
                                  token_lora_mapping, adapter_enabled, sorted_pair_ids, tile_expert,
-                                 tile_lora, expert_tile_offsets, num_rows_padded, workspace,
-                                 debug_word(), static_cast<hipStream_t>(stream)));
+                                 tile_lora, expert_tile_offsets, num_rows_padded, pair_rows,
+                                 workspace, debug_word(), static_cast<hipStream_t>(stream)));
+}
+
+int moe_lora_align(int32_t num_tokens, int32_t top_k, int32_t num_experts, int32_t num_loras,
+                   int32_t block_m, const int32_t* topk_ids, const int32_t* token_lora_mapping,
+                   const int32_t* adapter_enabled, int32_t* sorted_pair_ids, int32_t* tile_expert,
+                   int32_t* tile_lora, int32_t* expert_tile_offsets, int32_t* num_rows_padded,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  return align_impl(num_tokens, top_k, num_experts, num_loras, block_m, topk_ids,
+                    token_lora_mapping, adapter_enabled, sorted_pair_ids, tile_expert, tile_lora,
+                    expert_tile_offsets, num_rows_padded, nullptr, workspace, workspace_bytes,
+                    stream);
+}
+
+int moe_lora_align_pair_rows(int32_t num_tokens, int32_t top_k, int32_t num_experts,
+                             int32_t num_loras, int32_t block_m, const int32_t* topk_ids,
+                             const int32_t* token_lora_mapping, const int32_t* adapter_enabled,
+                             int32_t* sorted_pair_ids, int32_t* tile_expert, int32_t* tile_lora,
+                             int32_t* expert_tile_offsets, int32_t* num_rows_padded,
+                             int32_t* pair_rows, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (num_tokens > 0 && !pair_rows) return MOE_LORA_ERR_INVALID;
+  return align_impl(num_tokens, top_k, num_experts, num_loras, block_m, topk_ids,
+                    token_lora_mapping, adapter_enabled, sorted_pair_ids, tile_expert, tile_lora,
+                    expert_tile_offsets, num_rows_padded, pair_rows, workspace, workspace_bytes,
+                    stream);
 }
 
 int moe_lora_debug_flags(uint32_t* flags, int32_t clear, void* stream) {
@@ -297,6 +323,157 @@ int moe_lora_dense_forward_events(const moe_lora_dense_args* args, void* stream,
                                   void* const* events) {
   if (!events) return MOE_LORA_ERR_INVALID;
   return dense_impl(args, stream, events);
+}
+
+// ---- rows in expert order --------------------------------------------------
+
+
+constexpr int64_t kMaxRows = INT32_MAX;   // rows are named by int32
+constexpr int64_t kMaxCols = int64_t(1) << 24;
+
+static int to_layout(int32_t num_tokens, int32_t top_k, int32_t hidden, int64_t num_rows,
+                     const int32_t* sorted_pair_ids, const int32_t* pair_rows,
+                     const int32_t* num_rows_padded, bool spread, RowsLayout* l) {
+  if (num_tokens < 0 || top_k <= 0 || hidden <= 0 || num_rows < 0) return MOE_LORA_ERR_INVALID;
+  if ((int64_t)num_tokens * top_k > INT32_MAX / 2 || num_tokens > kMaxRows || num_rows > kMaxRows ||
+      hidden > kMaxCols)
+    return MOE_LORA_ERR_UNSUPPORTED;
+  if (num_tokens > 0 && !pair_rows) return MOE_LORA_ERR_INVALID;
+  if (spread && num_rows > 0 && (!sorted_pair_ids || !num_rows_padded)) return MOE_LORA_ERR_INVALID;
+  l->T = num_tokens; l->k = top_k; l->num_rows = num_rows;
+  l->sorted_ids = sorted_pair_ids; l->pair_rows = pair_rows; l->num_rows_padded = num_rows_padded;
+  return MOE_LORA_OK;
+}
+
+static bool off_by_element(const void* ptr, int32_t dtype) {
+  return reinterpret_cast<uintptr_t>(ptr) % (dtype == MOE_LORA_F32 ? 4 : 2) != 0;
+}
+
+static bool float_dtype(int32_t d) { return d == MOE_LORA_F32 || d == MOE_LORA_BF16; }
+
+int moe_lora_permute(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t dtype,
+                     int64_t num_rows, const void* x, const int32_t* sorted_pair_ids,
+                     const int32_t* pair_rows, const int32_t* num_rows_padded, void* rows,
+                     void* stream) {
+  RowsLayout l;
+  const int st = to_layout(num_tokens, top_k, hidden, num_rows, sorted_pair_ids, pair_rows,
+                           num_rows_padded, true, &l);
+  if (st != MOE_LORA_OK) return st;
+  if (!float_dtype(dtype) && dtype != MOE_LORA_U8) return MOE_LORA_ERR_UNSUPPORTED;
+  if (num_rows == 0) return MOE_LORA_OK;
+  if (!rows || (num_tokens > 0 && !x)) return MOE_LORA_ERR_INVALID;
+  if (dtype != MOE_LORA_U8 && (off_by_element(x, dtype) || off_by_element(rows, dtype)))
+    return MOE_LORA_ERR_INVALID;
+  const int64_t esz = dtype == MOE_LORA_F32 ? 4 : dtype == MOE_LORA_BF16 ? 2 : 1;
+  return hip_status(launch_permute(l, hidden * esz, x, rows, static_cast<hipStream_t>(stream)));
+}
+
+int moe_lora_unpermute(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t dtype,
+                       int32_t out_dtype, int64_t num_rows, const void* rows,
+                       const int32_t* pair_rows, const float* topk_weights, void* y,
+                       void* stream) {
+  RowsLayout l;
+  const int st = to_layout(num_tokens, top_k, hidden, num_rows, nullptr, pair_rows, nullptr, false, &l);
+  if (st != MOE_LORA_OK) return st;
+  if (!float_dtype(dtype) || !float_dtype(out_dtype)) return MOE_LORA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return MOE_LORA_OK;
+  if (!y || (num_rows > 0 && !rows) || off_by_element(y, out_dtype) || off_by_element(rows, dtype))
+    return MOE_LORA_ERR_INVALID;
+  return hip_status(launch_unpermute(l, hidden, dtype == MOE_LORA_F32, out_dtype == MOE_LORA_F32,
+                                     rows, topk_weights, y, static_cast<hipStream_t>(stream)));
+}
+
+int moe_lora_permute_backward(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t dtype,
+                              int32_t out_dtype, int64_t num_rows, const void* d_rows,
+                              const int32_t* pair_rows, void* dx, void* stream) {
+  return moe_lora_unpermute(num_tokens, top_k, hidden, dtype, out_dtype, num_rows, d_rows,
+                            pair_rows, nullptr, dx, stream);
+}
+
+int moe_lora_unpermute_backward(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t dtype,
+                                int32_t dy_dtype, int64_t num_rows, const void* dy,
+                                const void* rows, const int32_t* sorted_pair_ids,
+                                const int32_t* pair_rows, const int32_t* num_rows_padded,
+                                const float* topk_weights, void* d_rows, float* d_weights,
+                                void* stream) {
+  RowsLayout l;
+  const int st = to_layout(num_tokens, top_k, hidden, num_rows, sorted_pair_ids, pair_rows,
+                           num_rows_padded, true, &l);
+  if (st != MOE_LORA_OK) return st;
+  if (!float_dtype(dtype) || !float_dtype(dy_dtype)) return MOE_LORA_ERR_UNSUPPORTED;
+  if (num_rows == 0 && (num_tokens == 0 || !d_weights)) return MOE_LORA_OK;
+  if ((num_rows > 0 && !d_rows) || (num_tokens > 0 && !dy) ||
+      (d_weights && num_tokens > 0 && num_rows > 0 && !rows))
+    return MOE_LORA_ERR_INVALID;
+  if (d_weights && !topk_weights) return MOE_LORA_ERR_INVALID;   // no weights, no gradient
+  if (off_by_element(dy, dy_dtype) || off_by_element(rows, dtype) || off_by_element(d_rows, dtype))
+    return MOE_LORA_ERR_INVALID;
+  return hip_status(launch_unpermute_backward(l, hidden, dtype == MOE_LORA_F32,
+                                              dy_dtype == MOE_LORA_F32, dy, rows, topk_weights,
+                                              d_rows, d_weights,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+// ---- MX4 -------------------------------------------------------------------
+
+static int mx4_shape(int64_t num_rows, int32_t cols, int32_t dtype) {
+  if (num_rows < 0 || cols <= 0) return MOE_LORA_ERR_INVALID;
+  if (!float_dtype(dtype) || cols % 32 || cols > kMaxCols || num_rows > (int64_t(1) << 40) / cols)
+    return MOE_LORA_ERR_UNSUPPORTED;
+  return MOE_LORA_OK;
+}
+
+int moe_lora_mx4_quantize(int64_t num_rows, int32_t cols, int32_t dtype, const void* x,
+                          const int32_t* num_rows_used, uint8_t* codes, uint8_t* scales,
+                          void* stream) {
+  const int st = mx4_shape(num_rows, cols, dtype);
+  if (st != MOE_LORA_OK) return st;
+  if (num_rows == 0) return MOE_LORA_OK;
+  if (!x || !codes || !scales || misaligned(x) || misaligned(codes)) return MOE_LORA_ERR_INVALID;
+  return hip_status(launch_mx4_quantize(dtype == MOE_LORA_F32, num_rows, cols, x, num_rows_used,
+                                        codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+int moe_lora_mx4_dequantize(int64_t num_rows, int32_t cols, int32_t dtype, const uint8_t* codes,
+                            const uint8_t* scales, void* out, void* stream) {
+  const int st = mx4_shape(num_rows, cols, dtype);
+  if (st != MOE_LORA_OK) return st;
+  if (num_rows == 0) return MOE_LORA_OK;
+  if (!out || !codes || !scales || misaligned(out) || misaligned(codes)) return MOE_LORA_ERR_INVALID;
+  return hip_status(launch_mx4_dequantize(dtype == MOE_LORA_F32, num_rows, cols, codes, scales,
+                                          out, static_cast<hipStream_t>(stream)));
+}
+
+int moe_lora_mx4_gemm(const moe_lora_mx4_gemm_args* a, void* stream) {
+  if (!a || a->struct_size < sizeof(moe_lora_mx4_gemm_args)) return MOE_LORA_ERR_INVALID;
+  if ((a->x_dtype != MOE_LORA_BF16 && a->x_dtype != MOE_LORA_MX4) || !float_dtype(a->out_dtype))
+    return MOE_LORA_ERR_UNSUPPORTED;
+  if (a->num_rows < 0 || a->out_features <= 0 || a->in_features <= 0 || a->num_experts <= 0)
+    return MOE_LORA_ERR_INVALID;
+  if (a->in_features % 32 || a->out_features % (a->silu_mul ? 32 : 16) ||
+      a->in_features > kMaxCols || a->out_features > kMaxCols || a->num_rows > kMaxRows)
+    return MOE_LORA_ERR_UNSUPPORTED;
+  if (a->tile_expert) {
+    if (bad_block_m(a->block_m) || a->num_rows % a->block_m) return MOE_LORA_ERR_INVALID;
+  } else if (a->num_experts != 1) {
+    return MOE_LORA_ERR_INVALID;   // rows of several experts need their tiles
+  }
+  // threads of one launch are counted in 32 bits: 256 to 16 rows x 64 columns at the least
+  if ((a->num_rows + 15) / 16 * ((a->out_features + 63) / 64) >= (int64_t(1) << 24))
+    return MOE_LORA_ERR_UNSUPPORTED;
+  if (a->num_rows == 0) return MOE_LORA_OK;
+  if (!a->x || !a->w || !a->w_scale || !a->out || (a->x_dtype == MOE_LORA_MX4 && !a->x_scale) ||
+      misaligned(a->x) || misaligned(a->w) || misaligned(a->out))
+    return MOE_LORA_ERR_INVALID;
+  Mx4Gemm p;
+  p.M = a->num_rows; p.N = a->out_features; p.K = a->in_features; p.E = a->num_experts;
+  p.BM = a->tile_expert ? a->block_m : 0;
+  p.x_mx4 = a->x_dtype == MOE_LORA_MX4;
+  p.out_f32 = a->out_dtype == MOE_LORA_F32;
+  p.silu_mul = a->silu_mul != 0;
+  p.x = a->x; p.x_scale = a->x_scale; p.w = a->w; p.w_scale = a->w_scale;
+  p.tile_expert = a->tile_expert; p.out = a->out;
+  return hip_status(launch_mx4_gemm(p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

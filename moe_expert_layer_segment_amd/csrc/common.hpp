@@ -103,6 +103,18 @@ __device__ inline float silu_f(float v) {
   return v * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
+// MX4: the value 2^(b - 127) of an e8m0 scale byte (255: NaN; 0: 2^-127, below
+// the smallest normal float), and the value of the e2m1 code in the low 4 bits.
+__device__ inline float mx4_scale(uint32_t b) {
+  return __builtin_bit_cast(float, b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
+}
+__device__ inline float e2m1_value(uint32_t c) {
+  // twice the magnitudes of codes 0..7, one nibble each
+  const uint32_t twice = (0xC8643210u >> (4 * (c & 7))) & 15u;
+  const float m = 0.5f * (float)twice;
+  return (c & 8) ? -m : m;
+}
+
 __device__ inline int lane_id() { return threadIdx.x & 63; }
 
 // Device-side precondition checks of MOE_LORA_DEBUG builds: a violated

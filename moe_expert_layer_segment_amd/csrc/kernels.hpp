@@ -42,8 +42,48 @@ hipError_t launch_route(int32_t T, int32_t E, int32_t k, const float* logits, in
 hipError_t launch_align(int32_t T, int32_t k, int32_t E, int32_t L, int32_t BM,
                         const int32_t* topk_ids, const int32_t* mapping, const int32_t* enabled,
                         int32_t* sorted_ids, int32_t* tile_expert, int32_t* tile_lora,
-                        int32_t* expert_tile_offsets, int32_t* num_rows_padded, void* workspace,
-                        uint32_t* debug_word, hipStream_t stream);
+                        int32_t* expert_tile_offsets, int32_t* num_rows_padded, int32_t* pair_rows,
+                        void* workspace, uint32_t* debug_word, hipStream_t stream);
+
+// ---- rows in expert order --------------------------------------------------
+// The layout of align seen from both sides: sorted_ids[row] = pair (or >= P for a
+// pad), pair_rows[pair] = row (or -1 for a pair without one).
+struct RowsLayout {
+  int32_t T, k;
+  int64_t num_rows;                  // rows the buffers hold
+  const int32_t *sorted_ids, *pair_rows, *num_rows_padded;
+};
+// rows[pair_rows[t k + j]] = x[t] (row_bytes bytes each); pads are zeroed
+hipError_t launch_permute(const RowsLayout& l, int64_t row_bytes, const void* x, void* rows,
+                          hipStream_t stream);
+// y[t] = sum_j weights[t k + j] rows[pair_rows[t k + j]] (weights null: ones)
+hipError_t launch_unpermute(const RowsLayout& l, int64_t hidden, bool rows_f32, bool y_f32,
+                            const void* rows, const float* weights, void* y, hipStream_t stream);
+// d_rows[pair_rows[t k + j]] = weights[t k + j] dy[t], pads zeroed;
+// d_weights[t k + j] = dy[t] . rows[pair_rows[t k + j]] (null: not computed)
+hipError_t launch_unpermute_backward(const RowsLayout& l, int64_t hidden, bool rows_f32,
+                                     bool dy_f32, const void* dy, const void* rows,
+                                     const float* weights, void* d_rows, float* d_weights,
+                                     hipStream_t stream);
+
+// ---- MX4 -------------------------------------------------------------------
+hipError_t launch_mx4_quantize(bool x_f32, int64_t num_rows, int64_t cols, const void* x,
+                               const int32_t* rows_used, uint8_t* codes, uint8_t* scales,
+                               hipStream_t stream);
+hipError_t launch_mx4_dequantize(bool out_f32, int64_t num_rows, int64_t cols,
+                                 const uint8_t* codes, const uint8_t* scales, void* out,
+                                 hipStream_t stream);
+struct Mx4Gemm {
+  int64_t M, N, K, E, BM;            // BM: rows of a tile_expert entry
+  bool x_mx4, out_f32, silu_mul;
+  const void* x;                     // [M, K] bf16, or MX4 codes [M, K / 2]
+  const uint8_t* x_scale;            // MX4 x: [M, K / 32]
+  const uint8_t* w;                  // [E, N, K / 2]
+  const uint8_t* w_scale;            // [E, N, K / 32]
+  const int32_t* tile_expert;        // [M / BM], null: one weight for all rows
+  void* out;                         // [M, N], or [M, N / 2] with silu_mul
+};
+hipError_t launch_mx4_gemm(const Mx4Gemm& p, hipStream_t stream);
 
 // ---- forward ---------------------------------------------------------------
 // expert weights as fp8 e4m3 codes with 128 x 128 block scales (dtype bf16)
