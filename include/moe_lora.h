@@ -502,6 +502,9 @@ int moe_lora_mx4_dequantize(int64_t num_rows, int32_t cols, int32_t dtype, const
  *            multiple of block_m.  Rows of tiles whose entry is outside [0,
  *            num_experts) (-1 past the end) are left as they were.  NULL: one weight
  *            (num_experts == 1) for every row, any num_rows.
+ *   sorted_pair_ids [num_rows] of moe_lora_align and num_pairs = num_tokens * top_k, or
+ *            NULL.  With them padding rows (entries outside [0, num_pairs)) are not
+ *            read and get zeros; most rows of a small batch are padding.
  *   out      [num_rows, out_features] (silu_mul: out_features / 2), BF16 or F32.
  *
  * MX4 x goes through the matrix cores' own 4-bit products, BF16 x multiplies the
@@ -511,9 +514,10 @@ int moe_lora_mx4_dequantize(int64_t num_rows, int32_t cols, int32_t dtype, const
  * A workgroup covers rows of one tile_expert entry, so block_m is also the most
  * rows that share one read of a weight: 16 for a few rows per expert, up to 256
  * for many (a multiple of 64 at least from 64 rows per expert on).
- * in_features: a multiple of 32; out_features: of 16 (32 with silu_mul); both at
- * most 2^24; num_rows / 16 * out_features / 64 < 2^24 (else
- * MOE_LORA_ERR_UNSUPPORTED).  x, w and out 16-byte aligned.  No workspace.
+ * in_features: a multiple of 32, at most 2^20; out_features: of 16 (32 with
+ * silu_mul), at most 2^24; out_features * in_features < 2^37 and
+ * num_rows / 16 * out_features / 64 < 2^24 (else MOE_LORA_ERR_UNSUPPORTED).  x, w
+ * and out 16-byte aligned.  No workspace.
  */
 typedef struct moe_lora_mx4_gemm_args {
   size_t struct_size; /* sizeof(moe_lora_mx4_gemm_args) */
@@ -527,6 +531,8 @@ typedef struct moe_lora_mx4_gemm_args {
   const uint8_t* w;
   const uint8_t* w_scale;
   const int32_t* tile_expert;
+  const int32_t* sorted_pair_ids;
+  int32_t num_pairs;
   void* out;
 } moe_lora_mx4_gemm_args;
 

@@ -810,7 +810,8 @@ class Mx4GemmArgs(ctypes.Structure):
         ("silu_mul", ctypes.c_int32),
         ("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p),
         ("w", ctypes.c_void_p), ("w_scale", ctypes.c_void_p),
-        ("tile_expert", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("tile_expert", ctypes.c_void_p), ("sorted_pair_ids", ctypes.c_void_p),
+        ("num_pairs", ctypes.c_int32), ("out", ctypes.c_void_p),
     ]
 
 
@@ -889,7 +890,8 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
     ``align_out`` None: w_codes [N, K/2], w_scales [N, K/32], x [M, K] of any M.
     Otherwise w_codes [E, N, K/2], w_scales [E, N, K/32] and x [capacity, K] in
     expert order (moe_lora_permute); rows behind the last used tile are left as they
-    are in ``out`` (undefined when it is not given).
+    are in ``out`` (undefined when it is not given).  With ``pair_rows`` in align_out
+    padding rows are not read and get zeros.
     x: bfloat16, or MX4 codes [M, K/2] with ``x_scales`` [M, K/32].  ``out`` /
     ``out_dtype``: bfloat16 (the default) or float32."""
     K = _mx4_pair(w_codes, w_scales, "w")
@@ -911,8 +913,10 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
             raise ValueError("x must hold whole tiles of block_m rows")
         _need(align_out["tile_expert"], "tile_expert", torch.int32, dev, M // a.block_m)
         a.tile_expert = align_out["tile_expert"].data_ptr()
-        if M == 0:
-            a.tile_expert = None
+        if "pair_rows" in align_out:   # its length tells pairs from padding
+            _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, M)
+            a.sorted_pair_ids = align_out["sorted_pair_ids"].data_ptr()
+            a.num_pairs = align_out["pair_rows"].numel()
     cols = N // 2 if silu_mul else N
     if out is None:
         out = torch.empty((M, cols), dtype=out_dtype or torch.bfloat16, device=dev)

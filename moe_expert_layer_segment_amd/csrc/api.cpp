@@ -330,6 +330,7 @@ int moe_lora_dense_forward_events(const moe_lora_dense_args* args, void* stream,
 
 constexpr int64_t kMaxRows = INT32_MAX;   // rows are named by int32
 constexpr int64_t kMaxCols = int64_t(1) << 24;
+constexpr int64_t kMaxGemmK = int64_t(1) << 20;   // 256 rows of bf16 x, in 32-bit offsets
 
 static int to_layout(int32_t num_tokens, int32_t top_k, int32_t hidden, int64_t num_rows,
                      const int32_t* sorted_pair_ids, const int32_t* pair_rows,
@@ -451,13 +452,16 @@ int moe_lora_mx4_gemm(const moe_lora_mx4_gemm_args* a, void* stream) {
   if (a->num_rows < 0 || a->out_features <= 0 || a->in_features <= 0 || a->num_experts <= 0)
     return MOE_LORA_ERR_INVALID;
   if (a->in_features % 32 || a->out_features % (a->silu_mul ? 32 : 16) ||
-      a->in_features > kMaxCols || a->out_features > kMaxCols || a->num_rows > kMaxRows)
+      a->in_features > kMaxGemmK || a->out_features > kMaxCols || a->num_rows > kMaxRows)
     return MOE_LORA_ERR_UNSUPPORTED;
   if (a->tile_expert) {
     if (bad_block_m(a->block_m) || a->num_rows % a->block_m) return MOE_LORA_ERR_INVALID;
   } else if (a->num_experts != 1) {
     return MOE_LORA_ERR_INVALID;   // rows of several experts need their tiles
   }
+  if (a->sorted_pair_ids && (!a->tile_expert || a->num_pairs < 0)) return MOE_LORA_ERR_INVALID;
+  // the scales of one weight are addressed with 32-bit offsets
+  if ((int64_t)a->out_features * (a->in_features / 32) >= kMaxOffsetBytes) return MOE_LORA_ERR_UNSUPPORTED;
   // threads of one launch are counted in 32 bits: 256 to 16 rows x 64 columns at the least
   if ((a->num_rows + 15) / 16 * ((a->out_features + 63) / 64) >= (int64_t(1) << 24))
     return MOE_LORA_ERR_UNSUPPORTED;
@@ -473,6 +477,7 @@ int moe_lora_mx4_gemm(const moe_lora_mx4_gemm_args* a, void* stream) {
   p.silu_mul = a->silu_mul != 0;
   p.x = a->x; p.x_scale = a->x_scale; p.w = a->w; p.w_scale = a->w_scale;
   p.tile_expert = a->tile_expert; p.out = a->out;
+  p.row_ids = a->sorted_pair_ids; p.num_ids = a->num_pairs;
   return hip_status(launch_mx4_gemm(p, static_cast<hipStream_t>(stream)));
 }
 

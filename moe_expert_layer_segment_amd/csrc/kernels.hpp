@@ -81,6 +81,8 @@ struct Mx4Gemm {
   const uint8_t* w;                  // [E, N, K / 2]
   const uint8_t* w_scale;            // [E, N, K / 32]
   const int32_t* tile_expert;        // [M / BM], null: one weight for all rows
+  const int32_t* row_ids;            // [M], null, or rows outside [0, num_ids) are pads
+  int32_t num_ids;
   void* out;                         // [M, N], or [M, N / 2] with silu_mul
 };
 hipError_t launch_mx4_gemm(const Mx4Gemm& p, hipStream_t stream);

@@ -7,8 +7,7 @@
 // row.  One MFMA of 128 K values wants, per lane, the 32 values (16 bytes) of
 // one block of one row and that block's scale: lane l holds row l % 16 and one of
 // four blocks.  Which four blocks of a row make up a step is free as long as both
-// operands agree; here lane group g = l / 16 takes blocks 2g and 2g + 1 of every 8
-// (one 128-byte line of codes), so its two scale bytes are neighbours.
+// operands agree.
 //
 //   MX4 x:   v_mfma_scale_f32_16x16x128_f8f6f4 on the codes as they are.  Products
 //            of codes are exact; the sums are fp32.
@@ -21,6 +20,9 @@
 #include "gemm_common.hpp"
 #include "kernels.hpp"
 
+#ifndef FEWG
+#define FEWG 512
+#endif
 namespace moelora {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -46,6 +48,16 @@ __device__ __forceinline__ floatx4 mfma_mx4(u32x4 a, int sa, u32x4 b, int sb, fl
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, 0, sa, 0, sb);
 }
 
+// t[q] of lane group g = w[g] of lane group q: a 4 x 4 transpose over the groups of
+// 16 lanes, in four swaps
+__device__ __forceinline__ u32x4 transpose_groups(u32x4 w) {
+  const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  return u32x4{c[0], c[1], d[0], d[1]};
+}
+
 __device__ __forceinline__ void store_out(const Mx4Gemm& p, int64_t at, floatx4 v) {
   if (p.out_f32) {
     *reinterpret_cast<floatx4*>(static_cast<float*>(p.out) + at) = v;
@@ -63,105 +75,231 @@ __device__ __forceinline__ int64_t weight_row(const Mx4Gemm& p, int64_t cb) {
   return p.silu_mul ? (cb & 1) * (p.N / 2) + (cb >> 1) * 16 : cb * 16;
 }
 
-// Few rows: the weights are streamed from memory into registers, once.  A workgroup
-// holds 16 MB rows and 16 NB columns; its WV waves take every WV-th group of 8
-// blocks (256 K values) and add their sums through LDS.
-template <bool XMX, int MB, int NB, int WV>
-__global__ void __launch_bounds__(64 * WV) mx4_stream_kernel(Mx4Gemm p, int col_groups) {
-  extern __shared__ floatx4 sums[];   // [WV][MB * NB][64]
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+// ---- few rows --------------------------------------------------------------
+// The weights are streamed from memory into registers, once, and bound the kernel.
+// A workgroup holds 16 MB rows and 16 NB columns; its WV waves take every WV-th group
+// of GB blocks and add their sums through LDS.
+//
+// A group is steps of four blocks.  In a step lane group g loads block g of it, so the
+// 16 bytes of neighbouring groups make up 64 bytes of a row; so do the bytes of bf16 x,
+// of which group g loads 16 g..16 g + 15 of each of the step's blocks.  To match, the
+// weights' words are exchanged between the groups: 4 x 4 words, in four swaps.
+// (Loading x to match the weights instead, 16 bytes in 64, took 91 us where this took
+// 64 on gate and up of 64 tokens x 8 of 128 experts, 1536 x 2048.)
+//
+// What the rows and the scales cost there, beside 36 us for the codes alone (5.9 TB/s):
+// 16 us for x, whose padding rows (three in four) are therefore not read, and 10 us
+// for scales loaded as they are used, 8 bytes of a row at a time.  The 16 rows of a
+// block have their scales in one piece of memory, so a workgroup fetches them
+// 16 bytes a lane into LDS first, up to K = kStageK.
+constexpr int kStageK = 16384;
+
+template <bool XMX, int MB, int NB, int GB, int WV>
+__global__ void __launch_bounds__(64 * WV, 2) mx4_stream_kernel(Mx4Gemm p, int row_groups,
+                                                                int col_groups, int spread) {
+  constexpr int STEPS = GB / 4;
+  __shared__ floatx4 sums[WV][MB * NB][64];
+  extern __shared__ __attribute__((aligned(16))) uint8_t staged[];   // [NB (+ MB)][16][nblk]
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
-  const int64_t m0 = (int64_t)(blockIdx.x / col_groups) * (16 * MB);
-  const int64_t cb0 = (int64_t)(blockIdx.x % col_groups) * NB;
-  const int64_t ncb = p.N / 16;
-  int64_t e = 0;
-  if (p.tile_expert) {
-    e = p.tile_expert[m0 / p.BM];
-    if (e < 0 || e >= p.E) return;
+  // With many row groups (spread) the column groups of two neighbouring ones run on one
+  // XCD (workgroup b on XCD b % 8), in pairs: its L2 then holds their rows, and the
+  // weights where the two are of one expert.
+  int row_group, col_group;
+  if (spread) {
+    const int at = (int)(blockIdx.x / 8), two = 2 * col_groups;
+    row_group = (at / two * 8 + (int)(blockIdx.x % 8)) * 2 + at % 2;
+    col_group = at % two / 2;
+  } else {
+    row_group = (int)blockIdx.x / col_groups;
+    col_group = (int)blockIdx.x % col_groups;
   }
-  const int nblk = (int)(p.K / 32);
-  const uint8_t *wc[NB], *ws[NB], *xc[MB], *xs[MB];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int64_t n = e * p.N + weight_row(p, min(cb0 + nb, ncb - 1)) + r;
-    wc[nb] = p.w + n * (p.K / 2);
-    ws[nb] = p.w_scale + n * nblk;
-  }
+  if (row_group >= row_groups) return;
+  const int64_t m0 = (int64_t)row_group * (16 * MB);
+  const int64_t cb0 = (int64_t)col_group * NB, ncb = p.N / 16;
+  int32_t id[MB];
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb) {
     const int64_t m = min(m0 + mb * 16 + r, p.M - 1);
-    xc[mb] = static_cast<const uint8_t*>(p.x) + m * (XMX ? p.K / 2 : p.K * 2);
-    xs[mb] = XMX ? p.x_scale + m * nblk : nullptr;
+    id[mb] = p.row_ids ? p.row_ids[m] : 0;
   }
+  int64_t e = 0;
+  if (p.tile_expert) {
+    e = __builtin_amdgcn_readfirstlane(p.tile_expert[m0 / p.BM]);
+    if (e < 0 || e >= p.E) return;
+  }
+  const int nblk = (int)(p.K / 32);
+  // uniform bases and an offset per lane
+  const int64_t w_row = p.K / 2, x_row = XMX ? p.K / 2 : p.K * 2;
+  const uint8_t* const x_base = static_cast<const uint8_t*>(p.x) + m0 * x_row;
+  const uint8_t* const xs_base = XMX ? p.x_scale + m0 * nblk : nullptr;
+  uint32_t m_lane[MB];
+  bool live[MB];
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    m_lane[mb] = (uint32_t)min((int64_t)mb * 16 + r, p.M - 1 - m0);
+    live[mb] = !p.row_ids || (id[mb] >= 0 && id[mb] < p.num_ids);
+  }
+  // Scales on their way to LDS, in pieces of 16 bytes: nblk of a block's 16 rows.  The
+  // first piece of a thread travels beside its first codes.
+  const bool stage = p.K <= kStageK;
+  const bool stage_x = XMX && stage && m0 + 16 * MB <= p.M;
+  const int pieces = stage ? (NB + (stage_x ? MB : 0)) * nblk : 0;
+  auto fetch = [&](int at) {
+    const int blk = at / nblk, in = (at - blk * nblk) * 16;
+    const uint8_t* src = p.w_scale + (e * p.N + weight_row(p, min(cb0 + blk, ncb - 1))) * nblk;
+    if constexpr (XMX) {
+      if (blk >= NB) src = xs_base + (int64_t)(blk - NB) * 16 * nblk;
+    }
+    u32x4 v;
+    __builtin_memcpy(&v, src + in, 16);
+    return v;
+  };
+  auto put = [&](int at, u32x4 v) { *reinterpret_cast<u32x4*>(staged + at * 16) = v; };
+#pragma unroll 1
+  for (int at = 64 * WV + (int)threadIdx.x; at < pieces; at += 64 * WV) put(at, fetch(at));
+  u32x4 piece = {0, 0, 0, 0};
+  if ((int)threadIdx.x < pieces) piece = fetch(threadIdx.x);
+
+  struct Group {
+    u32x4 w[NB][STEPS], x[MB][XMX ? STEPS : GB];
+  };
+  // the scales of group s, 2^0 behind the end and for padding rows (whose scales may be
+  // anything, NaN too)
+  uint32_t wsc[NB][STEPS], xsc[XMX ? MB : 1][STEPS];
+  auto load_scales = [&](int s, auto end) {
+    auto get = [&](uint32_t (&v)[STEPS], const uint8_t* row) {
+      if constexpr (!decltype(end)::value) {
+        __builtin_memcpy(v, row + s * GB, GB);
+      } else {
+#pragma unroll
+        for (int h = 0; h < STEPS; ++h) {
+          v[h] = 0;
+#pragma unroll
+          for (int i = 3; i >= 0; --i) {
+            const int b = s * GB + 4 * h + i;
+            v[h] = v[h] << 8 | (b < nblk ? row[b] : 127);
+          }
+        }
+      }
+    };
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      if (stage) {
+        get(wsc[nb], staged + (nb * 16 + r) * nblk);
+      } else {
+        get(wsc[nb], p.w_scale + (e * p.N + weight_row(p, min(cb0 + nb, ncb - 1)) + r) * nblk);
+      }
+    }
+    if constexpr (XMX) {
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        if (stage_x) {
+          get(xsc[mb], staged + ((NB + mb) * 16 + r) * nblk);
+        } else {
+          get(xsc[mb], xs_base + (int64_t)m_lane[mb] * nblk);
+        }
+        if (!live[mb]) {
+#pragma unroll
+          for (int h = 0; h < STEPS; ++h) xsc[mb][h] = 0x7F7F7F7Fu;
+        }
+      }
+    }
+  };
+  auto load = [&](Group& f, int s, auto end) {
+    constexpr bool kEnd = decltype(end)::value;
+    // blocks behind the row's end: zero codes under the scale of 1
+    auto codes = [&](const uint8_t* base, uint32_t row, int h) {
+      const int blk = s * GB + 4 * h + g;
+      const bool in = !kEnd || blk < nblk;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(base + (row + (in ? blk : 0) * 16));
+      return in ? v : u32x4{0, 0, 0, 0};
+    };
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int64_t n = e * p.N + weight_row(p, min(cb0 + nb, ncb - 1));
+#pragma unroll
+      for (int h = 0; h < STEPS; ++h) f.w[nb][h] = codes(p.w + n * w_row, r * (uint32_t)w_row, h);
+    }
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+#pragma unroll
+      for (int q = 0; q < (XMX ? STEPS : GB); ++q) f.x[mb][q] = u32x4{0, 0, 0, 0};
+      if (live[mb]) {
+        const uint32_t row = m_lane[mb] * (uint32_t)x_row;
+        if constexpr (XMX) {
+#pragma unroll
+          for (int h = 0; h < STEPS; ++h) f.x[mb][h] = codes(x_base, row, h);
+        } else {
+#pragma unroll
+          for (int q = 0; q < GB; ++q)
+            if (!kEnd || s * GB + q < nblk)
+              f.x[mb][q] = *reinterpret_cast<const u32x4*>(x_base + (row + (s * GB + q) * 64 + g * 16));
+        }
+      }
+    }
+  };
   floatx4 acc[MB][NB];
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  for (int s = wave; s * 8 < nblk; s += WV) {
+  auto multiply = [&](const Group& f) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      // blocks behind the row's end: zero codes under the scale of 1
-      const int blk = s * 8 + 2 * g + b;
-      const bool in = blk < nblk;
-      const int at = in ? blk : 0;
-      u32x4 wf[NB];
-      int wsc[NB];
+    for (int h = 0; h < STEPS; ++h) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        wf[nb] = *reinterpret_cast<const u32x4*>(wc[nb] + at * 16);
-        wsc[nb] = ws[nb][at];
-        if (!in) {
-          wf[nb] = u32x4{0, 0, 0, 0};
-          wsc[nb] = 127;
-        }
-      }
-      if constexpr (XMX) {
+        if constexpr (XMX) {
+          const int sw = (int)(wsc[nb][h] >> (8 * g));
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          u32x4 xf = *reinterpret_cast<const u32x4*>(xc[mb] + at * 16);
-          int xsc = xs[mb][at];
-          if (!in) {
-            xf = u32x4{0, 0, 0, 0};
-            xsc = 127;
-          }
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            acc[mb][nb] = mfma_mx4(wf[nb], wsc[nb], xf, xsc, acc[mb][nb]);
-        }
-      } else {
-        bf16x8 xf[MB][4];
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
+          for (int mb = 0; mb < MB; ++mb)
+            acc[mb][nb] = mfma_mx4(f.w[nb][h], sw, f.x[mb][h], (int)(xsc[mb][h] >> (8 * g)),
+                                   acc[mb][nb]);
+        } else {
+          const u32x4 t = transpose_groups(f.w[nb][h]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            xf[mb][q] = *reinterpret_cast<const bf16x8*>(xc[mb] + at * 64 + q * 16);
-            if (!in) xf[mb][q] = Elt<bf16_t>::zero();
-          }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const float scale = mx4_scale((uint32_t)wsc[nb]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const bf16x8 a = mx4_bf16x8(wf[nb][q], scale);
+            // the scale byte as an exponent; the conversion reads 0 as 2^-127, 255 as NaN
+            const uint32_t scale = (wsc[nb][h] >> (8 * q) & 255) << 23;
+            const bf16x8 a = mx4_bf16x8(t[q], __builtin_bit_cast(float, scale));
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
-              acc[mb][nb] = Elt<bf16_t>::mma(a, xf[mb][q], acc[mb][nb]);
+              acc[mb][nb] = Elt<bf16_t>::mma(a, __builtin_bit_cast(bf16x8, f.x[mb][4 * h + q]),
+                                             acc[mb][nb]);
           }
         }
       }
     }
+  };
+  Group f;
+  int s = wave;
+  const int whole = nblk / GB;
+  if (s < whole) load(f, s, std::false_type{});
+  if (stage) {
+    if ((int)threadIdx.x < pieces) put(threadIdx.x, piece);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the first loads stay in flight
+  }
+  while (s < whole) {
+    load_scales(s, std::false_type{});
+    multiply(f);
+    s += WV;
+    if (s < whole) load(f, s, std::false_type{});
+  }
+  if (s * GB < nblk) {   // the wave whose turn it is takes the end of the rows
+    load(f, s, std::true_type{});
+    load_scales(s, std::true_type{});
+    multiply(f);
   }
 
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) sums[(wave * MB * NB + mb * NB + nb) * 64 + lane] = acc[mb][nb];
+    for (int nb = 0; nb < NB; ++nb) sums[wave][mb * NB + nb][lane] = acc[mb][nb];
   __syncthreads();
   auto total = [&](int tile) {
-    floatx4 v = sums[tile * 64 + lane];
-    for (int w = 1; w < WV; ++w) v += sums[(w * MB * NB + tile) * 64 + lane];
+    floatx4 v = sums[0][tile][lane];
+#pragma unroll
+    for (int w = 1; w < WV; ++w) v += sums[w][tile][lane];
     return v;
   };
   if (p.silu_mul) {
@@ -187,66 +325,81 @@ __global__ void __launch_bounds__(64 * WV) mx4_stream_kernel(Mx4Gemm p, int col_
 
 // ---- many rows -------------------------------------------------------------
 // Tiles of TM rows x 256 weight rows, K in steps of 128-byte LDS rows of x: 256
-// values of MX4 x or 64 of bf16.  Codes reach LDS by global -> LDS DMA in a ring of
-// two slots; scales take the long way through registers, because their rows need not be
-// aligned.
-// Eight waves as 2 x 4, each (TM / 2) x 64.
+// values of MX4 x or 64 of bf16.  Eight waves as 2 x 4, each (TM / 2) x 64.
+//
+// Codes reach LDS by global -> LDS DMA, in a ring of RING K tiles: three of bf16 x
+// (40 KB each; two took the prefill product of a 4096 x 14336 layer from 0.97 to
+// 1.13 ms), two of MX4 x (64 KB; a ring of nine quarters, one of which stays in
+// flight over each wait, was 8% slower).  What bounds both is the L1, which keeps
+// about 64 lines in flight: 64 KB per 256 x 256 x 256 products, at that window over
+// the latency of the L2.
 //
 // A K tile is two steps.  In a step a wave keeps its four weight fragments in
 // registers and takes the 16-row blocks of x one after another, four MFMAs each,
 // reading the block that comes kAhead later meanwhile.  When the last fragments of
 // a tile have been read, a barrier admits the next tile; behind it the wave starts
-// the DMA of the tile after next into the slot just left and reads the next tile's
-// first fragments under the MFMAs that remain.
+// the DMA into the places just left and reads the next tile's first fragments under
+// the MFMAs that remain.
 //
-// LDS rows of x (and of MX4 weights) are eight 16-byte chunks, chunk c of a row in
-// place c ^ ((row >> 1) & 7): the 16 rows of a fragment read then fall on all banks.
+// LDS rows of x (and of MX4 weights) are eight 16-byte chunks.  Lane group g wants
+// chunk 2g + h in step h.  A fragment read serves 16 lanes at a time, rows of two
+// neighbouring groups among them; without a bank met twice it reads a chunk either from
+// place (4h + g) ^ (bits 3, 2, 1 of the row's number) or from place (2g + h) ^ (bits
+// 3, 1, 2).  The first spreads the four lanes of a DMA that should share 64 bytes over
+// 128, which costs MX4 x, whose two operands both come this way, 5%; bf16 x is 7%
+// faster with it.
 constexpr int kTileN = 256;
 
 __device__ __attribute__((aligned(16))) uint32_t mx4_zeros[4];   // what lies behind a row's end
 
-// as dma16, with an address per lane
-__device__ __forceinline__ void dma16_lane(const void* p, uint32_t lds_addr) {
+// as dma16, with an address per lane, of 16 or of 4 bytes a lane
+template <int BYTES>
+__device__ __forceinline__ void dma_lane(const void* p, uint32_t lds_addr) {
   const uint32_t la = __builtin_amdgcn_readfirstlane(lds_addr);
   uint32_t saved;
-  asm volatile(
-      "s_mov_b32 %[sv], m0\n\t"
-      "s_mov_b32 m0, %[la]\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %[p], off\n\t"
-      "s_mov_b32 m0, %[sv]"
-      : [sv] "=&s"(saved)
-      : [la] "s"(la), [p] "v"((uint64_t)(uintptr_t)p)
-      : "memory");
+  if constexpr (BYTES == 16)
+    asm volatile(
+        "s_mov_b32 %[sv], m0\n\t"
+        "s_mov_b32 m0, %[la]\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %[p], off\n\t"
+        "s_mov_b32 m0, %[sv]"
+        : [sv] "=&s"(saved)
+        : [la] "s"(la), [p] "v"((uint64_t)(uintptr_t)p)
+        : "memory");
+  else
+    asm volatile(
+        "s_mov_b32 %[sv], m0\n\t"
+        "s_mov_b32 m0, %[la]\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %[p], off\n\t"
+        "s_mov_b32 m0, %[sv]"
+        : [sv] "=&s"(saved)
+        : [la] "s"(la), [p] "v"((uint64_t)(uintptr_t)p)
+        : "memory");
 }
 
-// this wave's DMA and LDS accesses are done, then every wave's
-__device__ __forceinline__ void wait_all_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// COUNT (4 or 16) scale bytes of a row from block b0 on
-template <int COUNT> struct ScaleWords { typedef uint32_t type __attribute__((ext_vector_type(COUNT / 4))); };
-template <> struct ScaleWords<4> { typedef uint32_t type; };
-template <int COUNT>
-__device__ __forceinline__ typename ScaleWords<COUNT>::type load_scales(const uint8_t* row, int b0) {
-  typename ScaleWords<COUNT>::type v;
-  __builtin_memcpy(&v, row + b0, COUNT);
-  return v;
+// this wave's DMA but the newest N and its LDS accesses are done, then every wave's
+template <int N>
+__device__ __forceinline__ void wait_dma_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 template <bool XMX, int TM>
 __global__ void __launch_bounds__(512) mx4_tile_kernel(
-    Mx4Gemm p, int m_tiles, int n_tiles, int pn, int n_patches) {
-  constexpr int WM = 2, WN = 4, NW = WM * WN, NT = 64 * NW;
-  constexpr int MB = TM / 16 / WM, NB = kTileN / 16 / WN;   // 16-row blocks of a wave
+    Mx4Gemm p, int m_tiles, int n_tiles, int pn, int n_patches, int dma_scales) {
+  constexpr int WN = 4, NW = 8;
+  constexpr int MB = TM / 32, NB = kTileN / 16 / WN;        // 16-row blocks of a wave
   constexpr int WROWB = XMX ? 128 : 32;                     // LDS bytes of a weight row
-  constexpr int XSTAGE = TM * 128, STAGE = XSTAGE + kTileN * WROWB;
+  constexpr int RING = XMX ? 2 : 3;
+  constexpr int XPART = TM * 128, STAGE = XPART + kTileN * WROWB;
+  constexpr int XSEG = XPART / 1024 / NW, WSEG = kTileN * WROWB / 1024 / NW;  // a wave's DMAs
   constexpr int SROWS = (XMX ? TM : 0) + kTileN;            // rows with scales; x's come first
   constexpr int KB = XMX ? 8 : 2;                           // blocks of 32 in a K tile
   constexpr int SB = 2 * KB;                                // scale bytes of a row for two K tiles
-  constexpr int SPT = (SROWS + NT - 1) / NT;                // scale rows of a thread
-  __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE + 2 * SROWS * SB];
+  constexpr int SCALES = RING * STAGE;                      // where the two scale buffers lie
+  static_assert(SROWS <= 64 * NW && SROWS % 64 == 0, "one scale row per thread");
+  __shared__ __attribute__((aligned(1024))) char lds[SCALES + 2 * SROWS * SB];
 
   // patches of (32 / pn) x pn tiles go round the eight XCDs (workgroup b runs on
   // XCD b % 8), so the 32 workgroups that an XCD holds share rows and weights in its L2
@@ -272,103 +425,98 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
   const char* x_base = static_cast<const char*>(p.x) + m0 * x_row;
   const uint8_t* w_base = p.w + e * p.N * (p.K / 2);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
-  auto swz = [](int row) { return (row >> 1) & 7; };
+  auto swz = [](int row) {
+    return XMX ? (row >> 1 & 4) | (row & 2) | (row >> 2 & 1) : (row >> 1) & 7;
+  };
+  auto chunk_in = [](int place) { return XMX ? place : (place & 3) * 2 + (place >> 2); };
   // weight row of LDS row n (rows of column blocks behind the last repeat it)
   auto w_row = [&](int n) { return weight_row(p, min(cb0 + n / 16, ncb - 1)) + n % 16; };
 
   // One KB of LDS per DMA: 8 rows of x or MX4 weights, 32 of the weights beside
-  // bf16 x.  The 8 rows of a segment lie at a uniform base, so two offsets per
-  // lane (the swizzle of even and of odd segments) serve them all.  A tile behind
-  // the end of K or of M takes an address per lane instead, worked out on the spot
-  // (kept over the loop, the addresses would cost more registers than there are).
-  constexpr int XSEG = XSTAGE / 1024 / NW, WSEG = kTileN * WROWB / 1024 / NW;
-  static_assert(XSEG % 2 == 0 && (!XMX || WSEG % 2 == 0), "segments come in pairs");
+  // bf16 x.  The 8 rows of a segment lie at a uniform base, so an offset per lane
+  // (one for even and one for odd segments: their swizzle differs) serves them all.
+  // A tile behind the end of K or of M takes an address per lane instead, worked out
+  // on the spot (kept over the loop, these would cost more registers than there are).
+  static_assert(XSEG % 2 == 0 && (!XMX || WSEG % 2 == 0), "segments of a wave come in pairs");
   uint32_t lane_off[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    lane_off[h] = (uint32_t)(lane / 8 * (int)x_row + ((lane % 8) ^ swz(h * 8 + lane / 8)) * 16);
+    lane_off[h] = (uint32_t)(lane / 8 * (int)x_row + chunk_in((lane % 8) ^ swz(h * 8 + lane / 8)) * 16);
   const bool all_rows = m_last == TM - 1;
-  auto issue = [&](int t, int slot, auto fast) {   // fast: a whole tile of whole rows
-    const uint32_t at = lds0 + slot * STAGE;
-    if constexpr (decltype(fast)::value) {
-#pragma unroll
-      for (int i = 0; i < XSEG; ++i) {
-        const int seg = wave * XSEG + i;
+  constexpr int DMAS = XSEG + WSEG;      // of a wave, for a tile
+  // the i-th of them; fast: a whole tile of whole rows
+  auto issue_one = [&](int t, int place, int i, auto fast) {
+    constexpr bool kWhole = decltype(fast)::value;
+    const uint32_t at = lds0 + place * STAGE;
+    int l = lane;
+    if constexpr (!kWhole) asm volatile("" : "+v"(l));
+    if (i < XSEG) {
+      const int seg = wave * XSEG + i;
+      if constexpr (kWhole) {
         dma16(x_base + seg * 8 * x_row, lane_off[i % 2] + t * 128, at + seg * 1024);
-      }
-    } else {
-      int l = lane;
-      asm volatile("" : "+v"(l));
-#pragma unroll
-      for (int i = 0; i < XSEG; ++i) {
-        const int seg = wave * XSEG + i, row = seg * 8 + l / 8, c = (l % 8) ^ swz(row);
+      } else {
+        const int row = seg * 8 + l / 8, c = chunk_in((l % 8) ^ swz(row));
         // chunks of 16 bytes: a block of MX4, a quarter of one in bf16
         const bool in_row = t * KB + (XMX ? c : c / 4) < nblk;
         const char* src = x_base + min(row, m_last) * x_row + t * 128 + c * 16;
-        dma16_lane(in_row ? (const void*)src : (const void*)mx4_zeros, at + seg * 1024);
-      }
-    }
-    if constexpr (XMX && decltype(fast)::value) {
-#pragma unroll
-      for (int i = 0; i < WSEG; ++i) {
-        const int seg = wave * WSEG + i;
-        dma16(w_base + w_row(seg * 8) * (p.K / 2), lane_off[i % 2] + t * 128,
-              at + XSTAGE + seg * 1024);
+        dma_lane<16>(in_row ? (const void*)src : (const void*)mx4_zeros, at + seg * 1024);
       }
     } else {
-      int l = lane;
-      asm volatile("" : "+v"(l));
-#pragma unroll
-      for (int i = 0; i < WSEG; ++i) {
-        const int seg = wave * WSEG + i;
-        const int row = XMX ? seg * 8 + l / 8 : seg * 32 + l / 2;
-        const int c = XMX ? (l % 8) ^ swz(row) : l % 2;
-        const uint8_t* src = w_base + w_row(row) * (p.K / 2) + t * WROWB + c * 16;
-        dma16_lane(t * KB + c < nblk ? (const void*)src : (const void*)mx4_zeros,
-                   at + XSTAGE + seg * 1024);
-      }
-    }
-  };
-
-  // scale rows of this thread, and their way through registers into LDS
-  const uint8_t* s_row[SPT];
-  // The scales of tiles 2 grp and 2 grp + 1 go through registers into LDS: the load
-  // behind the barrier of the even tile before them, the store ahead of that of
-  // the odd one.
-  typename ScaleWords<SB>::type s_val[SPT];
-#pragma unroll
-  for (int i = 0; i < SPT; ++i) {
-    const int q = min((int)threadIdx.x + i * NT, SROWS - 1);
-    if (XMX && q < TM) s_row[i] = p.x_scale + (m0 + min(q, m_last)) * nblk;
-    else s_row[i] = p.w_scale + (e * p.N + w_row(q - (XMX ? TM : 0))) * nblk;
-  }
-  auto scales_load = [&](int grp, auto fast) {   // fast: both tiles are whole
-#pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-      if (decltype(fast)::value || (grp + 1) * SB <= nblk) {
-        s_val[i] = load_scales<SB>(s_row[i], grp * SB);
+      const int seg = wave * WSEG + i - XSEG;
+      const uint32_t to = at + XPART + seg * 1024;
+      if constexpr (XMX && kWhole) {
+        dma16(w_base + w_row(seg * 8) * (p.K / 2), lane_off[(i - XSEG) % 2] + t * 128, to);
       } else {
-        // 2^0 behind the end of the row
-        uint8_t bytes[SB];
-#pragma unroll
-        for (int b = 0; b < SB; ++b) bytes[b] = grp * SB + b < nblk ? s_row[i][grp * SB + b] : 127;
-        __builtin_memcpy(&s_val[i], bytes, SB);
+        const int row = XMX ? seg * 8 + l / 8 : seg * 32 + l / 2;
+        const int c = XMX ? chunk_in((l % 8) ^ swz(row)) : l % 2;
+        const uint8_t* src = w_base + w_row(row) * (p.K / 2) + t * WROWB + c * 16;
+        const bool in_row = kWhole || t * KB + c < nblk;
+        dma_lane<16>(in_row ? (const void*)src : (const void*)mx4_zeros, to);
       }
     }
   };
-  char* const s_lds = lds + 2 * STAGE;
-  auto scales_store = [&](int grp) {
+  auto issue = [&](int t, int place, int from, int to, auto fast) {
 #pragma unroll
-    for (int i = 0; i < SPT; ++i) {
-      const int q = (int)threadIdx.x + i * NT;
-      if (SROWS % NT == 0 || q < SROWS)
-        __builtin_memcpy(s_lds + ((grp & 1) * SROWS + q) * SB, &s_val[i], SB);
-    }
+    for (int i = 0; i < DMAS; ++i)
+      if (i >= from && i < to) issue_one(t, place, i, fast);
   };
 
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  // Scales of tiles 2 grp and 2 grp + 1, a row per thread.  Beside bf16 x they take
+  // the DMA (4 bytes a row) where rows of them are aligned to words; MX4's 16 bytes a
+  // row go through registers (by DMA they took a third more requests to the L2, and
+  // 347 instead of 326 us), loaded behind the barrier of an even tile and stored ahead
+  // of that of the odd one; so do those at the end of a row, with 2^0 behind it.
+  // (a wave's 64 rows are all of x or all of the weights: a uniform base)
+  const int s_lane = min(wave * 64 + lane, SROWS - 1);
+  const bool s_of_x = XMX && wave < TM / 64;
+  const uint8_t* const s_base = s_of_x ? p.x_scale + m0 * nblk : p.w_scale + e * p.N * nblk;
+  const uint32_t s_off = (uint32_t)(s_of_x ? min(s_lane, m_last) : w_row(s_lane - (XMX ? TM : 0))) *
+                         (uint32_t)nblk;
+  struct Words { uint32_t w[SB / 4]; } s_val;
+  auto scales_load = [&](int grp) {
+    __builtin_memcpy(&s_val, s_base + grp * SB + s_off, SB);
+  };
+  auto scales_load_end = [&](int grp) {
+#pragma unroll
+    for (int w = 0; w < SB / 4; ++w) {
+      s_val.w[w] = 0;
+#pragma unroll 1
+      for (int b = grp * SB + 4 * w + 3; b >= grp * SB + 4 * w; --b)
+        s_val.w[w] = s_val.w[w] << 8 | (b < nblk ? s_base[s_off + b] : 127);
+    }
+  };
+  auto scales_store = [&](int grp) {
+    if (SROWS == 64 * NW || (int)threadIdx.x < SROWS)
+      __builtin_memcpy(lds + SCALES + ((grp & 1) * SROWS + threadIdx.x) * SB, &s_val, SB);
+  };
+  auto scales_dma = [&](int grp) {
+    if (wave < SROWS / 64)
+      dma_lane<SB>(s_base + grp * SB + s_off, lds0 + SCALES + ((grp & 1) * SROWS + wave * 64) * SB);
+  };
+
   constexpr int kAhead = 3, kRing = 4;
   static_assert((2 * MB) % kRing == 0 && MB > kAhead, "the ring starts each tile at its first place");
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   // of a K tile.  MX4: a word holds the bytes of both steps of two neighbouring
   // blocks; bf16 x: the weights' codes of both steps, and their scale bytes
   struct TileScales {
@@ -376,30 +524,26 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
     u32x2 codes[XMX ? 1 : NB];
   };
   // places of this lane's row of a wave's first block; a block is 16 rows further
-  int x_at[2], w_at[2];
+  const int x_lane = (wm * MB * 16 + r) * 128, w_lane = XPART + (wn * NB * 16 + r) * WROWB;
+  int c_at[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c = ((2 * g + h) ^ swz(r)) * 16;
-    x_at[h] = (wm * MB * 16 + r) * 128 + c;
-    w_at[h] = XSTAGE + (wn * NB * 16 + r) * 128 + c;
-  }
-  const int codes_at = XSTAGE + (wn * NB * 16 + r) * 32 + g * 8;
-  const int xs_at = 2 * STAGE + (wm * MB * 16 + r) * SB + 2 * g;
-  const int ws_at = 2 * STAGE + ((XMX ? TM : 0) + wn * NB * 16 + r) * SB + (XMX ? 2 * g : g >> 1);
-  auto read_x = [&](int slot, int i, int step) {
-    return *reinterpret_cast<const u32x4*>(lds + slot * STAGE + x_at[step] + i * 2048);
+  for (int h = 0; h < 2; ++h) c_at[h] = ((XMX ? 2 * g + h : 4 * h + g) ^ swz(r)) * 16;
+  const int xs_at = SCALES + (wm * MB * 16 + r) * SB + 2 * g;
+  const int ws_at = SCALES + ((XMX ? TM : 0) + wn * NB * 16 + r) * SB + (XMX ? 2 * g : g >> 1);
+  auto read_x = [&](int place, int i, int step) {
+    return *reinterpret_cast<const u32x4*>(lds + place * STAGE + x_lane + c_at[step] + i * 2048);
   };
-  auto read_w = [&](int slot, int j, int step) {
-    return *reinterpret_cast<const u32x4*>(lds + slot * STAGE + w_at[step] + j * 2048);
+  auto read_w = [&](int place, int j, int step) {
+    return *reinterpret_cast<const u32x4*>(lds + place * STAGE + w_lane + c_at[step] + j * 2048);
   };
-  auto read_scales = [&](TileScales& f, int slot, int t) {
-    const char* s = lds + ((t / 2) & 1) * SROWS * SB + slot * KB;
+  auto read_scales = [&](TileScales& f, int place, int t) {
+    const char* s = lds + ((t / 2) & 1) * SROWS * SB + (t & 1) * KB;
     if constexpr (XMX) {
       typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-      auto two = [&](const char* at) {
+      auto two = [&](const char* q) {
         u16x2 v;
-        v[0] = *reinterpret_cast<const uint16_t*>(at);
-        v[1] = *reinterpret_cast<const uint16_t*>(at + 16 * SB);
+        v[0] = *reinterpret_cast<const uint16_t*>(q);
+        v[1] = *reinterpret_cast<const uint16_t*>(q + 16 * SB);
         return __builtin_bit_cast(int, v);
       };
 #pragma unroll
@@ -409,7 +553,7 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
     } else {
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        f.codes[j] = *reinterpret_cast<const u32x2*>(lds + slot * STAGE + codes_at + j * 512);
+        f.codes[j] = *reinterpret_cast<const u32x2*>(lds + place * STAGE + w_lane + g * 8 + j * 512);
         f.ws[j] = (int)*reinterpret_cast<const uint8_t*>(s + ws_at + j * 16 * SB);
       }
     }
@@ -456,28 +600,44 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
   constexpr std::integral_constant<int, 0> first{};
   constexpr std::integral_constant<int, 1> second{};
   // first fragments of tile t, as far as they are read before its MFMAs
-  auto read_first = [&](TileScales& f, int t) {
-    const int slot = t & 1;
-    read_scales(f, slot, t);
+  auto read_first = [&](TileScales& f, int place, int t) {
+    read_scales(f, place, t);
     if constexpr (XMX) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) w0[j] = read_w(slot, j, 0);
+      for (int j = 0; j < NB; ++j) w0[j] = read_w(place, j, 0);
     }
   };
-  // kEven, kOdd: a tile of that number with two whole tiles of whole rows or more
-  // behind the next; kAny: any but the last
+  int where = 0;          // place of the present tile in the ring
+  // kEven, kOdd: a tile of that number, with every tile and scale that it sends
+  // for whole; kAny: any but the last
   enum { kEven, kOdd, kAny, kLast };
+  // A wave's DMAs go out kPerBlock beside each block of x, the first kEarly of a tile
+  // behind the barrier that empties its place, the others in the tile that follows:
+  // one after another they hold the wave, and its MFMAs, at the L1's pace (bf16 x:
+  // 0.96 instead of 0.93 ms).
+  constexpr int kPerBlock = 2, kEarly = kAhead * kPerBlock < DMAS ? kAhead * kPerBlock : DMAS;
+  static_assert(kEarly + MB * kPerBlock >= DMAS, "every DMA has its block");
   auto tile = [&](int t, auto mode) {
     constexpr int kMode = decltype(mode)::value;
-    const int slot = t & 1;
+    // in a ring of two an even tile lies in place 0: known, it costs no address sums
+    constexpr bool kKnown = RING == 2 && (kMode == kEven || kMode == kOdd);
+    const int place = kKnown ? kMode == kOdd : where;
+    const int ahead = place + 1 == RING ? 0 : place + 1;
     if constexpr (!XMX) {
 #pragma unroll
       for (int j = 0; j < NB; ++j) w0[j] = expand(sc, j, 0);
     }
+    const int behind = place == 0 ? RING - 1 : place - 1;   // left by the tile before
     static_for<MB>([&](auto I) {
       constexpr int i = decltype(I)::value, q = i + kAhead;
-      x[q % kRing] = q < MB ? read_x(slot, q, 0) : read_x(slot, q - MB, 1);
-      if constexpr (i < NB) w1[i] = XMX ? read_w(slot, i, 1) : expand(sc, XMX ? 0 : i, 1);
+      x[q % kRing] = q < MB ? read_x(place, q, 0) : read_x(place, q - MB, 1);
+      if constexpr (i < NB) w1[i] = XMX ? read_w(place, i, 1) : expand(sc, XMX ? 0 : i, 1);
+      constexpr int from = kEarly + i * kPerBlock;
+      if constexpr (kMode == kAny) {
+        if (t + RING - 1 < tiles) issue(t + RING - 1, behind, from, from + kPerBlock, std::false_type{});
+      } else if constexpr (kMode != kLast) {
+        issue(t + RING - 1, behind, from, from + kPerBlock, std::true_type{});
+      }
       multiply(first, I, w0);
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -485,37 +645,50 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
     static_for<MB>([&](auto I) {
       constexpr int i = decltype(I)::value, q = MB + i + kAhead;
       if constexpr (i + kAhead < MB) {
-        x[q % kRing] = read_x(slot, i + kAhead, 1);
+        x[q % kRing] = read_x(place, i + kAhead, 1);
       } else if constexpr (kMode != kLast) {
         if constexpr (i + kAhead == MB) {
           pin();
-          if (kMode == kOdd || (kMode == kAny && (t & 1))) scales_store((t + 1) / 2);
-          wait_all_barrier();
-          if constexpr (kMode != kAny) issue(t + 2, slot, std::true_type{});
-          else if (t + 2 < tiles) issue(t + 2, slot, std::false_type{});
-          if constexpr (kMode == kEven) scales_load(t / 2 + 1, std::true_type{});
-          else if (kMode == kAny && !(t & 1) && t + 2 < tiles) scales_load(t / 2 + 1, std::false_type{});
-          read_first(next, t + 1);
+          if constexpr (kMode == kAny) {
+            if (t & 1) scales_store((t + 1) / 2);
+            wait_dma_barrier<0>();
+            if (!(t & 1) && t + 2 < tiles) scales_load_end(t / 2 + 1);
+          } else {
+            if constexpr (XMX && kMode == kOdd) scales_store((t + 1) / 2);
+            wait_dma_barrier<(RING - 2) * DMAS>();
+            if constexpr (!XMX && kMode == kEven) scales_dma(t / 2 + 1);
+            if constexpr (XMX && kMode == kEven) scales_load(t / 2 + 1);
+          }
+          read_first(next, ahead, t + 1);
         }
-        x[q % kRing] = read_x(slot ^ 1, i + kAhead - MB, 0);
+        x[q % kRing] = read_x(ahead, i + kAhead - MB, 0);
+        constexpr int from = (i + kAhead - MB) * kPerBlock;
+        if constexpr (kMode != kAny) issue(t + RING, place, from, from + kPerBlock, std::true_type{});
+        else if (t + RING < tiles) issue(t + RING, place, from, from + kPerBlock, std::false_type{});
       }
       multiply(second, I, w1);
       __builtin_amdgcn_sched_barrier(0);
     });
-    if constexpr (kMode != kLast) sc = next;
+    if constexpr (kMode != kLast) {
+      sc = next;
+      where = ahead;
+    }
   };
 
-  scales_load(0, std::false_type{});
+  issue(0, 0, 0, DMAS, std::false_type{});
+  scales_load_end(0);
   scales_store(0);
-  issue(0, 0, std::false_type{});
-  wait_all_barrier();
-  if (tiles > 1) issue(1, 1, std::false_type{});
-  read_first(sc, 0);
+  wait_dma_barrier<0>();
+#pragma unroll
+  for (int j = 1; j < RING; ++j)
+    if (j < tiles) issue(j, j, 0, j + 1 < RING ? DMAS : kEarly, std::false_type{});
+  read_first(sc, 0, 0);
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) x[i] = read_x(0, i, 0);
   int t = 0;
-  if (all_rows) {
-    for (; (t + 4) * KB <= nblk; t += 2) {
+  if (all_rows && (XMX || dma_scales)) {
+    // tile t + 1 sends for tile t + 1 + RING, tile t for the scales of t + 2 and t + 3
+    for (; (t + 2 + RING) * KB <= nblk; t += 2) {
       tile(t, std::integral_constant<int, kEven>{});
       tile(t + 1, std::integral_constant<int, kOdd>{});
     }
@@ -528,6 +701,10 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
     const int row = (wm * MB + i) * 16 + r;
     if (row > m_last) continue;
     const int64_t m = m0 + row;
+    if (p.row_ids && !(p.row_ids[m] >= 0 && p.row_ids[m] < p.num_ids)) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
     if (p.silu_mul) {
 #pragma unroll
       for (int j = 0; j < NB; j += 2) {
@@ -555,41 +732,46 @@ static hipError_t tiled(const Mx4Gemm& p, hipStream_t stream) {
   while (pn > n_tiles) pn /= 2;
   const int64_t n_patches = ceil_div(n_tiles, pn);
   const int64_t patches = ceil_div(m_tiles, 32 / pn) * n_patches;
+  const bool dma_scales = p.K % 128 == 0 && reinterpret_cast<uintptr_t>(p.w_scale) % 4 == 0;
   const auto kernel = mx4_tile_kernel<XMX, TM>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(ceil_div(patches, 8) * 256)), dim3(512), 0,
-                     stream, p, (int)m_tiles, (int)n_tiles, pn, (int)n_patches);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(ceil_div(patches, 8) * 256)), dim3(512), 0, stream, p,
+                     (int)m_tiles, (int)n_tiles, pn, (int)n_patches, (int)dma_scales);
   return hipGetLastError();
 }
 
-template <bool XMX, int MB, int NB, int WV>
+template <bool XMX, int MB, int NB, int GB, int WV>
 static hipError_t stream(const Mx4Gemm& p, hipStream_t stream) {
-  const int64_t col_groups = ceil_div(p.N / 16, NB);
-  const int64_t blocks = ceil_div(p.M, 16 * MB) * col_groups;
-  hipLaunchKernelGGL((mx4_stream_kernel<XMX, MB, NB, WV>), dim3((unsigned)blocks), dim3(64 * WV),
-                     (size_t)WV * MB * NB * 64 * sizeof(floatx4), stream, p, (int)col_groups);
+  const int64_t col_groups = ceil_div(p.N / 16, NB), row_groups = ceil_div(p.M, 16 * MB);
+  const bool spread = row_groups >= 32;
+  const size_t staged = p.K <= kStageK ? (size_t)(NB + (XMX ? MB : 0)) * 16 * (p.K / 32) : 0;
+  const auto kernel = mx4_stream_kernel<XMX, MB, NB, GB, WV>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((spread ? round_up(row_groups, 16) : row_groups) * col_groups)),
+                     dim3(64 * WV), staged, stream, p, (int)row_groups, (int)col_groups, (int)spread);
   return hipGetLastError();
+}
+
+// a workgroup of 4 waves and 16 NB columns, or, where those would not fill the chip,
+// of WIDE waves and 32 columns
+template <bool XMX, int MB, int NB, int WIDE>
+static hipError_t few(const Mx4Gemm& p, hipStream_t s) {
+  if (ceil_div(p.M, 16 * MB) * ceil_div(p.N, 16 * NB) >= FEWG) return stream<XMX, MB, NB, 8, 4>(p, s);
+  return stream<XMX, MB, 2, 8, WIDE>(p, s);
+}
+
+template <bool XMX>
+static hipError_t product(const Mx4Gemm& p, hipStream_t s) {
+  // rows of a workgroup: within one tile_expert entry, or those there are
+  const int64_t rows = p.tile_expert ? p.BM : p.M;
+  auto takes = [&](int64_t n) { return p.tile_expert ? rows % n == 0 : rows > n / 2; };
+  if (takes(256)) return tiled<XMX, 256>(p, s);
+  if (takes(128)) return tiled<XMX, 128>(p, s);
+  if (takes(64)) return few<XMX, 4, 2, 8>(p, s);
+  if (takes(32)) return few<XMX, 2, 4, 8>(p, s);
+  return few<XMX, 1, 4, 16>(p, s);
 }
 
 hipError_t launch_mx4_gemm(const Mx4Gemm& p, hipStream_t s) {
-  // rows of a workgroup: within one tile_expert entry
-  const int64_t rows = p.tile_expert ? p.BM : p.M;
-  const bool r64 = p.tile_expert ? rows % 64 == 0 : rows > 32;
-  const bool r32 = p.tile_expert ? rows % 32 == 0 : rows > 16;
-  // whole tiles of 128 rows and more
-  const bool r256 = p.tile_expert ? rows % 256 == 0 : rows > 128;
-  const bool r128 = p.tile_expert ? rows % 128 == 0 : rows > 64;
-  if (p.x_mx4) {
-    if (r256) return tiled<true, 256>(p, s);
-    if (r128) return tiled<true, 128>(p, s);
-    if (r64) return stream<true, 4, 2, 4>(p, s);
-    if (r32) return stream<true, 2, 4, 4>(p, s);
-    return stream<true, 1, 4, 4>(p, s);
-  }
-  if (r256) return tiled<false, 256>(p, s);
-  if (r128) return tiled<false, 128>(p, s);
-  if (r64) return stream<false, 4, 2, 4>(p, s);
-  if (r32) return stream<false, 2, 4, 4>(p, s);
-  return stream<false, 1, 4, 4>(p, s);
+  return p.x_mx4 ? product<true>(p, s) : product<false>(p, s);
 }
 
 }  // namespace moelora

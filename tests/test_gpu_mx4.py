@@ -233,6 +233,37 @@ def test_rows_do_not_reach_other_rows(kind, bm):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mx4"])
+@pytest.mark.parametrize("bm", [16, 32, 64, 128, 256])
+def test_padding_rows_are_not_read(kind, bm):
+    """With pair_rows in the layout the padding rows (NaN here) give zeros, the other
+    rows the same bits as without it, and rows behind the last tile are untouched."""
+    T, k, E, N, K = 90, 2, 5, 160, 544
+    say(f"padding rows {kind} block_m {bm}")
+    g = torch.Generator().manual_seed(15)
+    ids = torch.stack([torch.randperm(E - 1, generator=g)[:k] for _ in range(T)]).int().cuda()
+    al = binding.moe_lora_align(ids, torch.full((T,), -1, dtype=torch.int32, device="cuda"), None, E, 0,
+                                bm, pair_rows=True)
+    used, M = int(al["num_rows_padded"].cpu()[0]), al["capacity"]
+    assert used < M
+    sid = al["sorted_pair_ids"]
+    pad = (sid >= T * k).clone()
+    wc, ws, w64 = weights(E, N, K, 16)
+    x, xs, x64 = activations(M, K, kind, 17)
+    (x if kind == "bf16" else xs)[pad] = torch.tensor(float("nan")).bfloat16() if kind == "bf16" else 255
+    plain = {n: al[n] for n in ("block_m", "tile_expert")}
+    row_expert = al["tile_expert"].cpu().numpy().repeat(bm)[:M]
+    row_expert = np.where(pad.cpu().numpy(), -1, row_expert)
+    for silu in (False, True):
+        mark = torch.full((M, N // 2 if silu else N), -9.5, dtype=torch.float32, device="cuda")
+        y = binding.moe_lora_mx4_gemm(x, wc, ws, x_scales=xs, align_out=al, silu_mul=silu, out=mark.clone())
+        check_product(np64(y), torch.float32, x64, w64, row_expert, silu, K, f"silu {silu}")
+        assert bool((y[:used][pad[:used]] == 0).all())
+        assert torch.equal(y[used:], mark[used:])
+        z = binding.moe_lora_mx4_gemm(x, wc, ws, x_scales=xs, align_out=plain, silu_mul=silu, out=mark.clone())
+        assert torch.equal(y[~pad], z[~pad])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mx4"])
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_extreme_scales(kind, M):
     """Scales at both ends of the e8m0 range; sums stay in fp32's."""

@@ -161,6 +161,9 @@ def test_gemm_codes():
     assert call(block_m=24) == INVALID
     assert call(num_rows=72) == INVALID                      # not whole tiles
     assert call(tile_expert=None) == INVALID                 # four experts, no tiles
+    assert call(tile_expert=None, num_experts=1, sorted_pair_ids=0x1000) == INVALID
+    assert call(sorted_pair_ids=0x1000, num_pairs=-1) == INVALID
+    assert call(in_features=1 << 20, out_features=1 << 17) == UNSUPPORTED   # scales of 4 GiB
     for n in ("x", "x_scale", "w", "w_scale", "out"):
         assert call(**{n: None}) == INVALID, n
     for n in ("x", "w", "out"):
