@@ -365,8 +365,8 @@ int moe_lora_permute(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t 
   if (!rows || (num_tokens > 0 && !x)) return MOE_LORA_ERR_INVALID;
   if (dtype != MOE_LORA_U8 && (off_by_element(x, dtype) || off_by_element(rows, dtype)))
     return MOE_LORA_ERR_INVALID;
-  const int64_t esz = dtype == MOE_LORA_F32 ? 4 : dtype == MOE_LORA_BF16 ? 2 : 1;
-  return hip_status(launch_permute(l, hidden * esz, x, rows, static_cast<hipStream_t>(stream)));
+  const int esz = dtype == MOE_LORA_F32 ? 4 : dtype == MOE_LORA_BF16 ? 2 : 1;
+  return hip_status(launch_permute(l, hidden, esz, x, rows, static_cast<hipStream_t>(stream)));
 }
 
 int moe_lora_unpermute(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t dtype,

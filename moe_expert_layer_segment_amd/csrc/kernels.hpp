@@ -53,9 +53,9 @@ struct RowsLayout {
   int64_t num_rows;                  // rows the buffers hold
   const int32_t *sorted_ids, *pair_rows, *num_rows_padded;
 };
-// rows[pair_rows[t k + j]] = x[t] (row_bytes bytes each); pads are zeroed
-hipError_t launch_permute(const RowsLayout& l, int64_t row_bytes, const void* x, void* rows,
-                          hipStream_t stream);
+// rows[pair_rows[t k + j]] = x[t] (elements of 1, 2 or 4 bytes); pads are zeroed
+hipError_t launch_permute(const RowsLayout& l, int64_t hidden, int elem_bytes, const void* x,
+                          void* rows, hipStream_t stream);
 // y[t] = sum_j weights[t k + j] rows[pair_rows[t k + j]] (weights null: ones)
 hipError_t launch_unpermute(const RowsLayout& l, int64_t hidden, bool rows_f32, bool y_f32,
                             const void* rows, const float* weights, void* y, hipStream_t stream);

@@ -26,12 +26,31 @@ static constexpr int kPadRows = 16;   // rows of the layout a pad block looks at
 static constexpr int64_t kTokenBlocks = int64_t(1) << 22;
 static constexpr int64_t kPadBlocks = int64_t(1) << 20;
 
-template <typename T, int V> struct Vec { typedef T type __attribute__((ext_vector_type(V))); };
+// V elements at any address aligned to one of them: global memory is read and written
+// 16 bytes at a time whatever the alignment, so rows of odd lengths go the same way.
+// ONCE: what is touched once, the rows that unpermute reads and the tokens it writes,
+// goes past the caches (fp32 rows of 8192 x 8 tokens, 2048 wide: 136 -> 93 us; the
+// stores of the other direction gain nothing, its loads lose 10%).
+template <typename T, int V> struct Vec {
+  typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+};
 template <typename T> struct Vec<T, 1> { typedef T type; };
 
-template <typename T, int V>
+template <typename T, int V, bool ONCE = false>
+__device__ __forceinline__ typename Vec<T, V>::type load_vec(const T* p) {
+  const typename Vec<T, V>::type* from = reinterpret_cast<const typename Vec<T, V>::type*>(p);
+  if constexpr (ONCE) return __builtin_nontemporal_load(from);
+  else return *from;
+}
+template <typename T, int V, bool ONCE = false>
+__device__ __forceinline__ void store_vec(T* p, typename Vec<T, V>::type v) {
+  typename Vec<T, V>::type* to = reinterpret_cast<typename Vec<T, V>::type*>(p);
+  if constexpr (ONCE) __builtin_nontemporal_store(v, to);
+  else *to = v;
+}
+template <typename T, int V, bool ONCE = false>
 __device__ __forceinline__ void load_floats(const T* p, float (&v)[V]) {
-  const typename Vec<T, V>::type x = *reinterpret_cast<const typename Vec<T, V>::type*>(p);
+  const auto x = load_vec<T, V, ONCE>(p);
   if constexpr (V == 1) {
     v[0] = (float)x;
   } else {
@@ -39,7 +58,7 @@ __device__ __forceinline__ void load_floats(const T* p, float (&v)[V]) {
     for (int i = 0; i < V; ++i) v[i] = (float)x[i];
   }
 }
-template <typename T, int V>
+template <typename T, int V, bool ONCE = false>
 __device__ __forceinline__ void store_floats(T* p, const float (&v)[V]) {
   typename Vec<T, V>::type x;
   if constexpr (V == 1) {
@@ -48,26 +67,41 @@ __device__ __forceinline__ void store_floats(T* p, const float (&v)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = (T)v[i];
   }
-  *reinterpret_cast<typename Vec<T, V>::type*>(p) = x;
+  store_vec<T, V, ONCE>(p, x);
+}
+// 16 bytes of the rows to a thread; rows shorter than that, element by element
+template <typename T> constexpr int kWide = 16 / (int)sizeof(T);
+
+// A row of n elements is taken V at a time; the last piece of a row that V does not
+// divide starts early, and repeats elements of the one before.
+template <int V>
+__device__ __forceinline__ int64_t piece_at(int64_t u, int64_t n) {
+  return min(u * V, n - V);
 }
 
-// Zeroes units [u0, u1) of the pad rows: rows before *num_rows_padded whose entry
+// Zeroes pieces [u0, u1) of the pad rows: rows before *num_rows_padded whose entry
 // names no pair, kPadRows rows of the layout per block at a time.  Rows behind it
 // are not touched.
-template <typename U>
+template <typename T, int V>
 __device__ __forceinline__ void zero_pads(const RowsLayout& l, int64_t block, int64_t blocks,
-                                          int64_t units, int64_t u0, int64_t u1,
-                                          U* __restrict__ rows) {
+                                          int64_t n, int64_t u0, int64_t u1, T* __restrict__ rows) {
   const int64_t used = min((int64_t)l.num_rows_padded[0], l.num_rows);
   const int64_t pairs = (int64_t)l.T * l.k;
   constexpr int kPerWave = kPadRows / (kRowThreads / 64);
   for (int64_t r0 = block * kPadRows; r0 < used; r0 += blocks * kPadRows) {
+    bool pad[kPerWave];
+#pragma unroll
     for (int i = 0; i < kPerWave; ++i) {
       const int64_t r = r0 + (threadIdx.x >> 6) * kPerWave + i;
-      if (r >= used) break;
-      const int32_t id = l.sorted_ids[r];
-      if (id >= 0 && id < pairs) continue;
-      for (int64_t u = u0 + (threadIdx.x & 63); u < u1; u += 64) rows[r * units + u] = U{};
+      const int32_t id = l.sorted_ids[min(r, used - 1)];
+      pad[i] = r < used && (id < 0 || id >= pairs);
+    }
+#pragma unroll
+    for (int i = 0; i < kPerWave; ++i) {
+      const int64_t r = r0 + (threadIdx.x >> 6) * kPerWave + i;
+      if (!pad[i]) continue;
+      for (int64_t u = u0 + (threadIdx.x & 63); u < u1; u += 64)
+        store_vec<T, V>(rows + r * n + piece_at<V>(u, n), typename Vec<T, V>::type{});
     }
   }
 }
@@ -80,45 +114,59 @@ static unsigned pad_blocks(const RowsLayout& l) {
 }
 
 // Blocks [0, tblocks): a token each; blocks behind them: the pads.  blockIdx.y
-// takes kRowThreads * PER units of the row.
-template <typename U, int PER>
+// takes kRowThreads * PER pieces of the row.
+template <typename T, int V, int PER>
 __global__ void __launch_bounds__(kRowThreads)
-permute_kernel(RowsLayout l, unsigned tblocks, int64_t units, const U* __restrict__ x,
-               U* __restrict__ rows) {
+permute_kernel(RowsLayout l, unsigned tblocks, int64_t n, const T* __restrict__ x,
+               T* __restrict__ rows) {
+  const int64_t units = (n + V - 1) / V;
   const int64_t u0 = (int64_t)blockIdx.y * (kRowThreads * PER);
   if (blockIdx.x >= tblocks) {
-    zero_pads<U>(l, blockIdx.x - tblocks, gridDim.x - tblocks, units, u0,
-                 min(units, u0 + (int64_t)kRowThreads * PER), rows);
+    zero_pads<T, V>(l, blockIdx.x - tblocks, gridDim.x - tblocks, n, u0,
+                    min(units, u0 + (int64_t)kRowThreads * PER), rows);
     return;
   }
   for (int64_t t = blockIdx.x; t < l.T; t += tblocks) {
-    U v[PER];
+    typename Vec<T, V>::type v[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int64_t u = u0 + i * kRowThreads + threadIdx.x;
-      v[i] = u < units ? x[t * units + u] : U{};
+      v[i] = {};
+      if (u < units) v[i] = load_vec<T, V>(x + t * n + piece_at<V>(u, n));
     }
-    for (int j = 0; j < l.k; ++j) {
-      const int64_t r = l.pair_rows[t * l.k + j];
-      if (r < 0 || r >= l.num_rows) continue;
+    // the pairs' rows are read ahead of the stores: for all the compiler knows these could
+    // change them, and each would wait for the one before
+    constexpr int kRowsAtOnce = 8;
+    for (int j0 = 0; j0 < l.k; j0 += kRowsAtOnce) {
+      int64_t to[kRowsAtOnce];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int64_t u = u0 + i * kRowThreads + threadIdx.x;
-        if (u < units) rows[r * units + u] = v[i];
+      for (int q = 0; q < kRowsAtOnce; ++q) {
+        const int64_t r = l.pair_rows[t * l.k + min(j0 + q, l.k - 1)];
+        to[q] = j0 + q < l.k && r < l.num_rows ? r : -1;
+      }
+#pragma unroll
+      for (int q = 0; q < kRowsAtOnce; ++q) {
+        if (to[q] < 0) continue;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int64_t u = u0 + i * kRowThreads + threadIdx.x;
+          if (u < units) store_vec<T, V>(rows + to[q] * n + piece_at<V>(u, n), v[i]);
+        }
       }
     }
   }
 }
 
-// One unit of V columns per thread; a token's rows are loaded kRowsAtOnce at a
-// time, all in flight before the first is added.
+// V columns per thread; a token's rows are loaded kRowsAtOnce at a time, all in flight
+// before the first is added.
 template <typename TR, typename TY, int V>
 __global__ void __launch_bounds__(kRowThreads)
 unpermute_kernel(RowsLayout l, int64_t hidden, const TR* __restrict__ rows,
                  const float* __restrict__ weights, TY* __restrict__ y) {
   constexpr int kRowsAtOnce = 8;
-  const int64_t c = ((int64_t)blockIdx.y * kRowThreads + threadIdx.x) * V;
+  int64_t c = ((int64_t)blockIdx.y * kRowThreads + threadIdx.x) * V;
   if (c >= hidden) return;
+  c = min(c, hidden - V);   // the last piece of an odd row repeats columns
   for (int64_t t = blockIdx.x; t < l.T; t += gridDim.x) {
     float acc[V];
 #pragma unroll
@@ -135,7 +183,7 @@ unpermute_kernel(RowsLayout l, int64_t hidden, const TR* __restrict__ rows,
           const int64_t r = l.pair_rows[p];
           live[q] = r >= 0 && r < l.num_rows;
           w[q] = weights ? weights[p] : 1.0f;
-          if (live[q]) load_floats<TR, V>(rows + r * hidden + c, z[q]);
+          if (live[q]) load_floats<TR, V, true>(rows + r * hidden + c, z[q]);
         }
       }
 #pragma unroll
@@ -145,7 +193,7 @@ unpermute_kernel(RowsLayout l, int64_t hidden, const TR* __restrict__ rows,
           for (int i = 0; i < V; ++i) acc[i] = fmaf(w[q], z[q][i], acc[i]);
         }
     }
-    store_floats<TY, V>(y + t * hidden + c, acc);
+    store_floats<TY, V, true>(y + t * hidden + c, acc);
   }
 }
 
@@ -160,9 +208,8 @@ unpermute_backward_kernel(RowsLayout l, unsigned tblocks, int64_t hidden, const 
   constexpr int kWaves = kRowThreads / 64;
   __shared__ float part[kWaves][kRowsAtOnce];
   if (blockIdx.x >= tblocks) {
-    zero_pads<typename Vec<TR, V>::type>(l, blockIdx.x - tblocks, gridDim.x - tblocks, hidden / V,
-                                         0, hidden / V,
-                                         reinterpret_cast<typename Vec<TR, V>::type*>(d_rows));
+    zero_pads<TR, V>(l, blockIdx.x - tblocks, gridDim.x - tblocks, hidden, 0, (hidden + V - 1) / V,
+                     d_rows);
     return;
   }
   for (int64_t t = blockIdx.x; t < l.T; t += tblocks) {
@@ -181,22 +228,28 @@ unpermute_backward_kernel(RowsLayout l, unsigned tblocks, int64_t hidden, const 
           if (weights) w[q] = weights[p];
         }
       }
-      for (int64_t c = (int64_t)threadIdx.x * V; c < hidden; c += kRowThreads * V) {
-        float g[V];
+      for (int64_t c0 = (int64_t)threadIdx.x * V; c0 < hidden; c0 += kRowThreads * V) {
+        const int64_t c = min(c0, hidden - V);
+        float g[V], z[kRowsAtOnce][V];
         load_floats<TY, V>(dy + t * hidden + c, g);
+        if (d_weights) {
+#pragma unroll
+          for (int q = 0; q < kRowsAtOnce; ++q)
+            if (at[q] >= 0) load_floats<TR, V>(rows + at[q] + c, z[q]);
+        }
 #pragma unroll
         for (int q = 0; q < kRowsAtOnce; ++q) {
           if (at[q] < 0) continue;
-          if (d_weights) {
-            float z[V];
-            load_floats<TR, V>(rows + at[q] + c, z);
-#pragma unroll
-            for (int i = 0; i < V; ++i) dot[q] = fmaf(g[i], z[i], dot[q]);
-          }
           float d[V];
 #pragma unroll
           for (int i = 0; i < V; ++i) d[i] = w[q] * g[i];
           store_floats<TR, V>(d_rows + at[q] + c, d);
+          if (d_weights) {
+            // columns that the last piece repeats are counted once
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if (V == 1 || c + i >= c0) dot[q] = fmaf(g[i], z[q][i], dot[q]);
+          }
         }
       }
       if (!d_weights) continue;
@@ -218,59 +271,54 @@ unpermute_backward_kernel(RowsLayout l, unsigned tblocks, int64_t hidden, const 
   }
 }
 
-static bool aligned(const void* p, int64_t bytes) {
-  return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0;
+template <typename T>
+static void permute_elements(const RowsLayout& l, int64_t n, const void* x, void* rows,
+                             hipStream_t stream) {
+  auto go = [&](auto v, auto per) {
+    constexpr int V = decltype(v)::value, PER = decltype(per)::value;
+    const dim3 grid(token_blocks(l) + pad_blocks(l), (unsigned)ceil_div(n, V * kRowThreads * PER));
+    hipLaunchKernelGGL((permute_kernel<T, V, PER>), grid, dim3(kRowThreads), 0, stream, l,
+                       token_blocks(l), n, static_cast<const T*>(x), static_cast<T*>(rows));
+  };
+  if (n >= kWide<T>) go(std::integral_constant<int, kWide<T>>{}, std::integral_constant<int, 4>{});
+  else go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
 }
 
-template <typename U>
-static void permute_units(const RowsLayout& l, int64_t units, const void* x, void* rows,
-                          hipStream_t stream) {
-  constexpr int PER = 4;
-  const dim3 grid(token_blocks(l) + pad_blocks(l), (unsigned)ceil_div(units, kRowThreads * PER));
-  hipLaunchKernelGGL((permute_kernel<U, PER>), grid, dim3(kRowThreads), 0, stream, l,
-                     token_blocks(l), units, static_cast<const U*>(x), static_cast<U*>(rows));
-}
-
-hipError_t launch_permute(const RowsLayout& l, int64_t row_bytes, const void* x, void* rows,
-                          hipStream_t stream) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  if (row_bytes % 16 == 0 && aligned(x, 16) && aligned(rows, 16))
-    permute_units<u32x4>(l, row_bytes / 16, x, rows, stream);
-  else if (row_bytes % 4 == 0 && aligned(x, 4) && aligned(rows, 4))
-    permute_units<uint32_t>(l, row_bytes / 4, x, rows, stream);
-  else if (row_bytes % 2 == 0 && aligned(x, 2) && aligned(rows, 2))
-    permute_units<uint16_t>(l, row_bytes / 2, x, rows, stream);
-  else
-    permute_units<uint8_t>(l, row_bytes, x, rows, stream);
+hipError_t launch_permute(const RowsLayout& l, int64_t hidden, int elem_bytes, const void* x,
+                          void* rows, hipStream_t stream) {
+  if (elem_bytes == 4) permute_elements<uint32_t>(l, hidden, x, rows, stream);
+  else if (elem_bytes == 2) permute_elements<uint16_t>(l, hidden, x, rows, stream);
+  else permute_elements<uint8_t>(l, hidden, x, rows, stream);
   return hipGetLastError();
 }
 
-// f(TR{}, TY{}) for the element types of the rows and of the tokens
+// f(TR{}, TY{}, V) for the element types of the rows and of the tokens, and the columns
+// that a thread takes
 template <typename F>
-static void for_types(bool rows_f32, bool y_f32, F&& f) {
+static void for_types(bool rows_f32, bool y_f32, int64_t hidden, F&& f) {
+  auto width = [&](auto tr, auto ty) {
+    constexpr int V = kWide<decltype(tr)>;
+    if (hidden >= V) f(tr, ty, std::integral_constant<int, V>{});
+    else f(tr, ty, std::integral_constant<int, 1>{});
+  };
   if (rows_f32) {
-    if (y_f32) f(float{}, float{});
-    else f(float{}, bf16_t{});
+    if (y_f32) width(float{}, float{});
+    else width(float{}, bf16_t{});
   } else {
-    if (y_f32) f(bf16_t{}, float{});
-    else f(bf16_t{}, bf16_t{});
+    if (y_f32) width(bf16_t{}, float{});
+    else width(bf16_t{}, bf16_t{});
   }
 }
 
 hipError_t launch_unpermute(const RowsLayout& l, int64_t hidden, bool rows_f32, bool y_f32,
                             const void* rows, const float* weights, void* y, hipStream_t stream) {
-  const bool wide = hidden % 8 == 0 && aligned(rows, 16) && aligned(y, 16);
-  for_types(rows_f32, y_f32, [&](auto tr, auto ty) {
+  for_types(rows_f32, y_f32, hidden, [&](auto tr, auto ty, auto v) {
     using TR = decltype(tr);
     using TY = decltype(ty);
-    auto go = [&](auto v) {
-      constexpr int V = decltype(v)::value;
-      const dim3 grid(token_blocks(l), (unsigned)ceil_div(hidden, kRowThreads * V));
-      hipLaunchKernelGGL((unpermute_kernel<TR, TY, V>), grid, dim3(kRowThreads), 0, stream, l,
-                         hidden, static_cast<const TR*>(rows), weights, static_cast<TY*>(y));
-    };
-    if (wide) go(std::integral_constant<int, 8>{});
-    else go(std::integral_constant<int, 1>{});
+    constexpr int V = decltype(v)::value;
+    const dim3 grid(token_blocks(l), (unsigned)ceil_div(hidden, kRowThreads * V));
+    hipLaunchKernelGGL((unpermute_kernel<TR, TY, V>), grid, dim3(kRowThreads), 0, stream, l, hidden,
+                       static_cast<const TR*>(rows), weights, static_cast<TY*>(y));
   });
   return hipGetLastError();
 }
@@ -279,20 +327,14 @@ hipError_t launch_unpermute_backward(const RowsLayout& l, int64_t hidden, bool r
                                      bool dy_f32, const void* dy, const void* rows,
                                      const float* weights, void* d_rows, float* d_weights,
                                      hipStream_t stream) {
-  const bool wide = hidden % 8 == 0 && aligned(dy, 16) && aligned(d_rows, 16) &&
-                    (!d_weights || aligned(rows, 16));
-  for_types(rows_f32, dy_f32, [&](auto tr, auto ty) {
+  for_types(rows_f32, dy_f32, hidden, [&](auto tr, auto ty, auto v) {
     using TR = decltype(tr);
     using TY = decltype(ty);
-    auto go = [&](auto v) {
-      constexpr int V = decltype(v)::value;
-      const dim3 grid(token_blocks(l) + pad_blocks(l));
-      hipLaunchKernelGGL((unpermute_backward_kernel<TR, TY, V>), grid, dim3(kRowThreads), 0, stream,
-                         l, token_blocks(l), hidden, static_cast<const TY*>(dy),
-                         static_cast<const TR*>(rows), weights, static_cast<TR*>(d_rows), d_weights);
-    };
-    if (wide) go(std::integral_constant<int, 8>{});
-    else go(std::integral_constant<int, 1>{});
+    constexpr int V = decltype(v)::value;
+    const dim3 grid(token_blocks(l) + pad_blocks(l));
+    hipLaunchKernelGGL((unpermute_backward_kernel<TR, TY, V>), grid, dim3(kRowThreads), 0, stream, l,
+                       token_blocks(l), hidden, static_cast<const TY*>(dy),
+                       static_cast<const TR*>(rows), weights, static_cast<TR*>(d_rows), d_weights);
   });
   return hipGetLastError();
 }
