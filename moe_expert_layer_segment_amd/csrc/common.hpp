@@ -103,16 +103,19 @@ __device__ inline float silu_f(float v) {
   return v * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// MX4: the value 2^(b - 127) of an e8m0 scale byte (255: NaN; 0: 2^-127, below
-// the smallest normal float), and the value of the e2m1 code in the low 4 bits.
-__device__ inline float mx4_scale(uint32_t b) {
-  return __builtin_bit_cast(float, b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
-}
-__device__ inline float e2m1_value(uint32_t c) {
-  // twice the magnitudes of codes 0..7, one nibble each
-  const uint32_t twice = (0xC8643210u >> (4 * (c & 7))) & 15u;
-  const float m = 0.5f * (float)twice;
-  return (c & 8) ? -m : m;
+// MX4: the 8 values of a word of e2m1 codes, the first in the low 4 bits, times `scale`,
+// of which the hardware reads the exponent alone (a field of 0 is 2^-127, of 255 NaN).
+// Exact, but for magnitudes past the largest finite value, which become infinities.
+typedef bf16_t bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ bf16x8 mx4_bf16x8(uint32_t w, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+  bf16x8 v;
+  v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
+  v[4] = c[0]; v[5] = c[1]; v[6] = d[0]; v[7] = d[1];
+  return v;
 }
 
 __device__ inline int lane_id() { return threadIdx.x & 63; }

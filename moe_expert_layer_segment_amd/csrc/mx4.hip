@@ -19,8 +19,10 @@ namespace moelora {
 
 static constexpr int kMxThreads = 256;
 
-// 8 consecutive values per lane, so 4 lanes share a block
-template <typename T>
+// 8 consecutive values per lane, so 4 lanes share a block.  A thread takes kUnits such
+// units kMxThreads apart, all loaded before the first is worked on: one where they would
+// not fill the chip otherwise, four else.
+template <typename T, int kUnits>
 __global__ void __launch_bounds__(kMxThreads)
 mx4_quantize_kernel(int64_t num_rows, int64_t cols, const T* __restrict__ x,
                     const int32_t* __restrict__ rows_used, uint32_t* __restrict__ codes,
@@ -28,63 +30,106 @@ mx4_quantize_kernel(int64_t num_rows, int64_t cols, const T* __restrict__ x,
   typedef T tx8 __attribute__((ext_vector_type(8)));
   const int64_t rows = rows_used ? min((int64_t)max(rows_used[0], 0), num_rows) : num_rows;
   const int64_t n = rows * cols / 8;
-  const int64_t step = (int64_t)gridDim.x * kMxThreads;
-  // n and step are multiples of 4: the four lanes of a block stay together
-  for (int64_t i = (int64_t)blockIdx.x * kMxThreads + threadIdx.x; i < n; i += step) {
-    const tx8 v = reinterpret_cast<const tx8*>(x)[i];
-    // magnitudes compare as integers: finite < infinity < NaN
-    uint32_t a = 0;
+  // n is a multiple of 4: the four lanes of a block stay together
+  for (int64_t base = (int64_t)blockIdx.x * (kMxThreads * kUnits); base < n;
+       base += (int64_t)gridDim.x * (kMxThreads * kUnits)) {
+    tx8 v[kUnits];
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      a = max(a, __builtin_bit_cast(uint32_t, (float)v[q]) & 0x7FFFFFFFu);
-    a = max(a, (uint32_t)__shfl_xor((int)a, 1, 64));
-    a = max(a, (uint32_t)__shfl_xor((int)a, 2, 64));
-    const uint32_t field = a >> 23;
-    const uint32_t b = field == 255 ? 255u : field > 2 ? field - 2 : 0u;
-    const float scale = __builtin_bit_cast(float, b << 23);
-    uint32_t c = 0;
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, (float)v[0], (float)v[1], scale, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, (float)v[2], (float)v[3], scale, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, (float)v[4], (float)v[5], scale, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, (float)v[6], (float)v[7], scale, 3);
-    codes[i] = b == 255 ? 0u : c;
-    if ((i & 3) == 0) scales[i >> 2] = (uint8_t)b;
+    for (int u = 0; u < kUnits; ++u) {
+      const int64_t i = base + u * kMxThreads + threadIdx.x;
+      if (i < n) v[u] = reinterpret_cast<const tx8*>(x)[i];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int64_t i = base + u * kMxThreads + threadIdx.x;
+      if (i >= n) break;
+      float f[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[q] = (float)v[u][q];
+      // magnitudes compare as integers: finite < infinity < NaN
+      uint32_t a = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) a = max(a, __builtin_bit_cast(uint32_t, f[q]) & 0x7FFFFFFFu);
+      a = max(a, (uint32_t)__shfl_xor((int)a, 1, 64));
+      a = max(a, (uint32_t)__shfl_xor((int)a, 2, 64));
+      const uint32_t field = a >> 23;
+      const uint32_t b = field == 255 ? 255u : field > 2 ? field - 2 : 0u;
+      const float scale = __builtin_bit_cast(float, b << 23);   // read by its exponent: 0 is 2^-127
+      uint32_t c = 0;
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[0], f[1], scale, 0);
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[2], f[3], scale, 1);
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[4], f[5], scale, 2);
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[6], f[7], scale, 3);
+      codes[i] = b == 255 ? 0u : c;
+      if ((i & 3) == 0) scales[i >> 2] = (uint8_t)b;
+    }
   }
 }
 
 // 8 values (one word of codes) per lane
-template <typename T>
+template <typename T, int kUnits>
 __global__ void __launch_bounds__(kMxThreads)
 mx4_dequantize_kernel(int64_t n, const uint32_t* __restrict__ codes,
                       const uint8_t* __restrict__ scales, T* __restrict__ out) {
   typedef T tx8 __attribute__((ext_vector_type(8)));
-  const int64_t step = (int64_t)gridDim.x * kMxThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kMxThreads + threadIdx.x; i < n; i += step) {
-    const uint32_t c = codes[i];
-    const float scale = mx4_scale(scales[i >> 2]);
-    tx8 v;
+  for (int64_t base = (int64_t)blockIdx.x * (kMxThreads * kUnits); base < n;
+       base += (int64_t)gridDim.x * (kMxThreads * kUnits)) {
+    uint32_t c[kUnits], b[kUnits];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = (T)(e2m1_value(c >> (4 * q)) * scale);
-    reinterpret_cast<tx8*>(out)[i] = v;
+    for (int u = 0; u < kUnits; ++u) {
+      const int64_t i = base + u * kMxThreads + threadIdx.x;
+      if (i < n) {
+        c[u] = codes[i];
+        b[u] = scales[i >> 2];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int64_t i = base + u * kMxThreads + threadIdx.x;
+      if (i >= n) break;
+      // read by its exponent: 0 is 2^-127, 255 NaN
+      const float scale = __builtin_bit_cast(float, b[u] << 23);
+      tx8 v;
+      if constexpr (sizeof(T) == 2) {
+        v = mx4_bf16x8(c[u], scale);
+      } else {
+        static_for<4>([&](auto Q) {
+          constexpr int q = decltype(Q)::value;
+          const auto two = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], scale, q);
+          v[2 * q] = two[0];
+          v[2 * q + 1] = two[1];
+        });
+      }
+      reinterpret_cast<tx8*>(out)[i] = v;
+    }
   }
 }
 
-static unsigned mx4_grid(int64_t n) {
-  return (unsigned)std::min<int64_t>(ceil_div(n, kMxThreads), 256 * 32);
+// go(kernel of one or of four units, its blocks): all units at once up to 2^20 blocks
+// (threads of a launch are counted in 32 bits), round by round behind that
+template <typename F>
+static void for_units(int64_t n, F&& go) {
+  if (n < int64_t(4) * kMxThreads * 256 * 8) {
+    go(std::integral_constant<int, 1>{}, dim3((unsigned)ceil_div(n, kMxThreads)));
+  } else {
+    go(std::integral_constant<int, 4>{},
+       dim3((unsigned)std::min<int64_t>(ceil_div(n, 4 * kMxThreads), int64_t(1) << 20)));
+  }
 }
 
 hipError_t launch_mx4_quantize(bool x_f32, int64_t num_rows, int64_t cols, const void* x,
                                const int32_t* rows_used, uint8_t* codes, uint8_t* scales,
                                hipStream_t stream) {
-  const dim3 grid(mx4_grid(num_rows * cols / 8)), block(kMxThreads);
-  if (x_f32)
-    hipLaunchKernelGGL(mx4_quantize_kernel<float>, grid, block, 0, stream, num_rows, cols,
-                       static_cast<const float*>(x), rows_used, reinterpret_cast<uint32_t*>(codes),
-                       scales);
-  else
-    hipLaunchKernelGGL(mx4_quantize_kernel<bf16_t>, grid, block, 0, stream, num_rows, cols,
-                       static_cast<const bf16_t*>(x), rows_used, reinterpret_cast<uint32_t*>(codes),
-                       scales);
+  for_units(num_rows * cols / 8, [&](auto units, dim3 grid) {
+    constexpr int U = decltype(units)::value;
+    uint32_t* c = reinterpret_cast<uint32_t*>(codes);
+    if (x_f32)
+      hipLaunchKernelGGL((mx4_quantize_kernel<float, U>), grid, dim3(kMxThreads), 0, stream, num_rows,
+                         cols, static_cast<const float*>(x), rows_used, c, scales);
+    else
+      hipLaunchKernelGGL((mx4_quantize_kernel<bf16_t, U>), grid, dim3(kMxThreads), 0, stream,
+                         num_rows, cols, static_cast<const bf16_t*>(x), rows_used, c, scales);
+  });
   return hipGetLastError();
 }
 
@@ -92,13 +137,16 @@ hipError_t launch_mx4_dequantize(bool out_f32, int64_t num_rows, int64_t cols,
                                  const uint8_t* codes, const uint8_t* scales, void* out,
                                  hipStream_t stream) {
   const int64_t n = num_rows * cols / 8;
-  const dim3 grid(mx4_grid(n)), block(kMxThreads);
-  if (out_f32)
-    hipLaunchKernelGGL(mx4_dequantize_kernel<float>, grid, block, 0, stream, n,
-                       reinterpret_cast<const uint32_t*>(codes), scales, static_cast<float*>(out));
-  else
-    hipLaunchKernelGGL(mx4_dequantize_kernel<bf16_t>, grid, block, 0, stream, n,
-                       reinterpret_cast<const uint32_t*>(codes), scales, static_cast<bf16_t*>(out));
+  for_units(n, [&](auto units, dim3 grid) {
+    constexpr int U = decltype(units)::value;
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
+    if (out_f32)
+      hipLaunchKernelGGL((mx4_dequantize_kernel<float, U>), grid, dim3(kMxThreads), 0, stream, n, c,
+                         scales, static_cast<float*>(out));
+    else
+      hipLaunchKernelGGL((mx4_dequantize_kernel<bf16_t, U>), grid, dim3(kMxThreads), 0, stream, n, c,
+                         scales, static_cast<bf16_t*>(out));
+  });
   return hipGetLastError();
 }
 

@@ -20,27 +20,11 @@
 #include "gemm_common.hpp"
 #include "kernels.hpp"
 
-#ifndef FEWG
-#define FEWG 512
-#endif
 namespace moelora {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef bf16_t bf16x2 __attribute__((ext_vector_type(2)));
 typedef bf16_t bf16x4 __attribute__((ext_vector_type(4)));
-
-// the 8 values of one word of codes, times 2^(scale byte - 127)
-__device__ __forceinline__ bf16x8 mx4_bf16x8(uint32_t w, float scale) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
-  bf16x8 v;
-  v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
-  v[4] = c[0]; v[5] = c[1]; v[6] = d[0]; v[7] = d[1];
-  return v;
-}
 
 __device__ __forceinline__ floatx4 mfma_mx4(u32x4 a, int sa, u32x4 b, int sb, floatx4 c) {
   const i32x8 va = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
@@ -95,7 +79,7 @@ __device__ __forceinline__ int64_t weight_row(const Mx4Gemm& p, int64_t cb) {
 constexpr int kStageK = 16384;
 
 template <bool XMX, int MB, int NB, int GB, int WV>
-__global__ void __launch_bounds__(64 * WV, 2) mx4_stream_kernel(Mx4Gemm p, int row_groups,
+__global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2) mx4_stream_kernel(Mx4Gemm p, int row_groups,
                                                                 int col_groups, int spread) {
   constexpr int STEPS = GB / 4;
   __shared__ floatx4 sums[WV][MB * NB][64];
@@ -750,12 +734,15 @@ static hipError_t stream(const Mx4Gemm& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// a workgroup of 4 waves and 16 NB columns, or, where those would not fill the chip,
-// of WIDE waves and 32 columns
+// A workgroup of 4 waves and 16 NB columns, or, where those would not fill the chip, of
+// WIDE waves and 32 columns (2112 columns for one row: 13 us against 24).  Groups of one
+// step leave registers for another workgroup on the CU (7168 x 2048 of 32 experts, tiles
+// of 32 rows: 84 us against 97 with two steps).
 template <bool XMX, int MB, int NB, int WIDE>
 static hipError_t few(const Mx4Gemm& p, hipStream_t s) {
-  if (ceil_div(p.M, 16 * MB) * ceil_div(p.N, 16 * NB) >= FEWG) return stream<XMX, MB, NB, 8, 4>(p, s);
-  return stream<XMX, MB, 2, 8, WIDE>(p, s);
+  constexpr int GB = 4;
+  if (ceil_div(p.M, 16 * MB) * ceil_div(p.N, 16 * NB) >= 512) return stream<XMX, MB, NB, GB, 4>(p, s);
+  return stream<XMX, MB, 2, GB, WIDE>(p, s);
 }
 
 template <bool XMX>
