@@ -648,11 +648,13 @@ def _rows_layout(align_out, top_k, dev, num_rows=None):
 
 def _apart(out, *inputs):
     """Outputs must not share memory with inputs."""
-    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    lo = out.data_ptr()
+    hi = lo + out.nbytes
     for t in inputs:
-        if t is not None and t.numel() and lo < t.data_ptr() + t.numel() * t.element_size() \
-                and t.data_ptr() < hi:
-            raise ValueError("an output overlaps an input")
+        if t is not None:
+            p = t.data_ptr()
+            if lo < p + t.nbytes and p < hi:
+                raise ValueError("an output overlaps an input")
 
 
 def _matrix(t, name, dev=None):
@@ -661,9 +663,25 @@ def _matrix(t, name, dev=None):
         raise ValueError(f"{name} must have two dimensions")
 
 
-def _on(t: torch.Tensor):
-    """The device of ``t`` as the current one, and that device's current stream."""
-    return torch.cuda.device(t.device)
+# torch.cuda.current_stream builds a Stream object, which takes as long as a small kernel
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(where, device, call, *args):
+    """call(*args, stream) with ``device`` as the current one, on its current stream."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = call(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, _raw_stream(index))
+    if status != OK:
+        _check(status, where)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def moe_lora_permute(x: torch.Tensor, align_out: Dict[str, torch.Tensor], top_k: int,
@@ -683,15 +701,12 @@ def moe_lora_permute(x: torch.Tensor, align_out: Dict[str, torch.Tensor], top_k:
     if out is None:
         out = torch.empty((cap, H), dtype=x.dtype, device=x.device)
     _need(out, "out", x.dtype, x.device)
-    if tuple(out.shape) != (cap, H):
+    if out.shape != (cap, H):
         raise ValueError(f"out must be {(cap, H)}, got {tuple(out.shape)}")
     _apart(out, x)
-    with _on(x):
-        _check(lib().moe_lora_permute(T, top_k, H, dt, cap, _ptr(x),
-                                      _ptr(align_out["sorted_pair_ids"]),
-                                      _ptr(align_out["pair_rows"]),
-                                      _ptr(align_out["num_rows_padded"]), _ptr(out), _stream()),
-               "moe_lora_permute")
+    _launch("moe_lora_permute", x.device, lib().moe_lora_permute, T, top_k, H, dt, cap, _at(x),
+            _at(align_out["sorted_pair_ids"]), _at(align_out["pair_rows"]),
+            _at(align_out["num_rows_padded"]), _at(out))
     return out
 
 
@@ -705,17 +720,15 @@ def moe_lora_permute_backward(d_rows: torch.Tensor, align_out: Dict[str, torch.T
     if dx is None:
         dx = torch.empty((T, H), dtype=out_dtype or d_rows.dtype, device=d_rows.device)
     _token_out(dx, "dx", T, H, d_rows, out_dtype)
-    with _on(d_rows):
-        _check(lib().moe_lora_permute_backward(T, top_k, H, _row_dtype(d_rows, "d_rows"),
-                                               _row_dtype(dx, "dx"), cap, _ptr(d_rows),
-                                               _ptr(align_out["pair_rows"]), _ptr(dx), _stream()),
-               "moe_lora_permute_backward")
+    _launch("moe_lora_permute_backward", d_rows.device, lib().moe_lora_permute_backward, T, top_k, H,
+            _row_dtype(d_rows, "d_rows"), _row_dtype(dx, "dx"), cap, _at(d_rows),
+            _at(align_out["pair_rows"]), _at(dx))
     return dx
 
 
 def _token_out(t, name, T, H, rows, out_dtype):
     _need(t, name, out_dtype, rows.device)
-    if tuple(t.shape) != (T, H):
+    if t.shape != (T, H):
         raise ValueError(f"{name} must be {(T, H)}, got {tuple(t.shape)}")
     _apart(t, rows)
 
@@ -740,11 +753,9 @@ def moe_lora_unpermute(rows: torch.Tensor, align_out: Dict[str, torch.Tensor], t
     if y is None:
         y = torch.empty((T, H), dtype=out_dtype or rows.dtype, device=rows.device)
     _token_out(y, "y", T, H, rows, out_dtype)
-    with _on(rows):
-        _check(lib().moe_lora_unpermute(T, top_k, H, _row_dtype(rows, "rows"), _row_dtype(y, "y"),
-                                        cap, _ptr(rows), _ptr(align_out["pair_rows"]),
-                                        _ptr(topk_weights), _ptr(y), _stream()),
-               "moe_lora_unpermute")
+    _launch("moe_lora_unpermute", rows.device, lib().moe_lora_unpermute, T, top_k, H,
+            _row_dtype(rows, "rows"), _row_dtype(y, "y"), cap, _at(rows), _at(align_out["pair_rows"]),
+            _at(topk_weights), _at(y))
     return y
 
 
@@ -768,7 +779,7 @@ def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
         raise ValueError(f"dy has {dy.shape[0]} rows, the layout {T} tokens")
     if rows is not None:
         _need(rows, "rows", rows_dtype, dev)
-        if tuple(rows.shape) != (cap, H):
+        if rows.shape != (cap, H):
             raise ValueError(f"rows must be {(cap, H)}, got {tuple(rows.shape)}")
     if topk_weights is not None:
         _pair_weights(topk_weights, T, top_k, dev)
@@ -776,7 +787,7 @@ def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
     if d_rows is None:
         d_rows = torch.empty((cap, H), dtype=dt, device=dev)
     _need(d_rows, "d_rows", dt, dev)
-    if tuple(d_rows.shape) != (cap, H):
+    if d_rows.shape != (cap, H):
         raise ValueError(f"d_rows must be {(cap, H)}, got {tuple(d_rows.shape)}")
     _apart(d_rows, dy, rows, topk_weights)
     if rows is None or topk_weights is None:
@@ -787,12 +798,10 @@ def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
     if d_weights is not None:
         _pair_weights(d_weights, T, top_k, dev, "d_weights")
         _apart(d_weights, dy, rows, topk_weights, d_rows)
-    with _on(dy):
-        _check(lib().moe_lora_unpermute_backward(
-            T, top_k, H, _row_dtype(dt, "rows"), _row_dtype(dy, "dy"), cap, _ptr(dy), _ptr(rows),
-            _ptr(align_out["sorted_pair_ids"]), _ptr(align_out["pair_rows"]),
-            _ptr(align_out["num_rows_padded"]), _ptr(topk_weights), _ptr(d_rows), _ptr(d_weights),
-            _stream()), "moe_lora_unpermute_backward")
+    _launch("moe_lora_unpermute_backward", dev, lib().moe_lora_unpermute_backward, T, top_k, H,
+            _row_dtype(dt, "rows"), _row_dtype(dy, "dy"), cap, _at(dy), _at(rows),
+            _at(align_out["sorted_pair_ids"]), _at(align_out["pair_rows"]),
+            _at(align_out["num_rows_padded"]), _at(topk_weights), _at(d_rows), _at(d_weights))
     return d_rows, d_weights
 
 
@@ -820,7 +829,7 @@ def _mx4_pair(codes, scales, name, dev=None):
     _need(codes, f"{name} codes", torch.uint8, dev)
     _need(scales, f"{name} scales", torch.uint8, codes.device)
     if codes.dim() < 1 or codes.shape[-1] % 16 or \
-            tuple(scales.shape) != (*codes.shape[:-1], codes.shape[-1] // 16):
+            scales.shape != (*codes.shape[:-1], codes.shape[-1] // 16):
         raise ValueError(f"{name} must be codes [.., K/2] and scales [.., K/32], got "
                          f"{tuple(codes.shape)} and {tuple(scales.shape)}")
     return 2 * codes.shape[-1]
@@ -846,16 +855,14 @@ def moe_lora_mx4_quantize(x: torch.Tensor, num_rows_used: Optional[torch.Tensor]
     if scales is None:
         scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=dev)
     _mx4_pair(codes, scales, "the output", dev)
-    if tuple(codes.shape) != (*lead, K // 2):
+    if codes.shape != (*lead, K // 2):
         raise ValueError(f"codes must be {(*lead, K // 2)}, got {tuple(codes.shape)}")
     if num_rows_used is not None:
         _need(num_rows_used, "num_rows_used", torch.int32, dev, 1)
     _apart(codes, x, scales)
     _apart(scales, x)
-    with _on(x):
-        _check(lib().moe_lora_mx4_quantize(x.numel() // K, K, dt, _ptr(x), _ptr(num_rows_used),
-                                           _ptr(codes), _ptr(scales), _stream()),
-               "moe_lora_mx4_quantize")
+    _launch("moe_lora_mx4_quantize", dev, lib().moe_lora_mx4_quantize, x.numel() // K, K, dt, _at(x),
+            _at(num_rows_used), _at(codes), _at(scales))
     return codes, scales
 
 
@@ -868,15 +875,13 @@ def moe_lora_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor,
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=codes.device)
     _need(out, "out", out_dtype, codes.device)
-    if tuple(out.shape) != shape:
+    if out.shape != shape:
         raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
     _apart(out, codes, scales)
     if K == 0:
         return out
-    with _on(codes):
-        _check(lib().moe_lora_mx4_dequantize(out.numel() // K, K, _row_dtype(out, "out"),
-                                             _ptr(codes), _ptr(scales), _ptr(out), _stream()),
-               "moe_lora_mx4_dequantize")
+    _launch("moe_lora_mx4_dequantize", codes.device, lib().moe_lora_mx4_dequantize, out.numel() // K, K,
+            _row_dtype(out, "out"), _at(codes), _at(scales), _at(out))
     return out
 
 
@@ -921,7 +926,7 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
     if out is None:
         out = torch.empty((M, cols), dtype=out_dtype or torch.bfloat16, device=dev)
     _need(out, "out", out_dtype, dev)
-    if tuple(out.shape) != (M, cols):
+    if out.shape != (M, cols):
         raise ValueError(f"out must be {(M, cols)}, got {tuple(out.shape)}")
     _apart(out, x, x_scales, w_codes, w_scales)
     if M == 0:
@@ -934,8 +939,7 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
     a.x, a.w, a.w_scale, a.out = (x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
                                   out.data_ptr())
     a.x_scale = None if x_scales is None else x_scales.data_ptr()
-    with _on(x):
-        _check(lib().moe_lora_mx4_gemm(ctypes.byref(a), _stream()), "moe_lora_mx4_gemm")
+    _launch("moe_lora_mx4_gemm", dev, lib().moe_lora_mx4_gemm, ctypes.byref(a))
     return out
 
 
