@@ -369,13 +369,24 @@ __device__ __forceinline__ void wait_dma_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+constexpr int tile_ring(bool xmx) { return xmx ? 2 : 3; }
+// LDS of a tile: the ring, and two buffers of scales
+constexpr int tile_lds(bool xmx, int tm) {
+  return tile_ring(xmx) * (tm * 128 + kTileN * (xmx ? 128 : 32)) +
+         2 * ((xmx ? tm : 0) + kTileN) * (xmx ? 16 : 4);
+}
+
+// rows [m0, m0 + TM) of expert e, weight rows from 16 cb0 on; holds: a bit per row
+// that holds a pair
+struct Holds { uint64_t r0, r64, r128, r192; };   // not an array: those end in LDS
+
 template <bool XMX, int TM>
-__global__ void __launch_bounds__(512) mx4_tile_kernel(
-    Mx4Gemm p, int m_tiles, int n_tiles, int pn, int n_patches, int dma_scales) {
+__device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0, int64_t cb0,
+                                         int64_t e, Holds holds, int dma_scales) {
   constexpr int WN = 4, NW = 8;
   constexpr int MB = TM / 32, NB = kTileN / 16 / WN;        // 16-row blocks of a wave
   constexpr int WROWB = XMX ? 128 : 32;                     // LDS bytes of a weight row
-  constexpr int RING = XMX ? 2 : 3;
+  constexpr int RING = tile_ring(XMX);
   constexpr int XPART = TM * 128, STAGE = XPART + kTileN * WROWB;
   constexpr int XSEG = XPART / 1024 / NW, WSEG = kTileN * WROWB / 1024 / NW;  // a wave's DMAs
   constexpr int SROWS = (XMX ? TM : 0) + kTileN;            // rows with scales; x's come first
@@ -383,22 +394,8 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
   constexpr int SB = 2 * KB;                                // scale bytes of a row for two K tiles
   constexpr int SCALES = RING * STAGE;                      // where the two scale buffers lie
   static_assert(SROWS <= 64 * NW && SROWS % 64 == 0, "one scale row per thread");
-  __shared__ __attribute__((aligned(1024))) char lds[SCALES + 2 * SROWS * SB];
-
-  // patches of (32 / pn) x pn tiles go round the eight XCDs (workgroup b runs on
-  // XCD b % 8), so the 32 workgroups that an XCD holds share rows and weights in its L2
-  const int pm = 32 / pn;
-  const int patch = (int)(blockIdx.x / 256) * 8 + (int)(blockIdx.x % 8);
-  const int in = (int)(blockIdx.x / 8) % 32;
-  const int mt = patch / n_patches * pm + in % pm, nt = patch % n_patches * pn + in / pm;
-  if (mt >= m_tiles || nt >= n_tiles) return;
-  const int64_t m0 = (int64_t)mt * TM;
-  const int64_t cb0 = (int64_t)nt * (kTileN / 16), ncb = p.N / 16;
-  int64_t e = 0;
-  if (p.tile_expert) {
-    e = __builtin_amdgcn_readfirstlane(p.tile_expert[m0 / p.BM]);
-    if (e < 0 || e >= p.E) return;
-  }
+  static_assert(SCALES + 2 * SROWS * SB == tile_lds(XMX, TM), "the LDS of a tile");
+  const int64_t ncb = p.N / 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int wm = wave / WN, wn = wave % WN;
@@ -421,11 +418,12 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
   // (one for even and one for odd segments: their swizzle differs) serves them all.
   // A tile behind the end of K or of M takes an address per lane instead, worked out
   // on the spot (kept over the loop, these would cost more registers than there are).
-  static_assert(XSEG % 2 == 0 && (!XMX || WSEG % 2 == 0), "segments of a wave come in pairs");
+  static_assert((XSEG == 1 || XSEG % 2 == 0) && (!XMX || WSEG % 2 == 0), "even and odd segments");
   uint32_t lane_off[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     lane_off[h] = (uint32_t)(lane / 8 * (int)x_row + chunk_in((lane % 8) ^ swz(h * 8 + lane / 8)) * 16);
+  const uint32_t lane_off_one = wave % 2 ? lane_off[1] : lane_off[0];
   const bool all_rows = m_last == TM - 1;
   constexpr int DMAS = XSEG + WSEG;      // of a wave, for a tile
   // the i-th of them; fast: a whole tile of whole rows
@@ -437,7 +435,8 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
     if (i < XSEG) {
       const int seg = wave * XSEG + i;
       if constexpr (kWhole) {
-        dma16(x_base + seg * 8 * x_row, lane_off[i % 2] + t * 128, at + seg * 1024);
+        const uint32_t off = XSEG == 1 ? lane_off_one : lane_off[i % 2];
+        dma16(x_base + seg * 8 * x_row, off + t * 128, at + seg * 1024);
       } else {
         const int row = seg * 8 + l / 8, c = chunk_in((l % 8) ^ swz(row));
         // chunks of 16 bytes: a block of MX4, a quarter of one in bf16
@@ -480,13 +479,28 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
   auto scales_load = [&](int grp) {
     __builtin_memcpy(&s_val, s_base + grp * SB + s_off, SB);
   };
+  // whether or not they are all in the row: the row's last SB bytes are shifted down
   auto scales_load_end = [&](int grp) {
+    const int behind = (grp + 1) * SB - nblk;
+    if (behind <= 0) {
+      scales_load(grp);
+    } else if (nblk >= SB) {
+      __builtin_memcpy(&s_val, s_base + (nblk - SB) + s_off, SB);
+      for (int b = 0; b < behind; ++b) {
 #pragma unroll
-    for (int w = 0; w < SB / 4; ++w) {
-      s_val.w[w] = 0;
-#pragma unroll 1
-      for (int b = grp * SB + 4 * w + 3; b >= grp * SB + 4 * w; --b)
-        s_val.w[w] = s_val.w[w] << 8 | (b < nblk ? s_base[s_off + b] : 127);
+        for (int w = 0; w < SB / 4; ++w)
+          s_val.w[w] = __builtin_amdgcn_alignbyte(w + 1 < SB / 4 ? s_val.w[w + 1] : 127u, s_val.w[w], 1);
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < SB / 4; ++w) {
+        s_val.w[w] = 0;
+#pragma unroll
+        for (int b = 3; b >= 0; --b) {
+          const int at = grp * SB + 4 * w + b;
+          s_val.w[w] = s_val.w[w] << 8 | (at < nblk ? s_base[s_off + min(at, nblk - 1)] : 127);
+        }
+      }
     }
   };
   auto scales_store = [&](int grp) {
@@ -498,7 +512,7 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
       dma_lane<SB>(s_base + grp * SB + s_off, lds0 + SCALES + ((grp & 1) * SROWS + wave * 64) * SB);
   };
 
-  constexpr int kAhead = 3, kRing = 4;
+  constexpr int kAhead = MB > 3 ? 3 : 1, kRing = kAhead + 1;
   static_assert((2 * MB) % kRing == 0 && MB > kAhead, "the ring starts each tile at its first place");
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   // of a K tile.  MX4: a word holds the bytes of both steps of two neighbouring
@@ -615,7 +629,10 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
     static_for<MB>([&](auto I) {
       constexpr int i = decltype(I)::value, q = i + kAhead;
       x[q % kRing] = q < MB ? read_x(place, q, 0) : read_x(place, q - MB, 1);
-      if constexpr (i < NB) w1[i] = XMX ? read_w(place, i, 1) : expand(sc, XMX ? 0 : i, 1);
+      static_for<NB>([&](auto J) {
+        constexpr int j = decltype(J)::value;
+        if constexpr (j % MB == i) w1[j] = XMX ? read_w(place, j, 1) : expand(sc, XMX ? 0 : j, 1);
+      });
       constexpr int from = kEarly + i * kPerBlock;
       if constexpr (kMode == kAny) {
         if (t + RING - 1 < tiles) issue(t + RING - 1, behind, from, from + kPerBlock, std::false_type{});
@@ -680,12 +697,14 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
   for (; t + 1 < tiles; ++t) tile(t, std::integral_constant<int, kAny>{});
   tile(t, std::integral_constant<int, kLast>{});
 
+  const uint64_t mine[2] = {MB == 8 && wm ? holds.r128 : MB == 4 && wm ? holds.r64 : holds.r0,
+                            MB == 8 && wm ? holds.r192 : holds.r64};   // of the wave's rows
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
     const int row = (wm * MB + i) * 16 + r;
     if (row > m_last) continue;
     const int64_t m = m0 + row;
-    if (p.row_ids && !(p.row_ids[m] >= 0 && p.row_ids[m] < p.num_ids)) {
+    if (!(mine[i / 4] >> (row % 64) & 1)) {
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -709,17 +728,100 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(
   }
 }
 
+// Workgroups of the last, incomplete round of 256 (one to a CU) take a half or a quarter
+// of a tile's rows each, where that fills the round no more than once; a workgroup whose
+// live rows fit a smaller tile takes the smaller one (padding closes the rows of an
+// expert).  8192 rows of 8 experts, 4096 x 14336, bf16 x: 912 -> 793 us, 2.25 rounds
+// having run as three; 16384 rows of 32 experts, 4096 x 7168, MX4 x: 345 -> 318 us.
+//
+// Patches of (32 / pn) x pn tiles go round the eight XCDs (workgroup b runs on XCD b % 8),
+// so the 32 workgroups that an XCD holds share rows and weights in its L2.
+constexpr int kRound = 256;
+constexpr int64_t kTailTiles = 16 * kRound;   // with more, a share of a round does not count
+
+// TOP rows are one entry of tile_expert
+template <bool XMX, int TOP>
+__global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, int n_tiles, int pn,
+                                                       int n_patches, int tail, int dma_scales) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds(XMX, TOP)];
+  const int lane = threadIdx.x & 63;
+  const int pm = 32 / pn;
+  int patch = (int)(blockIdx.x / 256) * 8 + (int)(blockIdx.x % 8);
+  const int in = (int)(blockIdx.x / 8) % 32;
+  int used = m_tiles, whole = m_tiles, pieces = 1;   // tiles with rows; those taken whole
+  if (tail) {
+    if (p.tile_expert) {
+      used = 0;
+      for (int t0 = 0; t0 < m_tiles; t0 += 64) {
+        const int t = t0 + lane;
+        const int te = t < m_tiles ? p.tile_expert[t] : -1;
+        const uint64_t has = __ballot(te >= 0 && te < p.E);
+        if (has) used = t0 + 64 - __clzll(has);
+      }
+      used = __builtin_amdgcn_readfirstlane(used);
+    }
+    whole = used * n_tiles / kRound * kRound / n_tiles / pm * pm;
+    const int rest = (used - whole) * n_tiles;
+    if (TOP == 256 && 4 * rest <= kRound) pieces = 4;
+    else if (2 * rest <= kRound) pieces = 2;
+    else whole = used;
+  }
+  const int whole_patches = (whole + pm - 1) / pm * n_patches;
+  const bool part = patch >= whole_patches;
+  if (part) patch -= whole_patches;
+  const int mt = patch / n_patches * pm + in % pm, nt = patch % n_patches * pn + in / pm;
+  if (nt >= n_tiles || mt >= (part ? (used - whole) * pieces : whole)) return;
+  const int span = part ? TOP / pieces : TOP;
+  const int64_t m0 = part ? (int64_t)whole * TOP + (int64_t)mt * span : (int64_t)mt * TOP;
+  const int64_t cb0 = (int64_t)nt * (kTileN / 16);
+  int64_t e = 0;
+  if (p.tile_expert) {
+    e = __builtin_amdgcn_readfirstlane(p.tile_expert[part ? whole + mt / pieces : mt]);
+    if (e < 0 || e >= p.E) return;
+  }
+  const int rows = (int)min((int64_t)span, p.M - m0);
+  if (rows <= 0) return;
+  int live = rows;   // up to the last row that holds a pair
+  Holds holds = {~uint64_t(0), ~uint64_t(0), ~uint64_t(0), ~uint64_t(0)};
+  if (p.row_ids) {
+    auto id_at = [&](int i) { return p.row_ids[m0 + min(i * 64 + lane, rows - 1)]; };
+    auto bits = [&](int i, int32_t id) {
+      return (uint64_t)__ballot(i * 64 + lane < rows && id >= 0 && id < p.num_ids);
+    };
+    const int32_t id0 = id_at(0), id1 = id_at(1), id2 = TOP == 256 ? id_at(2) : -1,
+                  id3 = TOP == 256 ? id_at(3) : -1;
+    holds = {bits(0, id0), bits(1, id1), bits(2, id2), bits(3, id3)};
+    live = holds.r192   ? 256 - __clzll(holds.r192)
+           : holds.r128 ? 192 - __clzll(holds.r128)
+           : holds.r64  ? 128 - __clzll(holds.r64)
+           : holds.r0   ? 64 - __clzll(holds.r0)
+                        : 0;
+  }
+  // the rows behind the tile that these take hold no pair
+  const int done = live > 128 ? 256 : live > 64 ? 128 : live > 0 ? 64 : 0;
+  const int blocks = (int)min((int64_t)kTileN / 16, p.N / 16 - cb0) / (p.silu_mul ? 2 : 1);
+  const int64_t first = p.silu_mul ? cb0 / 2 : cb0, cols = p.silu_mul ? p.N / 2 : p.N;
+  for (int row = done + threadIdx.x / 64; row < rows; row += 8)
+    if (lane < blocks * 4) store_out(p, (m0 + row) * cols + first * 16 + lane * 4, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
+  if (TOP == 256 && done == 256) mx4_tile<XMX, TOP>(p, lds, m0, cb0, e, holds, dma_scales);
+  else if (done == 128) mx4_tile<XMX, 128>(p, lds, m0, cb0, e, holds, dma_scales);
+  else if (done == 64) mx4_tile<XMX, 64>(p, lds, m0, cb0, e, holds, dma_scales);
+}
+
 template <bool XMX, int TM>
 static hipError_t tiled(const Mx4Gemm& p, hipStream_t stream) {
   const int64_t m_tiles = ceil_div(p.M, TM), n_tiles = ceil_div(p.N, kTileN);
   int pn = 8;
   while (pn > n_tiles) pn /= 2;
   const int64_t n_patches = ceil_div(n_tiles, pn);
-  const int64_t patches = ceil_div(m_tiles, 32 / pn) * n_patches;
+  const bool tail = m_tiles * n_tiles <= kTailTiles;
+  // parts of tiles fill a round at most: 16 patches, and one more for each part of the
+  // columns in which their rows end
+  const int64_t patches = ceil_div(m_tiles, 32 / pn) * n_patches + (tail ? 16 + 2 * n_patches : 0);
   const bool dma_scales = p.K % 128 == 0 && reinterpret_cast<uintptr_t>(p.w_scale) % 4 == 0;
   const auto kernel = mx4_tile_kernel<XMX, TM>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(ceil_div(patches, 8) * 256)), dim3(512), 0, stream, p,
-                     (int)m_tiles, (int)n_tiles, pn, (int)n_patches, (int)dma_scales);
+                     (int)m_tiles, (int)n_tiles, pn, (int)n_patches, (int)tail, (int)dma_scales);
   return hipGetLastError();
 }
 

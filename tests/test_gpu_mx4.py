@@ -263,6 +263,44 @@ def test_padding_rows_are_not_read(kind, bm):
         assert torch.equal(y[~pad], z[~pad])
 
 
+MANY = [  # block_m, tiles in use and behind them, N: past 256 workgroups, whose last round is split
+    (256, 18, 2, 4096), (256, 21, 0, 4096), (256, 25, 1, 4096), (256, 31, 1, 2064), (128, 20, 3, 4096),
+    (256, 36, 1, 1040), (128, 1, 0, 16), (256, 2, 1, 528)]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"b{c[0]}t{c[1]}N{c[3]}")
+@pytest.mark.parametrize("kind", ["bf16", "mx4"])
+def test_many_tiles(case, kind):
+    """Row tiles with any number of rows in use, with gaps; the others give zeros."""
+    bm, tiles, behind, N = case
+    E, K, M = 3, 96, bm * (tiles + behind)
+    say(f"many tiles {case} {kind}")
+    g = torch.Generator().manual_seed(18)
+    experts = torch.cat((torch.randint(0, E, (tiles,), generator=g), torch.full((behind,), -1)))
+    fill = torch.randint(0, bm + 1, (tiles + behind,), generator=g)
+    for i, n in enumerate((0, 1, 64, 65, 128, bm)[:tiles]):
+        fill[i] = n
+    live = torch.arange(bm).view(1, -1) < fill.view(-1, 1)
+    live &= torch.rand(tiles + behind, bm, generator=g) < 0.9
+    live = live.reshape(-1)
+    pairs = int(live.sum()) + 1
+    sid = torch.full((M,), pairs, dtype=torch.int32)
+    sid[live] = torch.randperm(pairs - 1, generator=g).int()
+    sid[~live] = torch.where(torch.rand(int((~live).sum()), generator=g) < 0.5, -1, pairs).int()
+    al = dict(block_m=bm, tile_expert=experts.int().cuda(), sorted_pair_ids=sid.cuda(),
+              pair_rows=torch.empty(pairs, dtype=torch.int32, device="cuda"))
+    wc, ws, w64 = weights(E, N, K, 19)
+    x, xs, x64 = activations(M, K, kind, 20)
+    row_expert = np.where(live.numpy(), experts.numpy().repeat(bm), -1)
+    for silu in (False, True) if N % 32 == 0 else (False,):
+        mark = torch.full((M, N // 2 if silu else N), -9.5, dtype=torch.bfloat16, device="cuda")
+        y = binding.moe_lora_mx4_gemm(x, wc, ws, x_scales=xs, align_out=al, silu_mul=silu, out=mark.clone())
+        check_product(np64(y), torch.bfloat16, x64, w64, row_expert, silu, K, f"silu {silu}")
+        used = bm * tiles
+        assert bool((y[:used][~live[:used].cuda()] == 0).all())
+        assert torch.equal(y[used:], mark[used:])
+
+
 @pytest.mark.parametrize("kind", ["bf16", "mx4"])
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_extreme_scales(kind, M):
