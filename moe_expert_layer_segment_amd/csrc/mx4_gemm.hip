@@ -53,6 +53,19 @@ __device__ __forceinline__ void store_out(const Mx4Gemm& p, int64_t at, floatx4 
   }
 }
 
+// 8 neighbouring columns
+__device__ __forceinline__ void store_out(const Mx4Gemm& p, int64_t at, floatx4 v, floatx4 w) {
+  if (p.out_f32) {
+    store_out(p, at, v);
+    store_out(p, at + 4, w);
+  } else {
+    bf16x8 o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = (bf16_t)(i < 4 ? v[i] : w[i - 4]);
+    *reinterpret_cast<bf16x8*>(static_cast<bf16_t*>(p.out) + at) = o;
+  }
+}
+
 // first weight row of 16-column block cb; with silu_mul even blocks are gate
 // columns, odd ones the up columns beside them
 __device__ __forceinline__ int64_t weight_row(const Mx4Gemm& p, int64_t cb) {
@@ -395,7 +408,6 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
   constexpr int SCALES = RING * STAGE;                      // where the two scale buffers lie
   static_assert(SROWS <= 64 * NW && SROWS % 64 == 0, "one scale row per thread");
   static_assert(SCALES + 2 * SROWS * SB == tile_lds(XMX, TM), "the LDS of a tile");
-  const int64_t ncb = p.N / 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   const int wm = wave / WN, wn = wave % WN;
@@ -410,8 +422,17 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
     return XMX ? (row >> 1 & 4) | (row & 2) | (row >> 2 & 1) : (row >> 1) & 7;
   };
   auto chunk_in = [](int place) { return XMX ? place : (place & 3) * 2 + (place >> 2); };
-  // weight row of LDS row n (rows of column blocks behind the last repeat it)
-  auto w_row = [&](int n) { return weight_row(p, min(cb0 + n / 16, ncb - 1)) + n % 16; };
+  // LDS row n holds row spot(n) of the tile: rows 4q..4q + 3 of two blocks of 16 lie side
+  // by side, and so do the outputs that a lane has of the two
+  auto spot = [](int n) { return n / 32 * 32 + n % 16 / 4 * 8 + n / 16 % 2 * 4 + n % 4; };
+  // weight row of LDS row n; with silu_mul blocks of gate and of up rows alternate, and
+  // side by side lie those of two gate or two up blocks.  What would lie behind the last
+  // column repeats another, `room` rows of it.
+  const int out_cols = (int)(p.silu_mul ? p.N / 2 : p.N), col0 = (int)cb0 * (p.silu_mul ? 8 : 16);
+  auto w_row = [&](int n, int room) {
+    const int col = p.silu_mul ? spot(n / 64 * 32 + n / 32 % 2 * 16 + n % 16) : spot(n);
+    return min(col0 + col, out_cols - room) + (p.silu_mul ? n / 16 % 2 * out_cols : 0);
+  };
 
   // One KB of LDS per DMA: 8 rows of x or MX4 weights, 32 of the weights beside
   // bf16 x.  The 8 rows of a segment lie at a uniform base, so an offset per lane
@@ -422,7 +443,7 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
   uint32_t lane_off[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    lane_off[h] = (uint32_t)(lane / 8 * (int)x_row + chunk_in((lane % 8) ^ swz(h * 8 + lane / 8)) * 16);
+    lane_off[h] = (uint32_t)(spot(lane / 8) * (int)x_row + chunk_in((lane % 8) ^ swz(h * 8 + lane / 8)) * 16);
   const uint32_t lane_off_one = wave % 2 ? lane_off[1] : lane_off[0];
   const bool all_rows = m_last == TM - 1;
   constexpr int DMAS = XSEG + WSEG;      // of a wave, for a tile
@@ -436,23 +457,23 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
       const int seg = wave * XSEG + i;
       if constexpr (kWhole) {
         const uint32_t off = XSEG == 1 ? lane_off_one : lane_off[i % 2];
-        dma16(x_base + seg * 8 * x_row, off + t * 128, at + seg * 1024);
+        dma16(x_base + spot(seg * 8) * x_row, off + t * 128, at + seg * 1024);
       } else {
         const int row = seg * 8 + l / 8, c = chunk_in((l % 8) ^ swz(row));
         // chunks of 16 bytes: a block of MX4, a quarter of one in bf16
         const bool in_row = t * KB + (XMX ? c : c / 4) < nblk;
-        const char* src = x_base + min(row, m_last) * x_row + t * 128 + c * 16;
+        const char* src = x_base + min(spot(row), m_last) * x_row + t * 128 + c * 16;
         dma_lane<16>(in_row ? (const void*)src : (const void*)mx4_zeros, at + seg * 1024);
       }
     } else {
       const int seg = wave * WSEG + i - XSEG;
       const uint32_t to = at + XPART + seg * 1024;
       if constexpr (XMX && kWhole) {
-        dma16(w_base + w_row(seg * 8) * (p.K / 2), lane_off[(i - XSEG) % 2] + t * 128, to);
+        dma16(w_base + (int64_t)w_row(seg * 8, 12) * (p.K / 2), lane_off[(i - XSEG) % 2] + t * 128, to);
       } else {
         const int row = XMX ? seg * 8 + l / 8 : seg * 32 + l / 2;
         const int c = XMX ? chunk_in((l % 8) ^ swz(row)) : l % 2;
-        const uint8_t* src = w_base + w_row(row) * (p.K / 2) + t * WROWB + c * 16;
+        const uint8_t* src = w_base + (int64_t)w_row(row, 1) * (p.K / 2) + t * WROWB + c * 16;
         const bool in_row = kWhole || t * KB + c < nblk;
         dma_lane<16>(in_row ? (const void*)src : (const void*)mx4_zeros, to);
       }
@@ -473,7 +494,7 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
   const int s_lane = min(wave * 64 + lane, SROWS - 1);
   const bool s_of_x = XMX && wave < TM / 64;
   const uint8_t* const s_base = s_of_x ? p.x_scale + m0 * nblk : p.w_scale + e * p.N * nblk;
-  const uint32_t s_off = (uint32_t)(s_of_x ? min(s_lane, m_last) : w_row(s_lane - (XMX ? TM : 0))) *
+  const uint32_t s_off = (uint32_t)(s_of_x ? min(spot(s_lane), m_last) : w_row(s_lane - (XMX ? TM : 0), 1)) *
                          (uint32_t)nblk;
   struct Words { uint32_t w[SB / 4]; } s_val;
   auto scales_load = [&](int grp) {
@@ -701,28 +722,31 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
                             MB == 8 && wm ? holds.r192 : holds.r64};   // of the wave's rows
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
-    const int row = (wm * MB + i) * 16 + r;
+    const int row = spot((wm * MB + i) * 16 + r);
     if (row > m_last) continue;
-    const int64_t m = m0 + row;
-    if (!(mine[i / 4] >> (row % 64) & 1)) {
-#pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+    const bool holds_pair = mine[i / 4] >> (row % 64) & 1;
+    const int64_t at = (m0 + row) * out_cols;
     if (p.silu_mul) {
+      const int col = col0 + wn * (NB / 2) * 16 + 8 * g;
+      if (col >= out_cols) continue;
+      floatx4 v[2];
 #pragma unroll
-      for (int j = 0; j < NB; j += 2) {
-        const int64_t cb = cb0 + wn * NB + j;
-        if (cb + 1 >= ncb) continue;
-        floatx4 v;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = silu_f(acc[i][j][q]) * acc[i][j + 1][q];
-        store_out(p, m * (p.N / 2) + cb / 2 * 16 + 4 * g, v);
-      }
+        for (int q = 0; q < 4; ++q)
+          v[h][q] = holds_pair ? silu_f(acc[i][2 * h][q]) * acc[i][2 * h + 1][q] : 0.0f;
+      store_out(p, at + col, v[0], v[1]);
     } else {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int64_t cb = cb0 + wn * NB + j;
-        if (cb < ncb) store_out(p, m * p.N + cb * 16 + 4 * g, acc[i][j]);
+      for (int j = 0; j < NB; j += 2) {
+        const int col = col0 + (wn * NB + j) * 16 + 8 * g;
+        if (col >= out_cols) continue;
+        floatx4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[h][q] = holds_pair ? acc[i][j + h][q] : 0.0f;
+        store_out(p, at + col, v[0], v[1]);
       }
     }
   }
