@@ -947,7 +947,7 @@ def mx4_block_m(num_tokens: int, top_k: int, num_experts: int) -> int:
     """The block_m of moe_lora_align that suits moe_lora_mx4_gemm: about the rows an
     expert gets, so that its weights are read once without many padding rows."""
     per = num_tokens * top_k / num_experts
-    return 16 if per <= 24 else 32 if per <= 48 else 64 if per <= 128 else 128 if per <= 512 else 256
+    return 16 if per <= 24 else 32 if per <= 32 else 64 if per <= 128 else 128 if per <= 512 else 256
 
 
 def run_mx4_layer(inputs: dict, activations: str = "bf16", block_m: Optional[int] = None,

@@ -75,12 +75,14 @@ __device__ __forceinline__ int64_t weight_row(const Mx4Gemm& p, int64_t cb) {
 // ---- few rows --------------------------------------------------------------
 // The weights are streamed from memory into registers, once, and bound the kernel.
 // A workgroup holds 16 MB rows and 16 NB columns; its WV waves take every WV-th group
-// of GB blocks and add their sums through LDS.
+// group of four blocks and add their sums through LDS.  Longer groups cost the registers
+// of another workgroup on the CU (7168 x 2048 of 32 experts, MX4 x, tiles of 32 rows:
+// 97 us with eight blocks, 84 with four).
 //
-// A group is steps of four blocks.  In a step lane group g loads block g of it, so the
-// 16 bytes of neighbouring groups make up 64 bytes of a row; so do the bytes of bf16 x,
-// of which group g loads 16 g..16 g + 15 of each of the step's blocks.  To match, the
-// weights' words are exchanged between the groups: 4 x 4 words, in four swaps.
+// Lane group g loads block g of the four, so the 16 bytes of neighbouring lane groups
+// make up 64 bytes of a row; so do the bytes of bf16 x, of which lane group g loads
+// 16 g..16 g + 15 of each block.  To match, the weights' words are exchanged between the
+// lane groups: 4 x 4 words, in four swaps.
 // (Loading x to match the weights instead, 16 bytes in 64, took 91 us where this took
 // 64 on gate and up of 64 tokens x 8 of 128 experts, 1536 x 2048.)
 //
@@ -91,10 +93,10 @@ __device__ __forceinline__ int64_t weight_row(const Mx4Gemm& p, int64_t cb) {
 // 16 bytes a lane into LDS first, up to K = kStageK.
 constexpr int kStageK = 16384;
 
-template <bool XMX, int MB, int NB, int GB, int WV>
-__global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2) mx4_stream_kernel(Mx4Gemm p, int row_groups,
-                                                                int col_groups, int spread) {
-  constexpr int STEPS = GB / 4;
+template <bool XMX, int MB, int NB, int WV>
+__global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2)
+mx4_stream_kernel(Mx4Gemm p, int row_groups, int col_groups, int spread) {
+  constexpr int GB = 4;   // blocks of a group
   __shared__ floatx4 sums[WV][MB * NB][64];
   extern __shared__ __attribute__((aligned(16))) uint8_t staged[];   // [NB (+ MB)][16][nblk]
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2) mx4_stream_kernel(Mx
   }
   int64_t e = 0;
   if (p.tile_expert) {
-    e = __builtin_amdgcn_readfirstlane(p.tile_expert[m0 / p.BM]);
+    e = __builtin_amdgcn_readfirstlane(p.tile_expert[(uint32_t)m0 / (uint32_t)p.BM]);
     if (e < 0 || e >= p.E) return;
   }
   const int nblk = (int)(p.K / 32);
@@ -159,25 +161,19 @@ __global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2) mx4_stream_kernel(Mx
   if ((int)threadIdx.x < pieces) piece = fetch(threadIdx.x);
 
   struct Group {
-    u32x4 w[NB][STEPS], x[MB][XMX ? STEPS : GB];
+    u32x4 w[NB], x[MB][XMX ? 1 : GB];
   };
   // the scales of group s, 2^0 behind the end and for padding rows (whose scales may be
   // anything, NaN too)
-  uint32_t wsc[NB][STEPS], xsc[XMX ? MB : 1][STEPS];
+  uint32_t wsc[NB], xsc[XMX ? MB : 1];
   auto load_scales = [&](int s, auto end) {
-    auto get = [&](uint32_t (&v)[STEPS], const uint8_t* row) {
+    auto get = [&](uint32_t& v, const uint8_t* row) {
       if constexpr (!decltype(end)::value) {
-        __builtin_memcpy(v, row + s * GB, GB);
+        __builtin_memcpy(&v, row + s * GB, GB);
       } else {
+        v = 0;
 #pragma unroll
-        for (int h = 0; h < STEPS; ++h) {
-          v[h] = 0;
-#pragma unroll
-          for (int i = 3; i >= 0; --i) {
-            const int b = s * GB + 4 * h + i;
-            v[h] = v[h] << 8 | (b < nblk ? row[b] : 127);
-          }
-        }
+        for (int b = s * GB + GB - 1; b >= s * GB; --b) v = v << 8 | (b < nblk ? row[b] : 127);
       }
     };
 #pragma unroll
@@ -196,18 +192,15 @@ __global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2) mx4_stream_kernel(Mx
         } else {
           get(xsc[mb], xs_base + (int64_t)m_lane[mb] * nblk);
         }
-        if (!live[mb]) {
-#pragma unroll
-          for (int h = 0; h < STEPS; ++h) xsc[mb][h] = 0x7F7F7F7Fu;
-        }
+        if (!live[mb]) xsc[mb] = 0x7F7F7F7Fu;
       }
     }
   };
   auto load = [&](Group& f, int s, auto end) {
     constexpr bool kEnd = decltype(end)::value;
     // blocks behind the row's end: zero codes under the scale of 1
-    auto codes = [&](const uint8_t* base, uint32_t row, int h) {
-      const int blk = s * GB + 4 * h + g;
+    auto codes = [&](const uint8_t* base, uint32_t row) {
+      const int blk = s * GB + g;
       const bool in = !kEnd || blk < nblk;
       const u32x4 v = *reinterpret_cast<const u32x4*>(base + (row + (in ? blk : 0) * 16));
       return in ? v : u32x4{0, 0, 0, 0};
@@ -215,18 +208,16 @@ __global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2) mx4_stream_kernel(Mx
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int64_t n = e * p.N + weight_row(p, min(cb0 + nb, ncb - 1));
-#pragma unroll
-      for (int h = 0; h < STEPS; ++h) f.w[nb][h] = codes(p.w + n * w_row, r * (uint32_t)w_row, h);
+      f.w[nb] = codes(p.w + n * w_row, r * (uint32_t)w_row);
     }
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
-      for (int q = 0; q < (XMX ? STEPS : GB); ++q) f.x[mb][q] = u32x4{0, 0, 0, 0};
+      for (int q = 0; q < (XMX ? 1 : GB); ++q) f.x[mb][q] = u32x4{0, 0, 0, 0};
       if (live[mb]) {
         const uint32_t row = m_lane[mb] * (uint32_t)x_row;
         if constexpr (XMX) {
-#pragma unroll
-          for (int h = 0; h < STEPS; ++h) f.x[mb][h] = codes(x_base, row, h);
+          f.x[mb][0] = codes(x_base, row);
         } else {
 #pragma unroll
           for (int q = 0; q < GB; ++q)
@@ -243,27 +234,22 @@ __global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2) mx4_stream_kernel(Mx
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   auto multiply = [&](const Group& f) {
 #pragma unroll
-    for (int h = 0; h < STEPS; ++h) {
+    for (int nb = 0; nb < NB; ++nb) {
+      if constexpr (XMX) {
+        const int sw = (int)(wsc[nb] >> (8 * g));
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        if constexpr (XMX) {
-          const int sw = (int)(wsc[nb][h] >> (8 * g));
+        for (int mb = 0; mb < MB; ++mb)
+          acc[mb][nb] = mfma_mx4(f.w[nb], sw, f.x[mb][0], (int)(xsc[mb] >> (8 * g)), acc[mb][nb]);
+      } else {
+        const u32x4 t = transpose_groups(f.w[nb]);
+#pragma unroll
+        for (int q = 0; q < GB; ++q) {
+          // the scale byte as an exponent; the conversion reads 0 as 2^-127, 255 as NaN
+          const uint32_t scale = (wsc[nb] >> (8 * q) & 255) << 23;
+          const bf16x8 a = mx4_bf16x8(t[q], __builtin_bit_cast(float, scale));
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb)
-            acc[mb][nb] = mfma_mx4(f.w[nb][h], sw, f.x[mb][h], (int)(xsc[mb][h] >> (8 * g)),
-                                   acc[mb][nb]);
-        } else {
-          const u32x4 t = transpose_groups(f.w[nb][h]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            // the scale byte as an exponent; the conversion reads 0 as 2^-127, 255 as NaN
-            const uint32_t scale = (wsc[nb][h] >> (8 * q) & 255) << 23;
-            const bf16x8 a = mx4_bf16x8(t[q], __builtin_bit_cast(float, scale));
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
-              acc[mb][nb] = Elt<bf16_t>::mma(a, __builtin_bit_cast(bf16x8, f.x[mb][4 * h + q]),
-                                             acc[mb][nb]);
-          }
+            acc[mb][nb] = Elt<bf16_t>::mma(a, __builtin_bit_cast(bf16x8, f.x[mb][q]), acc[mb][nb]);
         }
       }
     }
@@ -336,7 +322,9 @@ __global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2) mx4_stream_kernel(Mx
 // reading the block that comes kAhead later meanwhile.  When the last fragments of
 // a tile have been read, a barrier admits the next tile; behind it the wave starts
 // the DMA into the places just left and reads the next tile's first fragments under
-// the MFMAs that remain.
+// the MFMAs that remain.  Beside its K tiles (16384 rows of 4 experts, 4096 x 7168 of MX4
+// x: 48 us of the 59 that 256 workgroups take) a workgroup spends 3 us before its first
+// products and 2 on its stores, and 3 go by until the CU holds the next one.
 //
 // LDS rows of x (and of MX4 weights) are eight 16-byte chunks.  Lane group g wants
 // chunk 2g + h in step h.  A fragment read serves 16 lanes at a time, rows of two
@@ -787,7 +775,7 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, i
     whole = used * n_tiles / kRound * kRound / n_tiles / pm * pm;
     const int rest = (used - whole) * n_tiles;
     if (TOP == 256 && 4 * rest <= kRound) pieces = 4;
-    else if (2 * rest <= kRound) pieces = 2;
+    else if (TOP >= 128 && 2 * rest <= kRound) pieces = 2;
     else whole = used;
   }
   const int whole_patches = (whole + pm - 1) / pm * n_patches;
@@ -812,7 +800,7 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, i
     auto bits = [&](int i, int32_t id) {
       return (uint64_t)__ballot(i * 64 + lane < rows && id >= 0 && id < p.num_ids);
     };
-    const int32_t id0 = id_at(0), id1 = id_at(1), id2 = TOP == 256 ? id_at(2) : -1,
+    const int32_t id0 = id_at(0), id1 = TOP >= 128 ? id_at(1) : -1, id2 = TOP == 256 ? id_at(2) : -1,
                   id3 = TOP == 256 ? id_at(3) : -1;
     holds = {bits(0, id0), bits(1, id1), bits(2, id2), bits(3, id3)};
     live = holds.r192   ? 256 - __clzll(holds.r192)
@@ -828,7 +816,7 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, i
   for (int row = done + threadIdx.x / 64; row < rows; row += 8)
     if (lane < blocks * 4) store_out(p, (m0 + row) * cols + first * 16 + lane * 4, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
   if (TOP == 256 && done == 256) mx4_tile<XMX, TOP>(p, lds, m0, cb0, e, holds, dma_scales);
-  else if (done == 128) mx4_tile<XMX, 128>(p, lds, m0, cb0, e, holds, dma_scales);
+  else if (TOP >= 128 && done == 128) mx4_tile<XMX, TOP >= 128 ? 128 : 64>(p, lds, m0, cb0, e, holds, dma_scales);
   else if (done == 64) mx4_tile<XMX, 64>(p, lds, m0, cb0, e, holds, dma_scales);
 }
 
@@ -849,36 +837,40 @@ static hipError_t tiled(const Mx4Gemm& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool XMX, int MB, int NB, int GB, int WV>
+template <bool XMX, int MB, int NB, int WV>
 static hipError_t stream(const Mx4Gemm& p, hipStream_t stream) {
   const int64_t col_groups = ceil_div(p.N / 16, NB), row_groups = ceil_div(p.M, 16 * MB);
   const bool spread = row_groups >= 32;
   const size_t staged = p.K <= kStageK ? (size_t)(NB + (XMX ? MB : 0)) * 16 * (p.K / 32) : 0;
-  const auto kernel = mx4_stream_kernel<XMX, MB, NB, GB, WV>;
+  const auto kernel = mx4_stream_kernel<XMX, MB, NB, WV>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)((spread ? round_up(row_groups, 16) : row_groups) * col_groups)),
                      dim3(64 * WV), staged, stream, p, (int)row_groups, (int)col_groups, (int)spread);
   return hipGetLastError();
 }
 
 // A workgroup of 4 waves and 16 NB columns, or, where those would not fill the chip, of
-// WIDE waves and 32 columns (2112 columns for one row: 13 us against 24).  Groups of one
-// step leave registers for another workgroup on the CU (7168 x 2048 of 32 experts, tiles
-// of 32 rows: 84 us against 97 with two steps).
+// WIDE waves and 32 columns (2112 columns for one row: 13 us against 24).
 template <bool XMX, int MB, int NB, int WIDE>
 static hipError_t few(const Mx4Gemm& p, hipStream_t s) {
-  constexpr int GB = 4;
-  if (ceil_div(p.M, 16 * MB) * ceil_div(p.N, 16 * NB) >= 512) return stream<XMX, MB, NB, GB, 4>(p, s);
-  return stream<XMX, MB, 2, GB, WIDE>(p, s);
+  if (ceil_div(p.M, 16 * MB) * ceil_div(p.N, 16 * NB) >= 512) return stream<XMX, MB, NB, 4>(p, s);
+  return stream<XMX, MB, 2, WIDE>(p, s);
 }
 
+// With more than 64 tiles of 64 rows x 256 columns a workgroup takes a tile.  Below that the
+// chip is filled by streaming 32 or 64 columns at a time past the same rows again: 4096 x
+// 7168 for 64, 256 and 384 rows of MX4 15, 24 and 40 us streamed and 32, 34 and 34 in
+// tiles, of bf16 31, 59 and 86 against 69, 74 and 73.
 template <bool XMX>
 static hipError_t product(const Mx4Gemm& p, hipStream_t s) {
   // rows of a workgroup: within one tile_expert entry, or those there are
   const int64_t rows = p.tile_expert ? p.BM : p.M;
   auto takes = [&](int64_t n) { return p.tile_expert ? rows % n == 0 : rows > n / 2; };
-  if (takes(256)) return tiled<XMX, 256>(p, s);
-  if (takes(128)) return tiled<XMX, 128>(p, s);
-  if (takes(64)) return few<XMX, 4, 2, 8>(p, s);
+  if (takes(64)) {
+    if (ceil_div(p.M, 64) * ceil_div(p.N, kTileN) <= 64) return few<XMX, 4, 2, 8>(p, s);
+    if (takes(256)) return tiled<XMX, 256>(p, s);
+    if (takes(128)) return tiled<XMX, 128>(p, s);
+    return tiled<XMX, 64>(p, s);
+  }
   if (takes(32)) return few<XMX, 2, 4, 8>(p, s);
   return few<XMX, 1, 4, 16>(p, s);
 }

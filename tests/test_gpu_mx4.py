@@ -152,7 +152,10 @@ def check_product(got, out_dtype, x64, w64, row_expert, silu, K, what):
 
 DENSE = [(1, 16, 32), (1, 2112, 736), (5, 48, 96), (16, 64, 256), (17, 80, 288), (33, 32, 512),
          (64, 128, 1056), (100, 272, 480), (129, 256, 256), (300, 96, 2080), (513, 528, 1312),
-         (257, 1040, 768)]
+         (257, 1040, 768),
+         # past 64 tiles of 64 x 256
+         (64, 16640, 736), (70, 16400, 288), (130, 8208, 544), (520, 2064, 1312), (1100, 1040, 2080),
+         (700, 1536, 2560)]
 
 
 @pytest.mark.parametrize("shape", DENSE, ids=lambda s: "x".join(map(str, s)))
@@ -179,6 +182,9 @@ GROUPED = [  # experts of the tiles (-1: unused), block_m, N, K
     ([2, 0, 1], 256, 544, 800),
     ([2, 2, 1, 1, 0, -1], 256, 256, 2304),
     ([-1, -1], 128, 64, 64),
+    ([0, 0, 2, 1, 3] * 8 + [-1], 64, 544, 800),
+    ([1, 1, 3, 0, 2] * 4 + [-1], 128, 544, 2304),
+    ([3, 2, 2, 0, 1, 3, 0], 256, 800, 1056),
 ]
 
 
@@ -203,11 +209,11 @@ def test_grouped_product(case, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mx4"])
-@pytest.mark.parametrize("bm", [16, 256])
-def test_rows_do_not_reach_other_rows(kind, bm):
+@pytest.mark.parametrize("bm,times", [(16, 1), (256, 1), (64, 23), (256, 6)])
+def test_rows_do_not_reach_other_rows(kind, bm, times):
     """NaN rows (what padding may hold) change no other row, bit for bit; a NaN scale of a
     weight row changes that output column alone."""
-    E, N, K, tiles = 2, 96, 416, [1, 0, 1]
+    E, N, K, tiles = 2, 96, 416, [1, 0, 1] * times
     M = bm * len(tiles)
     wc, ws, _ = weights(E, N, K, 6)
     al = dict(block_m=bm, tile_expert=torch.tensor(tiles, dtype=torch.int32, device="cuda"))
@@ -265,7 +271,7 @@ def test_padding_rows_are_not_read(kind, bm):
 
 MANY = [  # block_m, tiles in use and behind them, N: past 256 workgroups, whose last round is split
     (256, 18, 2, 4096), (256, 21, 0, 4096), (256, 25, 1, 4096), (256, 31, 1, 2064), (128, 20, 3, 4096),
-    (256, 36, 1, 1040), (128, 1, 0, 16), (256, 2, 1, 528)]
+    (256, 36, 1, 1040), (128, 1, 0, 16), (256, 2, 1, 528), (64, 30, 2, 1040), (64, 70, 1, 272)]
 
 
 @pytest.mark.parametrize("case", MANY, ids=lambda c: f"b{c[0]}t{c[1]}N{c[3]}")
@@ -302,7 +308,7 @@ def test_many_tiles(case, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mx4"])
-@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("M", [1, 40, 300, 4200])
 def test_extreme_scales(kind, M):
     """Scales at both ends of the e8m0 range; sums stay in fp32's."""
     N, K = 64, 128
