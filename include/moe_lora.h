@@ -437,8 +437,7 @@ int moe_lora_dense_forward_events(const moe_lora_dense_args* args, void* stream,
  * dtype is the type of the rows: F32 or BF16 (moe_lora_permute, whose x has it
  * too, copies U8 as well: `hidden` bytes a row, for the codes and scales of MX4
  * rows).  The tokens' type is given apart; the two may differ.  Any hidden from 1
- * to 2^24 and any pointer aligned to its element works; rows of a multiple of 16
- * bytes at 16-byte aligned addresses are moved 16 bytes at a time.
+ * to 2^24 and any pointer aligned to its element works.
  * num_tokens * top_k < 2^30, num_rows < 2^31 (else MOE_LORA_ERR_UNSUPPORTED).
  *
  * topk_weights NULL stands for ones (d_weights must then be NULL).  d_weights NULL

@@ -378,12 +378,12 @@ constexpr int tile_lds(bool xmx, int tm) {
 }
 
 // rows [m0, m0 + TM) of expert e, weight rows from 16 cb0 on; holds: a bit per row
-// that holds a pair
+// that holds a pair; rows before m0 + skip are left to another workgroup
 struct Holds { uint64_t r0, r64, r128, r192; };   // not an array: those end in LDS
 
 template <bool XMX, int TM>
 __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0, int64_t cb0,
-                                         int64_t e, Holds holds, int dma_scales) {
+                                         int64_t e, Holds holds, int skip, int dma_scales) {
   constexpr int WN = 4, NW = 8;
   constexpr int MB = TM / 32, NB = kTileN / 16 / WN;        // 16-row blocks of a wave
   constexpr int WROWB = XMX ? 128 : 32;                     // LDS bytes of a weight row
@@ -711,7 +711,7 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
     const int row = spot((wm * MB + i) * 16 + r);
-    if (row > m_last) continue;
+    if (row > m_last || row < skip) continue;
     const bool holds_pair = mine[i / 4] >> (row % 64) & 1;
     const int64_t at = (m0 + row) * out_cols;
     if (p.silu_mul) {
@@ -763,8 +763,8 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, i
   int used = m_tiles, whole = m_tiles, pieces = 1;   // tiles with rows; those taken whole
   if (tail) {
     if (p.tile_expert) {
-      used = 0;
-      for (int t0 = 0; t0 < m_tiles; t0 += 64) {
+      used = 0;   // from the end, where the entries without an expert are
+      for (int t0 = (m_tiles - 1) / 64 * 64; t0 >= 0 && used == 0; t0 -= 64) {
         const int t = t0 + lane;
         const int te = t < m_tiles ? p.tile_expert[t] : -1;
         const uint64_t has = __ballot(te >= 0 && te < p.E);
@@ -812,12 +812,17 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, i
   // the rows behind the tile that these take hold no pair
   const int done = live > 128 ? 256 : live > 64 ? 128 : live > 0 ? 64 : 0;
   const int blocks = (int)min((int64_t)kTileN / 16, p.N / 16 - cb0) / (p.silu_mul ? 2 : 1);
-  const int64_t first = p.silu_mul ? cb0 / 2 : cb0, cols = p.silu_mul ? p.N / 2 : p.N;
+  const int64_t block0 = p.silu_mul ? cb0 / 2 : cb0, cols = p.silu_mul ? p.N / 2 : p.N;
   for (int row = done + threadIdx.x / 64; row < rows; row += 8)
-    if (lane < blocks * 4) store_out(p, (m0 + row) * cols + first * 16 + lane * 4, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
-  if (TOP == 256 && done == 256) mx4_tile<XMX, TOP>(p, lds, m0, cb0, e, holds, dma_scales);
-  else if (TOP >= 128 && done == 128) mx4_tile<XMX, TOP >= 128 ? 128 : 64>(p, lds, m0, cb0, e, holds, dma_scales);
-  else if (done == 64) mx4_tile<XMX, 64>(p, lds, m0, cb0, e, holds, dma_scales);
+    if (lane < blocks * 4) store_out(p, (m0 + row) * cols + block0 * 16 + lane * 4, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
+  // whole tiles of whole rows are the fast ones: where the rows end inside the last tile it
+  // starts early (1000 rows, 8192 x 7168, MX4 x: 66 -> 45 us; bf16 x: 163 -> 112)
+  const int early = !p.tile_expert && rows < done && p.M >= done ? done - rows : 0;
+  const int64_t from = m0 - early;
+  if (TOP == 256 && done == 256) mx4_tile<XMX, TOP>(p, lds, from, cb0, e, holds, early, dma_scales);
+  else if (TOP >= 128 && done == 128)
+    mx4_tile<XMX, TOP >= 128 ? 128 : 64>(p, lds, from, cb0, e, holds, early, dma_scales);
+  else if (done == 64) mx4_tile<XMX, 64>(p, lds, from, cb0, e, holds, early, dma_scales);
 }
 
 template <bool XMX, int TM>

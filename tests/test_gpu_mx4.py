@@ -155,7 +155,7 @@ DENSE = [(1, 16, 32), (1, 2112, 736), (5, 48, 96), (16, 64, 256), (17, 80, 288),
          (257, 1040, 768),
          # past 64 tiles of 64 x 256
          (64, 16640, 736), (70, 16400, 288), (130, 8208, 544), (520, 2064, 1312), (1100, 1040, 2080),
-         (700, 1536, 2560)]
+         (700, 1536, 2560), (1000, 1056, 1568), (4129, 288, 96)]
 
 
 @pytest.mark.parametrize("shape", DENSE, ids=lambda s: "x".join(map(str, s)))
