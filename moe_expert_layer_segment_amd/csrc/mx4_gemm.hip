@@ -378,12 +378,12 @@ constexpr int tile_lds(bool xmx, int tm) {
 }
 
 // rows [m0, m0 + TM) of expert e, weight rows from 16 cb0 on; holds: a bit per row
-// that holds a pair; rows before m0 + skip are left to another workgroup
+// that holds a pair; DS: scales by DMA; rows before m0 + skip are left to another workgroup
 struct Holds { uint64_t r0, r64, r128, r192; };   // not an array: those end in LDS
 
-template <bool XMX, int TM>
+template <bool XMX, int TM, bool DS>
 __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0, int64_t cb0,
-                                         int64_t e, Holds holds, int skip, int dma_scales) {
+                                         int64_t e, Holds holds, int skip) {
   constexpr int WN = 4, NW = 8;
   constexpr int MB = TM / 32, NB = kTileN / 16 / WN;        // 16-row blocks of a wave
   constexpr int WROWB = XMX ? 128 : 32;                     // LDS bytes of a weight row
@@ -474,10 +474,13 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
   };
 
   // Scales of tiles 2 grp and 2 grp + 1, a row per thread.  Beside bf16 x they take
-  // the DMA (4 bytes a row) where rows of them are aligned to words; MX4's 16 bytes a
-  // row go through registers (by DMA they took a third more requests to the L2, and
-  // 347 instead of 326 us), loaded behind the barrier of an even tile and stored ahead
-  // of that of the odd one; so do those at the end of a row, with 2^0 behind it.
+  // the DMA (DS; 4 bytes a row) where rows of them are aligned to words.  Otherwise
+  // they go through registers, loaded behind the barrier of an even tile and stored
+  // ahead of that of the odd one, at the price of waiting there for the DMA of both
+  // tiles ahead (2048 rows, 4096 x 4128: 73 us; 4096 x 4096 64 so and 67 through
+  // registers, 94 with the address of each row worked out tile by tile).  MX4's 16 bytes
+  // a row always do: by DMA they took a third more requests to the L2, and 347 instead of
+  // 326 us.  So do those at the end of a row, with 2^0 behind it.
   // (a wave's 64 rows are all of x or all of the weights: a uniform base)
   const int s_lane = min(wave * 64 + lane, SROWS - 1);
   const bool s_of_x = XMX && wave < TM / 64;
@@ -664,10 +667,10 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
             wait_dma_barrier<0>();
             if (!(t & 1) && t + 2 < tiles) scales_load_end(t / 2 + 1);
           } else {
-            if constexpr (XMX && kMode == kOdd) scales_store((t + 1) / 2);
+            if constexpr (!DS && kMode == kOdd) scales_store((t + 1) / 2);
             wait_dma_barrier<(RING - 2) * DMAS>();
-            if constexpr (!XMX && kMode == kEven) scales_dma(t / 2 + 1);
-            if constexpr (XMX && kMode == kEven) scales_load(t / 2 + 1);
+            if constexpr (DS && kMode == kEven) scales_dma(t / 2 + 1);
+            if constexpr (!DS && kMode == kEven) scales_load(t / 2 + 1);
           }
           read_first(next, ahead, t + 1);
         }
@@ -696,7 +699,7 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) x[i] = read_x(0, i, 0);
   int t = 0;
-  if (all_rows && (XMX || dma_scales)) {
+  if (all_rows) {
     // tile t + 1 sends for tile t + 1 + RING, tile t for the scales of t + 2 and t + 3
     for (; (t + 2 + RING) * KB <= nblk; t += 2) {
       tile(t, std::integral_constant<int, kEven>{});
@@ -752,9 +755,9 @@ constexpr int kRound = 256;
 constexpr int64_t kTailTiles = 16 * kRound;   // with more, a share of a round does not count
 
 // TOP rows are one entry of tile_expert
-template <bool XMX, int TOP>
+template <bool XMX, int TOP, bool DS>
 __global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, int n_tiles, int pn,
-                                                       int n_patches, int tail, int dma_scales) {
+                                                       int n_patches, int tail) {
   __shared__ __attribute__((aligned(1024))) char lds[tile_lds(XMX, TOP)];
   const int lane = threadIdx.x & 63;
   const int pm = 32 / pn;
@@ -819,10 +822,10 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, i
   // starts early (1000 rows, 8192 x 7168, MX4 x: 66 -> 45 us; bf16 x: 163 -> 112)
   const int early = !p.tile_expert && rows < done && p.M >= done ? done - rows : 0;
   const int64_t from = m0 - early;
-  if (TOP == 256 && done == 256) mx4_tile<XMX, TOP>(p, lds, from, cb0, e, holds, early, dma_scales);
+  if (TOP == 256 && done == 256) mx4_tile<XMX, TOP, DS>(p, lds, from, cb0, e, holds, early);
   else if (TOP >= 128 && done == 128)
-    mx4_tile<XMX, TOP >= 128 ? 128 : 64>(p, lds, from, cb0, e, holds, early, dma_scales);
-  else if (done == 64) mx4_tile<XMX, 64>(p, lds, from, cb0, e, holds, early, dma_scales);
+    mx4_tile<XMX, TOP >= 128 ? 128 : 64, DS>(p, lds, from, cb0, e, holds, early);
+  else if (done == 64) mx4_tile<XMX, 64, DS>(p, lds, from, cb0, e, holds, early);
 }
 
 template <bool XMX, int TM>
@@ -835,10 +838,17 @@ static hipError_t tiled(const Mx4Gemm& p, hipStream_t stream) {
   // parts of tiles fill a round at most: 16 patches, and one more for each part of the
   // columns in which their rows end
   const int64_t patches = ceil_div(m_tiles, 32 / pn) * n_patches + (tail ? 16 + 2 * n_patches : 0);
-  const bool dma_scales = p.K % 128 == 0 && reinterpret_cast<uintptr_t>(p.w_scale) % 4 == 0;
-  const auto kernel = mx4_tile_kernel<XMX, TM>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(ceil_div(patches, 8) * 256)), dim3(512), 0, stream, p,
-                     (int)m_tiles, (int)n_tiles, pn, (int)n_patches, (int)tail, (int)dma_scales);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(ceil_div(patches, 8) * 256)), dim3(512), 0, stream, p,
+                       (int)m_tiles, (int)n_tiles, pn, (int)n_patches, (int)tail);
+  };
+  if constexpr (XMX) {
+    go(mx4_tile_kernel<XMX, TM, false>);
+  } else {
+    const bool dma_scales = p.K % 128 == 0 && reinterpret_cast<uintptr_t>(p.w_scale) % 4 == 0;
+    if (dma_scales) go(mx4_tile_kernel<XMX, TM, true>);
+    else go(mx4_tile_kernel<XMX, TM, false>);
+  }
   return hipGetLastError();
 }
 
