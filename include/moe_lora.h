@@ -511,8 +511,8 @@ int moe_lora_mx4_dequantize(int64_t num_rows, int32_t cols, int32_t dtype, const
  * more, which are infinities there); sums are fp32, rounded once.  A row's result
  * depends on that row alone: what padding rows hold reaches no other row.
  * A workgroup covers rows of one tile_expert entry, so block_m is also the most
- * rows that share one read of a weight: 16 for a few rows per expert, up to 256
- * for many (a multiple of 64 at least from 64 rows per expert on).
+ * rows that share one read of a weight: 16 for a few rows per expert, 64 from about
+ * 32 rows per expert on, 128 or 256 for many.
  * in_features: a multiple of 32, at most 2^20; out_features: of 16 (32 with
  * silu_mul), at most 2^24; out_features * in_features < 2^37 and
  * num_rows / 16 * out_features / 64 < 2^24 (else MOE_LORA_ERR_UNSUPPORTED).  x, w

@@ -754,10 +754,10 @@ __device__ __forceinline__ void mx4_tile(const Mx4Gemm& p, char* lds, int64_t m0
 constexpr int kRound = 256;
 constexpr int64_t kTailTiles = 16 * kRound;   // with more, a share of a round does not count
 
-// TOP rows are one entry of tile_expert
+// per_entry: tiles of an entry of tile_expert (three of 64 rows for block_m = 192)
 template <bool XMX, int TOP, bool DS>
 __global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, int n_tiles, int pn,
-                                                       int n_patches, int tail) {
+                                                       int n_patches, int per_entry, int tail) {
   __shared__ __attribute__((aligned(1024))) char lds[tile_lds(XMX, TOP)];
   const int lane = threadIdx.x & 63;
   const int pm = 32 / pn;
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, i
       used = 0;   // from the end, where the entries without an expert are
       for (int t0 = (m_tiles - 1) / 64 * 64; t0 >= 0 && used == 0; t0 -= 64) {
         const int t = t0 + lane;
-        const int te = t < m_tiles ? p.tile_expert[t] : -1;
+        const int te = t < m_tiles ? p.tile_expert[(uint32_t)t / (uint32_t)per_entry] : -1;
         const uint64_t has = __ballot(te >= 0 && te < p.E);
         if (has) used = t0 + 64 - __clzll(has);
       }
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(512) mx4_tile_kernel(Mx4Gemm p, int m_tiles, i
   const int64_t cb0 = (int64_t)nt * (kTileN / 16);
   int64_t e = 0;
   if (p.tile_expert) {
-    e = __builtin_amdgcn_readfirstlane(p.tile_expert[part ? whole + mt / pieces : mt]);
+    e = __builtin_amdgcn_readfirstlane(p.tile_expert[(uint32_t)(part ? whole + mt / pieces : mt) / (uint32_t)per_entry]);
     if (e < 0 || e >= p.E) return;
   }
   const int rows = (int)min((int64_t)span, p.M - m0);
@@ -840,7 +840,8 @@ static hipError_t tiled(const Mx4Gemm& p, hipStream_t stream) {
   const int64_t patches = ceil_div(m_tiles, 32 / pn) * n_patches + (tail ? 16 + 2 * n_patches : 0);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(ceil_div(patches, 8) * 256)), dim3(512), 0, stream, p,
-                       (int)m_tiles, (int)n_tiles, pn, (int)n_patches, (int)tail);
+                       (int)m_tiles, (int)n_tiles, pn, (int)n_patches,
+                       (int)(p.tile_expert ? p.BM / TM : 1), (int)tail);
   };
   if constexpr (XMX) {
     go(mx4_tile_kernel<XMX, TM, false>);

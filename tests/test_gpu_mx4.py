@@ -185,6 +185,9 @@ GROUPED = [  # experts of the tiles (-1: unused), block_m, N, K
     ([0, 0, 2, 1, 3] * 8 + [-1], 64, 544, 800),
     ([1, 1, 3, 0, 2] * 4 + [-1], 128, 544, 2304),
     ([3, 2, 2, 0, 1, 3, 0], 256, 800, 1056),
+    ([1, 0, 0, -1], 48, 64, 256),
+    ([2, 0, 1, -1], 96, 112, 320),
+    ([2, 0, 1, 3] * 6 + [-1], 192, 528, 544),
 ]
 
 
@@ -271,7 +274,7 @@ def test_padding_rows_are_not_read(kind, bm):
 
 MANY = [  # block_m, tiles in use and behind them, N: past 256 workgroups, whose last round is split
     (256, 18, 2, 4096), (256, 21, 0, 4096), (256, 25, 1, 4096), (256, 31, 1, 2064), (128, 20, 3, 4096),
-    (256, 36, 1, 1040), (128, 1, 0, 16), (256, 2, 1, 528), (64, 30, 2, 1040), (64, 70, 1, 272)]
+    (256, 36, 1, 1040), (128, 1, 0, 16), (256, 2, 1, 528), (64, 30, 2, 1040), (64, 70, 1, 272), (192, 24, 2, 1040), (192, 3, 1, 96)]
 
 
 @pytest.mark.parametrize("case", MANY, ids=lambda c: f"b{c[0]}t{c[1]}N{c[3]}")
