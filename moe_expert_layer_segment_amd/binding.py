@@ -700,10 +700,11 @@ def moe_lora_permute(x: torch.Tensor, align_out: Dict[str, torch.Tensor], top_k:
     H = x.shape[1]
     if out is None:
         out = torch.empty((cap, H), dtype=x.dtype, device=x.device)
-    _need(out, "out", x.dtype, x.device)
-    if out.shape != (cap, H):
-        raise ValueError(f"out must be {(cap, H)}, got {tuple(out.shape)}")
-    _apart(out, x)
+    else:
+        _need(out, "out", x.dtype, x.device)
+        if out.shape != (cap, H):
+            raise ValueError(f"out must be {(cap, H)}, got {tuple(out.shape)}")
+        _apart(out, x)
     _launch("moe_lora_permute", x.device, lib().moe_lora_permute, T, top_k, H, dt, cap, _at(x),
             _at(align_out["sorted_pair_ids"]), _at(align_out["pair_rows"]),
             _at(align_out["num_rows_padded"]), _at(out))
@@ -719,7 +720,8 @@ def moe_lora_permute_backward(d_rows: torch.Tensor, align_out: Dict[str, torch.T
     H = d_rows.shape[1]
     if dx is None:
         dx = torch.empty((T, H), dtype=out_dtype or d_rows.dtype, device=d_rows.device)
-    _token_out(dx, "dx", T, H, d_rows, out_dtype)
+    else:
+        _token_out(dx, "dx", T, H, d_rows, out_dtype)
     _launch("moe_lora_permute_backward", d_rows.device, lib().moe_lora_permute_backward, T, top_k, H,
             _row_dtype(d_rows, "d_rows"), _row_dtype(dx, "dx"), cap, _at(d_rows),
             _at(align_out["pair_rows"]), _at(dx))
@@ -752,7 +754,8 @@ def moe_lora_unpermute(rows: torch.Tensor, align_out: Dict[str, torch.Tensor], t
         _pair_weights(topk_weights, T, top_k, rows.device)
     if y is None:
         y = torch.empty((T, H), dtype=out_dtype or rows.dtype, device=rows.device)
-    _token_out(y, "y", T, H, rows, out_dtype)
+    else:
+        _token_out(y, "y", T, H, rows, out_dtype)
     _launch("moe_lora_unpermute", rows.device, lib().moe_lora_unpermute, T, top_k, H,
             _row_dtype(rows, "rows"), _row_dtype(y, "y"), cap, _at(rows), _at(align_out["pair_rows"]),
             _at(topk_weights), _at(y))
@@ -850,17 +853,19 @@ def moe_lora_mx4_quantize(x: torch.Tensor, num_rows_used: Optional[torch.Tensor]
     if K <= 0 or K % 32:
         raise ValueError("the last axis of x must be a multiple of 32")
     lead, dev = tuple(x.shape[:-1]), x.device
+    given = codes is not None or scales is not None
     if codes is None:
         codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
     if scales is None:
         scales = torch.empty((*lead, K // 32), dtype=torch.uint8, device=dev)
-    _mx4_pair(codes, scales, "the output", dev)
-    if codes.shape != (*lead, K // 2):
-        raise ValueError(f"codes must be {(*lead, K // 2)}, got {tuple(codes.shape)}")
+    if given:
+        _mx4_pair(codes, scales, "the output", dev)
+        if codes.shape != (*lead, K // 2):
+            raise ValueError(f"codes must be {(*lead, K // 2)}, got {tuple(codes.shape)}")
+        _apart(codes, x, scales)
+        _apart(scales, x)
     if num_rows_used is not None:
         _need(num_rows_used, "num_rows_used", torch.int32, dev, 1)
-    _apart(codes, x, scales)
-    _apart(scales, x)
     _launch("moe_lora_mx4_quantize", dev, lib().moe_lora_mx4_quantize, x.numel() // K, K, dt, _at(x),
             _at(num_rows_used), _at(codes), _at(scales))
     return codes, scales
@@ -874,10 +879,11 @@ def moe_lora_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor,
     shape = (*codes.shape[:-1], K)
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=codes.device)
-    _need(out, "out", out_dtype, codes.device)
-    if out.shape != shape:
-        raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
-    _apart(out, codes, scales)
+    else:
+        _need(out, "out", out_dtype, codes.device)
+        if out.shape != shape:
+            raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
+        _apart(out, codes, scales)
     if K == 0:
         return out
     _launch("moe_lora_mx4_dequantize", codes.device, lib().moe_lora_mx4_dequantize, out.numel() // K, K,
@@ -925,10 +931,11 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
     cols = N // 2 if silu_mul else N
     if out is None:
         out = torch.empty((M, cols), dtype=out_dtype or torch.bfloat16, device=dev)
-    _need(out, "out", out_dtype, dev)
-    if out.shape != (M, cols):
-        raise ValueError(f"out must be {(M, cols)}, got {tuple(out.shape)}")
-    _apart(out, x, x_scales, w_codes, w_scales)
+    else:
+        _need(out, "out", out_dtype, dev)
+        if out.shape != (M, cols):
+            raise ValueError(f"out must be {(M, cols)}, got {tuple(out.shape)}")
+        _apart(out, x, x_scales, w_codes, w_scales)
     if M == 0:
         return out
     a.struct_size = ctypes.sizeof(Mx4GemmArgs)
