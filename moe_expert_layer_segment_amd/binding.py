@@ -262,7 +262,8 @@ def moe_lora_align(topk_ids: torch.Tensor, token_lora_mapping: torch.Tensor,
     """Bucket (token, expert) pairs by (expert, adapter); returns the align outputs.
 
     ``pair_rows``: also write ``pair_rows`` (int32 [T * k], the row of each pair or
-    -1), which moe_lora_permute and moe_lora_unpermute need."""
+    -1), which moe_lora_permute and moe_lora_unpermute need.  Buffers in ``out`` may be
+    larger than this batch needs; ``num_pairs`` in the result says how many pairs it has."""
     dev = topk_ids.device
     T, k = topk_ids.shape
     _need(topk_ids, "topk_ids", torch.int32)
@@ -301,6 +302,7 @@ def moe_lora_align(topk_ids: torch.Tensor, token_lora_mapping: torch.Tensor,
     _check(st, "moe_lora_align")
     out["capacity"] = cap
     out["block_m"] = block_m
+    out["num_pairs"] = T * k
     return out
 
 
@@ -630,20 +632,26 @@ def _row_dtype(t, name, also=()):
     raise TypeError(f"unsupported dtype of {name}: {dtype}")
 
 
+def _num_pairs(align_out):
+    """Pairs of the batch: pair_rows may be a buffer of more."""
+    n = align_out.get("num_pairs")
+    return align_out["pair_rows"].numel() if n is None else int(n)
+
+
 def _rows_layout(align_out, top_k, dev, num_rows=None):
     """(tokens, rows of the layout) after checking its arrays."""
     if "pair_rows" not in align_out:
         raise ValueError("the layout has no pair_rows (moe_lora_align(..., pair_rows=True))")
-    pr = align_out["pair_rows"]
-    _need(pr, "pair_rows", torch.int32, dev)
+    pairs = _num_pairs(align_out)
+    _need(align_out["pair_rows"], "pair_rows", torch.int32, dev, pairs)
     cap = int(align_out["capacity"])
     _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, cap)
     _need(align_out["num_rows_padded"], "num_rows_padded", torch.int32, dev, 1)
-    if top_k <= 0 or (cap > 0 and pr.numel() % top_k):
+    if top_k <= 0 or (cap > 0 and pairs % top_k):
         raise ValueError("pair_rows is not [T, top_k]")
     if num_rows is not None and num_rows != cap:
         raise ValueError(f"the layout has {cap} rows, got {num_rows}")
-    return (pr.numel() // top_k if cap > 0 else 0), cap
+    return (pairs // top_k if cap > 0 else 0), cap
 
 
 def _apart(out, *inputs):
@@ -924,10 +932,10 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
             raise ValueError("x must hold whole tiles of block_m rows")
         _need(align_out["tile_expert"], "tile_expert", torch.int32, dev, M // a.block_m)
         a.tile_expert = align_out["tile_expert"].data_ptr()
-        if "pair_rows" in align_out:   # its length tells pairs from padding
+        if "pair_rows" in align_out:   # ids past the pairs are padding
             _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, M)
             a.sorted_pair_ids = align_out["sorted_pair_ids"].data_ptr()
-            a.num_pairs = align_out["pair_rows"].numel()
+            a.num_pairs = _num_pairs(align_out)
     cols = N // 2 if silu_mul else N
     if out is None:
         out = torch.empty((M, cols), dtype=out_dtype or torch.bfloat16, device=dev)

@@ -1,0 +1,57 @@
+"""Rows in expert order and MX4 products where a call's arguments, sizes or values
+leave the ordinary: reused buffers, weights that are not finite, every variant of the
+kernels, sizes past one launch.  Products are compared as in test_gpu_mx4, within its
+bounds."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import rows_mx4_oracle as ro
+from gpu_helpers import say
+from moe_expert_layer_segment_amd import binding
+from test_gpu_mx4 import activations, check_product, np64, weights
+
+pytestmark = pytest.mark.gpu
+
+
+def empty_layout(T, k, E, block_m):
+    """Buffers of moe_lora_align for up to T tokens, filled with what no layout holds."""
+    cap = binding.moe_lora_align_capacity_rows(T, k, E, 0, block_m)
+    i32 = lambda n: torch.full((n,), -7, dtype=torch.int32, device="cuda")  # noqa: E731
+    return dict(sorted_pair_ids=i32(cap), tile_expert=i32(cap // block_m), tile_lora=i32(cap // block_m),
+                expert_tile_offsets=i32(E + 1), num_rows_padded=i32(1), pair_rows=i32(T * k))
+
+
+def some_ids(T, k, E, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int().cuda()
+
+
+def no_slots(T):
+    return torch.full((max(T, 1),), -1, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mx4"])
+@pytest.mark.parametrize("bm", [16, 64])
+def test_layout_in_buffers_of_a_larger_batch(kind, bm):
+    """The results are those of a layout of the batch's own size: padding rows (NaN
+    here) give zeros, and the rows sum up to the batch's tokens."""
+    k, E, N, K = 2, 5, 96, 160
+    out = empty_layout(300, k, E, bm)
+    wc, ws, _ = weights(E, N, K, 31)
+    for T in (300, 41, 1):
+        say(f"larger buffers {kind} block_m {bm} T {T}")
+        ids = some_ids(T, k, E, T)
+        own = binding.moe_lora_align(ids, no_slots(T), None, E, 0, bm, pair_rows=True)
+        al = binding.moe_lora_align(ids, no_slots(T), None, E, 0, bm, out=out, pair_rows=True)
+        cap, used = al["capacity"], int(al["num_rows_padded"].cpu()[0])
+        assert cap == own["capacity"] and al["num_pairs"] == T * k
+        x, xs, _ = activations(cap, K, kind, 32)
+        pad = al["sorted_pair_ids"][:cap] >= T * k
+        (x if kind == "bf16" else xs)[pad] = float("nan") if kind == "bf16" else 255
+        z, z2 = (binding.moe_lora_mx4_gemm(x, wc, ws, x_scales=xs, align_out=a, out_dtype=torch.float32)
+                 for a in (al, own))
+        assert torch.equal(z[:used], z2[:used]) and bool((z[:used][pad[:used]] == 0).all())
+        w = torch.rand(T, k, device="cuda")
+        y, y2 = (binding.moe_lora_unpermute(z, a, k, w) for a in (al, own))
+        assert y.shape == (T, N) and torch.equal(y, y2)
