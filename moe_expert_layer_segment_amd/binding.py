@@ -262,8 +262,10 @@ def moe_lora_align(topk_ids: torch.Tensor, token_lora_mapping: torch.Tensor,
     """Bucket (token, expert) pairs by (expert, adapter); returns the align outputs.
 
     ``pair_rows``: also write ``pair_rows`` (int32 [T * k], the row of each pair or
-    -1), which moe_lora_permute and moe_lora_unpermute need.  Buffers in ``out`` may be
-    larger than this batch needs; ``num_pairs`` in the result says how many pairs it has."""
+    -1), which moe_lora_permute and moe_lora_unpermute need; they are written whenever
+    ``out`` holds a buffer for them, so that none stay from a batch before.  Buffers in
+    ``out`` may be larger than this batch needs; ``num_pairs`` in the result says how many
+    pairs it has."""
     dev = topk_ids.device
     T, k = topk_ids.shape
     _need(topk_ids, "topk_ids", torch.int32)
@@ -278,6 +280,7 @@ def moe_lora_align(topk_ids: torch.Tensor, token_lora_mapping: torch.Tensor,
             tile_lora=torch.empty(max(cap // block_m, 1), dtype=torch.int32, device=dev),
             expert_tile_offsets=torch.empty(num_experts + 1, dtype=torch.int32, device=dev),
             num_rows_padded=torch.empty(1, dtype=torch.int32, device=dev))
+    pair_rows = pair_rows or "pair_rows" in out
     if pair_rows:
         if "pair_rows" not in out:
             out["pair_rows"] = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)

@@ -55,3 +55,16 @@ def test_layout_in_buffers_of_a_larger_batch(kind, bm):
         w = torch.rand(T, k, device="cuda")
         y, y2 = (binding.moe_lora_unpermute(z, a, k, w) for a in (al, own))
         assert y.shape == (T, N) and torch.equal(y, y2)
+
+
+def test_layout_reused_without_pair_rows():
+    """Rows placed by a reused layout are those of its last batch."""
+    T, k, E, H = 90, 2, 6, 64
+    al = binding.moe_lora_align(some_ids(T, k, E, 1), no_slots(T), None, E, 0, 16, pair_rows=True)
+    ids = some_ids(T, k, E, 2)
+    binding.moe_lora_align(ids, no_slots(T), None, E, 0, 16, out=al)
+    own = binding.moe_lora_align(ids, no_slots(T), None, E, 0, 16, pair_rows=True)
+    x = torch.randn(T, H, device="cuda")
+    used = int(own["num_rows_padded"].cpu()[0])
+    assert torch.equal(al["pair_rows"], own["pair_rows"])
+    assert torch.equal(binding.moe_lora_permute(x, al, k)[:used], binding.moe_lora_permute(x, own, k)[:used])

@@ -85,3 +85,17 @@ def test_pairs_of_a_layout_made_by_hand(recorder):
     assert recorder.args("moe_lora_permute")[:2] == [4, 2]
     with pytest.raises(ValueError):
         binding.moe_lora_permute(dev(5, 8), dict(al, num_pairs=10), 2)
+
+
+def test_a_reused_layout_keeps_no_pair_rows_of_another_batch(recorder):
+    """align without pair_rows into a layout that has them writes them, too."""
+    al = align(6, 2, pair_rows=True)
+    recorder.calls.clear()
+    assert align(4, 2, out=al) is al
+    assert recorder.args("moe_lora_align_pair_rows")[13].value == al["pair_rows"].data_ptr()
+    assert al["num_pairs"] == 8
+    with pytest.raises(ValueError):
+        align(4, 2, out=dict(al, pair_rows=i32(7)))
+    recorder.calls.clear()
+    assert "pair_rows" not in align(4, 2)
+    recorder.args("moe_lora_align")
