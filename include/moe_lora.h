@@ -502,8 +502,9 @@ int moe_lora_mx4_dequantize(int64_t num_rows, int32_t cols, int32_t dtype, const
  *            num_experts) (-1 past the end) are left as they were.  NULL: one weight
  *            (num_experts == 1) for every row, any num_rows.
  *   sorted_pair_ids [num_rows] of moe_lora_align and num_pairs = num_tokens * top_k, or
- *            NULL.  With them padding rows (entries outside [0, num_pairs)) are not
- *            read and get zeros; most rows of a small batch are padding.
+ *            NULL.  With them padding rows (entries outside [0, num_pairs)) get zeros,
+ *            whatever x and W hold, and few of them are read; most rows of a small
+ *            batch are padding.
  *   out      [num_rows, out_features] (silu_mul: out_features / 2), BF16 or F32.
  *
  * MX4 x goes through the matrix cores' own 4-bit products, BF16 x multiplies the

@@ -913,7 +913,7 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
     Otherwise w_codes [E, N, K/2], w_scales [E, N, K/32] and x [capacity, K] in
     expert order (moe_lora_permute); rows behind the last used tile are left as they
     are in ``out`` (undefined when it is not given).  With ``pair_rows`` in align_out
-    padding rows are not read and get zeros.
+    padding rows get zeros, whatever x and the weights hold.
     x: bfloat16, or MX4 codes [M, K/2] with ``x_scales`` [M, K/32].  ``out`` /
     ``out_dtype``: bfloat16 (the default) or float32."""
     K = _mx4_pair(w_codes, w_scales, "w")

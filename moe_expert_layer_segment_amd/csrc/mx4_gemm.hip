@@ -274,10 +274,12 @@ mx4_stream_kernel(Mx4Gemm p, int row_groups, int col_groups, int spread) {
     multiply(f);
   }
 
+  // padding rows give zeros: their x is, but zero times a NaN or infinite weight is not
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) sums[wave][mb * NB + nb][lane] = acc[mb][nb];
+    for (int nb = 0; nb < NB; ++nb)
+      sums[wave][mb * NB + nb][lane] = live[mb] ? acc[mb][nb] : floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
   auto total = [&](int tile) {
     floatx4 v = sums[0][tile][lane];

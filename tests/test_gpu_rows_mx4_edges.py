@@ -68,3 +68,32 @@ def test_layout_reused_without_pair_rows():
     used = int(own["num_rows_padded"].cpu()[0])
     assert torch.equal(al["pair_rows"], own["pair_rows"])
     assert torch.equal(binding.moe_lora_permute(x, al, k)[:used], binding.moe_lora_permute(x, own, k)[:used])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mx4"])
+@pytest.mark.parametrize("bm", [16, 32, 48, 64, 128, 192, 256])
+@pytest.mark.parametrize("tokens", [9, 2000])
+def test_padding_rows_beside_weights_that_are_not_finite(kind, bm, tokens):
+    """Padding rows get zeros also where a weight is NaN (a scale byte of 255, as the
+    quantisation gives it) or, beside bf16 x, past the largest finite value (codes of 4
+    and 6 under 254); every other column of the rows that hold a pair keeps its bits."""
+    k, E, N, K = 2, 5, 160, 544
+    say(f"weights that are not finite {kind} block_m {bm} T {tokens}")
+    al = binding.moe_lora_align(some_ids(tokens, k, E, 7), no_slots(tokens), None, E, 0, bm, pair_rows=True)
+    used, M = int(al["num_rows_padded"].cpu()[0]), al["capacity"]
+    live = (al["sorted_pair_ids"][:M] < tokens * k)[:used]
+    assert not bool(live.all())
+    wc, ws, _ = weights(E, N, K, 33)
+    x, xs, _ = activations(M, K, kind, 34)
+    bad = ws.clone()
+    bad[:, 5, 3], bad[:, 90, K // 32 - 1] = 255, 254
+    wc[:, 90, -1] = 0x77   # two sixes
+    for silu in (False, True):
+        y, clean = (binding.moe_lora_mx4_gemm(x, wc, w, x_scales=xs, align_out=al, silu_mul=silu,
+                                              out_dtype=torch.float32)[:used] for w in (bad, ws))
+        assert bool((y[~live] == 0).all())
+        hit = [5, 90 - 80] if silu else [5, 90]
+        assert bool(torch.isnan(y[live][:, 5]).all())
+        keep = torch.ones(y.shape[1], dtype=torch.bool, device="cuda")
+        keep[hit] = False
+        assert torch.equal(y[:, keep], clean[:, keep])
