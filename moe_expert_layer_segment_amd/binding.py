@@ -974,7 +974,8 @@ def run_mx4_layer(inputs: dict, activations: str = "bf16", block_m: Optional[int
     gate_up product with SiLU * up -> down product -> unpermute.
 
     ``inputs``: x [T, H] bfloat16, topk_ids, topk_weights, and the weights
-    w_gate_up_mx4, w_down_mx4, each a (codes, scales) pair of moe_lora_mx4_quantize.
+    w_gate_up_mx4 [E, 2I, H], w_down_mx4 [E, H, I], each a (codes, scales) pair of
+    moe_lora_mx4_quantize.
     ``activations``: "bf16", or "mx4" to quantise x and the activations between the
     products as well."""
     if activations not in ("bf16", "mx4"):
@@ -982,7 +983,12 @@ def run_mx4_layer(inputs: dict, activations: str = "bf16", block_m: Optional[int
     x, ids, w = inputs["x"], inputs["topk_ids"], inputs["topk_weights"]
     T, k = ids.shape
     gu, down = inputs["w_gate_up_mx4"], inputs["w_down_mx4"]
+    H, I = _mx4_pair(*gu, "w_gate_up"), _mx4_pair(*down, "w_down")
     E = gu[0].shape[0]
+    if gu[0].shape != (E, 2 * I, H // 2) or down[0].shape != (E, H, I // 2) or x.shape != (T, H):
+        raise ValueError(f"x {tuple(x.shape)}, w_gate_up {tuple(gu[0].shape)} and w_down "
+                         f"{tuple(down[0].shape)} are not of one layer of {T} tokens: codes "
+                         "[E, 2I, H/2] and [E, H, I/2]")
     if block_m is None:
         block_m = mx4_block_m(T, k, E)
     slots = torch.full((max(T, 1),), -1, dtype=torch.int32, device=x.device)

@@ -99,3 +99,34 @@ def test_a_reused_layout_keeps_no_pair_rows_of_another_batch(recorder):
     recorder.calls.clear()
     assert "pair_rows" not in align(4, 2)
     recorder.args("moe_lora_align")
+
+
+def mx4(E, N, K):
+    return dev(E, N, K // 2, dtype=torch.uint8), dev(E, N, K // 32, dtype=torch.uint8)
+
+
+def layer(T=5, k=2, E=8, H=96, I=64, **over):  # noqa: E741
+    d = dict(x=dev(T, H, dtype=torch.bfloat16), topk_ids=i32(T, k), topk_weights=dev(T, k),
+             w_gate_up_mx4=mx4(E, 2 * I, H), w_down_mx4=mx4(E, H, I))
+    d.update(over)
+    return d
+
+
+@pytest.mark.parametrize("activations", ["bf16", "mx4"])
+def test_mx4_layer_takes_weights_of_one_layer(recorder, activations):
+    assert binding.run_mx4_layer(layer(), activations).shape == (5, 96)
+    assert binding.run_mx4_layer(layer(T=0), activations).shape == (0, 96)
+    bad = [dict(w_down_mx4=mx4(7, 96, 64)),        # fewer experts: rows of the others stay unwritten
+           dict(w_down_mx4=mx4(9, 96, 64)),
+           dict(w_down_mx4=mx4(8, 128, 64)),       # another hidden
+           dict(w_down_mx4=mx4(8, 96, 32)),        # another inner width
+           dict(w_gate_up_mx4=mx4(8, 64, 96)),     # the gate alone
+           dict(w_gate_up_mx4=mx4(8, 128, 64)),
+           dict(x=dev(4, 96, dtype=torch.bfloat16)),
+           dict(x=dev(5, 64, dtype=torch.bfloat16)),
+           dict(w_down_mx4=tuple(t[0] for t in mx4(8, 96, 64)))]
+    for over in bad:
+        recorder.calls.clear()
+        with pytest.raises(ValueError):
+            binding.run_mx4_layer(layer(**over), activations)
+        assert not recorder.calls, over
