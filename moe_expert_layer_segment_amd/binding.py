@@ -184,6 +184,23 @@ def _need(t: torch.Tensor, name: str, dtype=None, device=None, numel=None):
         raise ValueError(f"{name} needs at least {numel} elements, has {t.numel()}")
 
 
+# torch.cuda.current_stream builds a Stream object, which takes as long as a small kernel
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(where, device, call, *args):
+    """call(*args, stream) with ``device`` as the current one, on its current stream."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = call(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, _raw_stream(index))
+    if status != OK:
+        _check(status, where)
+
+
 # ---------------------------------------------------------------------------
 # router
 # ---------------------------------------------------------------------------
@@ -298,11 +315,10 @@ def moe_lora_align(topk_ids: torch.Tensor, token_lora_mapping: torch.Tensor,
             _ptr(out["tile_expert"]), _ptr(out["tile_lora"]), _ptr(out["expert_tile_offsets"]),
             _ptr(out["num_rows_padded"])]
     if pair_rows:
-        st = lib().moe_lora_align_pair_rows(*args, _ptr(out["pair_rows"]), _ptr(workspace),
-                                            workspace.numel(), _stream())
+        _launch("moe_lora_align", dev, lib().moe_lora_align_pair_rows, *args, _ptr(out["pair_rows"]),
+                _ptr(workspace), workspace.numel())
     else:
-        st = lib().moe_lora_align(*args, _ptr(workspace), workspace.numel(), _stream())
-    _check(st, "moe_lora_align")
+        _launch("moe_lora_align", dev, lib().moe_lora_align, *args, _ptr(workspace), workspace.numel())
     out["capacity"] = cap
     out["block_m"] = block_m
     out["num_pairs"] = T * k
@@ -672,23 +688,6 @@ def _matrix(t, name, dev=None):
     _need(t, name, None, dev)
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
-
-
-# torch.cuda.current_stream builds a Stream object, which takes as long as a small kernel
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _launch(where, device, call, *args):
-    """call(*args, stream) with ``device`` as the current one, on its current stream."""
-    index = device.index
-    if index == torch.cuda.current_device():
-        status = call(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            status = call(*args, _raw_stream(index))
-    if status != OK:
-        _check(status, where)
 
 
 def _at(t: Optional[torch.Tensor]):

@@ -130,3 +130,35 @@ def test_mx4_layer_takes_weights_of_one_layer(recorder, activations):
         with pytest.raises(ValueError):
             binding.run_mx4_layer(layer(**over), activations)
         assert not recorder.calls, over
+
+
+def test_calls_go_to_the_device_of_their_tensors(recorder, monkeypatch):
+    """With another device current, each call switches to its tensors' and takes the
+    stream that is current there."""
+    entered, streams = [], []
+
+    class Switch:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            entered.append(self.index)
+
+        def __exit__(self, *exc):
+            entered.append("left")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "device", Switch)
+    monkeypatch.setattr(binding, "_raw_stream", lambda index: streams.append(index) or 77)
+    al = align(4, 2, pair_rows=True)
+    align(4, 2)
+    rows = binding.moe_lora_permute(dev(4, 64), al, 2)
+    y = binding.moe_lora_unpermute(rows, al, 2, dev(4, 2))
+    binding.moe_lora_permute_backward(rows, al, 2)
+    binding.moe_lora_unpermute_backward(y, rows, al, 2, dev(4, 2))
+    codes, scales = binding.moe_lora_mx4_quantize(rows)
+    binding.moe_lora_mx4_dequantize(codes, scales)
+    binding.moe_lora_mx4_gemm(codes, *mx4(8, 32, 64), x_scales=scales, align_out=al)
+    assert len(recorder.calls) == 9
+    assert entered == [None, "left"] * 9 and streams == [None] * 9     # the index of a host tensor
+    assert [args[-1] for _, args in recorder.calls] == [77] * 9
