@@ -516,8 +516,9 @@ int moe_lora_mx4_dequantize(int64_t num_rows, int32_t cols, int32_t dtype, const
  * 32 rows per expert on, 128 or 256 for many.
  * in_features: a multiple of 32, at most 2^20; out_features: of 16 (32 with
  * silu_mul), at most 2^24; out_features * in_features < 2^37 and
- * num_rows / 16 * out_features / 64 < 2^24 (else MOE_LORA_ERR_UNSUPPORTED).  x, w
- * and out 16-byte aligned.  No workspace.
+ * num_rows / 16 * out_features / 64 < 2^24, also with num_rows rounded up to 256 where
+ * block_m is no multiple of 32 and num_rows is 512 or more (else
+ * MOE_LORA_ERR_UNSUPPORTED).  x, w and out 16-byte aligned.  No workspace.
  */
 typedef struct moe_lora_mx4_gemm_args {
   size_t struct_size; /* sizeof(moe_lora_mx4_gemm_args) */

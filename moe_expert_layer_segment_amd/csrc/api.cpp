@@ -465,6 +465,8 @@ int moe_lora_mx4_gemm(const moe_lora_mx4_gemm_args* a, void* stream) {
   // threads of one launch are counted in 32 bits: 256 to 16 rows x 64 columns at the least
   if ((a->num_rows + 15) / 16 * ((a->out_features + 63) / 64) >= (int64_t(1) << 24))
     return MOE_LORA_ERR_UNSUPPORTED;
+  if (a->tile_expert && mx4_stream_blocks(a->num_rows, a->out_features, a->block_m) >= (int64_t(1) << 24))
+    return MOE_LORA_ERR_UNSUPPORTED;
   if (a->num_rows == 0) return MOE_LORA_OK;
   if (!a->x || !a->w || !a->w_scale || !a->out || (a->x_dtype == MOE_LORA_MX4 && !a->x_scale) ||
       misaligned(a->x) || misaligned(a->w) || misaligned(a->out))

@@ -86,6 +86,19 @@ struct Mx4Gemm {
   void* out;                         // [M, N], or [M, N / 2] with silu_mul
 };
 hipError_t launch_mx4_gemm(const Mx4Gemm& p, hipStream_t stream);
+// groups of rows that the streaming kernel launches: from kSpreadGroups on they come in
+// sixteens, two for each XCD
+constexpr int64_t kSpreadGroups = 32;
+inline int64_t mx4_stream_groups(int64_t groups) {
+  return groups >= kSpreadGroups ? (groups + 15) / 16 * 16 : groups;
+}
+// its workgroups of 64 columns for blocks that 64 does not divide, 0 for the others (more
+// than 64 tiles of 64 x 256 never go through it)
+inline int64_t mx4_stream_blocks(int64_t num_rows, int64_t out_features, int32_t block_m) {
+  if (block_m % 64 == 0) return 0;
+  const int64_t rows = block_m % 32 ? 16 : 32;
+  return mx4_stream_groups((num_rows + rows - 1) / rows) * ((out_features + 63) / 64);
+}
 
 // ---- forward ---------------------------------------------------------------
 // expert weights as fp8 e4m3 codes with 128 x 128 block scales (dtype bf16)

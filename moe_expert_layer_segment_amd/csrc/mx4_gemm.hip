@@ -858,10 +858,10 @@ static hipError_t tiled(const Mx4Gemm& p, hipStream_t stream) {
 template <bool XMX, int MB, int NB, int WV>
 static hipError_t stream(const Mx4Gemm& p, hipStream_t stream) {
   const int64_t col_groups = ceil_div(p.N / 16, NB), row_groups = ceil_div(p.M, 16 * MB);
-  const bool spread = row_groups >= 32;
+  const bool spread = row_groups >= kSpreadGroups;
   const size_t staged = p.K <= kStageK ? (size_t)(NB + (XMX ? MB : 0)) * 16 * (p.K / 32) : 0;
   const auto kernel = mx4_stream_kernel<XMX, MB, NB, WV>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)((spread ? round_up(row_groups, 16) : row_groups) * col_groups)),
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(mx4_stream_groups(row_groups) * col_groups)),
                      dim3(64 * WV), staged, stream, p, (int)row_groups, (int)col_groups, (int)spread);
   return hipGetLastError();
 }

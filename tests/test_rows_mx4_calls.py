@@ -162,3 +162,23 @@ def test_calls_go_to_the_device_of_their_tensors(recorder, monkeypatch):
     assert len(recorder.calls) == 9
     assert entered == [None, "left"] * 9 and streams == [None] * 9     # the index of a host tensor
     assert [args[-1] for _, args in recorder.calls] == [77] * 9
+
+
+def test_products_of_more_workgroups_than_a_launch_holds():
+    """The streaming kernel takes 16 rows x 64 columns a workgroup of 256 threads, the groups
+    of rows in sixteens from 32 of them on; threads of a launch are counted in 32 bits.  No
+    call here launches: sizes are checked before the pointers, and x is missing."""
+    import test_rows_mx4_api as api
+
+    def call(rows, cols, block_m):
+        a = api._gargs(num_rows=rows, out_features=cols, in_features=32, block_m=block_m, x=None)
+        return binding.lib().moe_lora_mx4_gemm(ctypes.byref(a), None)
+
+    for rows, cols, bm in ((976, 1 << 24, 16), (131088, 130896, 16), (144 * 7, 1 << 24, 144),
+                           (48 * 17, 1 << 24, 48)):
+        assert -(-rows // 16) * -(-cols // 64) < 1 << 24            # as they are counted
+        assert -(-rows // 256) * 16 * -(-cols // 64) >= 1 << 24     # as they are launched
+        assert call(rows, cols, bm) == binding.ERR_UNSUPPORTED, (rows, cols, bm)
+    for rows, cols, bm in ((768, 1 << 24, 16), (131072, 130896, 16), (992, 1 << 24, 32),
+                           (1056, 254200 * 64, 32), (960, 1 << 24, 64), (496, 1 << 24, 16)):
+        assert call(rows, cols, bm) == binding.ERR_INVALID, (rows, cols, bm)
