@@ -658,23 +658,25 @@ def _num_pairs(align_out):
 
 
 def _rows_layout(align_out, top_k, dev, num_rows=None):
-    """(tokens, rows of the layout) after checking its arrays."""
+    """(tokens, rows of the layout, spans of sorted_pair_ids, pair_rows and
+    num_rows_padded) after checking its arrays."""
     if "pair_rows" not in align_out:
         raise ValueError("the layout has no pair_rows (moe_lora_align(..., pair_rows=True))")
-    pairs = _num_pairs(align_out)
-    _need(align_out["pair_rows"], "pair_rows", torch.int32, dev, pairs)
-    cap = int(align_out["capacity"])
-    _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, cap)
-    _need(align_out["num_rows_padded"], "num_rows_padded", torch.int32, dev, 1)
+    pairs, cap = _num_pairs(align_out), int(align_out["capacity"])
+    pr, ids, used = align_out["pair_rows"], align_out["sorted_pair_ids"], align_out["num_rows_padded"]
+    _need(pr, "pair_rows", torch.int32, dev, pairs)
+    _need(ids, "sorted_pair_ids", torch.int32, dev, cap)
+    _need(used, "num_rows_padded", torch.int32, dev, 1)
     if top_k <= 0 or (cap > 0 and pairs % top_k):
         raise ValueError("pair_rows is not [T, top_k]")
     if num_rows is not None and num_rows != cap:
         raise ValueError(f"the layout has {cap} rows, got {num_rows}")
-    return (pairs // top_k if cap > 0 else 0), cap
+    return (pairs // top_k if cap > 0 else 0), cap, (
+        (ids.data_ptr(), 4 * cap), (pr.data_ptr(), 4 * pairs), (used.data_ptr(), 4))
 
 
-def _apart(out, *inputs):
-    """Outputs must not share memory with inputs."""
+def _apart(out, *inputs, spans=()):
+    """Outputs must not share memory with inputs: tensors, and ``spans`` of (address, bytes)."""
     lo = out.data_ptr()
     hi = lo + out.nbytes
     for t in inputs:
@@ -682,6 +684,9 @@ def _apart(out, *inputs):
             p = t.data_ptr()
             if lo < p + t.nbytes and p < hi:
                 raise ValueError("an output overlaps an input")
+    for p, n in spans:
+        if lo < p + n and p < hi:
+            raise ValueError("an output overlaps the layout")
 
 
 def _matrix(t, name, dev=None):
@@ -704,7 +709,7 @@ def moe_lora_permute(x: torch.Tensor, align_out: Dict[str, torch.Tensor], top_k:
     moe_lora_align with ``pair_rows=True``."""
     _matrix(x, "x")
     dt = _row_dtype(x, "x", (torch.uint8,))
-    T, cap = _rows_layout(align_out, top_k, x.device)
+    T, cap, spans = _rows_layout(align_out, top_k, x.device)
     if x.shape[0] != T:
         raise ValueError(f"x has {x.shape[0]} rows, the layout {T} tokens")
     H = x.shape[1]
@@ -714,10 +719,10 @@ def moe_lora_permute(x: torch.Tensor, align_out: Dict[str, torch.Tensor], top_k:
         _need(out, "out", x.dtype, x.device)
         if out.shape != (cap, H):
             raise ValueError(f"out must be {(cap, H)}, got {tuple(out.shape)}")
-        _apart(out, x)
-    _launch("moe_lora_permute", x.device, lib().moe_lora_permute, T, top_k, H, dt, cap, _at(x),
-            _at(align_out["sorted_pair_ids"]), _at(align_out["pair_rows"]),
-            _at(align_out["num_rows_padded"]), _at(out))
+        _apart(out, x, spans=spans)
+    (ids, _), (pair_rows, _), (used, _) = spans
+    _launch("moe_lora_permute", x.device, lib().moe_lora_permute, T, top_k, H, dt, cap, _at(x), ids,
+            pair_rows, used, _at(out))
     return out
 
 
@@ -726,23 +731,22 @@ def moe_lora_permute_backward(d_rows: torch.Tensor, align_out: Dict[str, torch.T
     """Gradient of moe_lora_permute: dx [T, H], the sum of each token's rows of
     ``d_rows`` (fp32 sums; ``out_dtype`` defaults to the rows' dtype)."""
     _matrix(d_rows, "d_rows")
-    T, cap = _rows_layout(align_out, top_k, d_rows.device, d_rows.shape[0])
+    T, cap, spans = _rows_layout(align_out, top_k, d_rows.device, d_rows.shape[0])
     H = d_rows.shape[1]
     if dx is None:
         dx = torch.empty((T, H), dtype=out_dtype or d_rows.dtype, device=d_rows.device)
     else:
-        _token_out(dx, "dx", T, H, d_rows, out_dtype)
+        _token_out(dx, "dx", T, H, out_dtype, d_rows, spans=spans)
     _launch("moe_lora_permute_backward", d_rows.device, lib().moe_lora_permute_backward, T, top_k, H,
-            _row_dtype(d_rows, "d_rows"), _row_dtype(dx, "dx"), cap, _at(d_rows),
-            _at(align_out["pair_rows"]), _at(dx))
+            _row_dtype(d_rows, "d_rows"), _row_dtype(dx, "dx"), cap, _at(d_rows), spans[1][0], _at(dx))
     return dx
 
 
-def _token_out(t, name, T, H, rows, out_dtype):
+def _token_out(t, name, T, H, out_dtype, rows, *others, spans):
     _need(t, name, out_dtype, rows.device)
     if t.shape != (T, H):
         raise ValueError(f"{name} must be {(T, H)}, got {tuple(t.shape)}")
-    _apart(t, rows)
+    _apart(t, rows, *others, spans=spans)
 
 
 def _pair_weights(w, T, top_k, dev, name="topk_weights"):
@@ -758,16 +762,16 @@ def moe_lora_unpermute(rows: torch.Tensor, align_out: Dict[str, torch.Tensor], t
     in pair order, rounded once; no weights: ones).  Pairs without a row take no
     part.  ``out_dtype`` defaults to the rows' dtype."""
     _matrix(rows, "rows")
-    T, cap = _rows_layout(align_out, top_k, rows.device, rows.shape[0])
+    T, cap, spans = _rows_layout(align_out, top_k, rows.device, rows.shape[0])
     H = rows.shape[1]
     if topk_weights is not None:
         _pair_weights(topk_weights, T, top_k, rows.device)
     if y is None:
         y = torch.empty((T, H), dtype=out_dtype or rows.dtype, device=rows.device)
     else:
-        _token_out(y, "y", T, H, rows, out_dtype)
+        _token_out(y, "y", T, H, out_dtype, rows, topk_weights, spans=spans)
     _launch("moe_lora_unpermute", rows.device, lib().moe_lora_unpermute, T, top_k, H,
-            _row_dtype(rows, "rows"), _row_dtype(y, "y"), cap, _at(rows), _at(align_out["pair_rows"]),
+            _row_dtype(rows, "rows"), _row_dtype(y, "y"), cap, _at(rows), spans[1][0],
             _at(topk_weights), _at(y))
     return y
 
@@ -786,7 +790,7 @@ def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
     left as they are."""
     _matrix(dy, "dy")
     dev = dy.device
-    T, cap = _rows_layout(align_out, top_k, dev)
+    T, cap, spans = _rows_layout(align_out, top_k, dev)
     H = dy.shape[1]
     if dy.shape[0] != T:
         raise ValueError(f"dy has {dy.shape[0]} rows, the layout {T} tokens")
@@ -802,7 +806,7 @@ def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
     _need(d_rows, "d_rows", dt, dev)
     if d_rows.shape != (cap, H):
         raise ValueError(f"d_rows must be {(cap, H)}, got {tuple(d_rows.shape)}")
-    _apart(d_rows, dy, rows, topk_weights)
+    _apart(d_rows, dy, rows, topk_weights, spans=spans)
     if rows is None or topk_weights is None:
         if d_weights is not None:
             raise ValueError("d_weights needs rows and topk_weights")
@@ -810,11 +814,11 @@ def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
         d_weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     if d_weights is not None:
         _pair_weights(d_weights, T, top_k, dev, "d_weights")
-        _apart(d_weights, dy, rows, topk_weights, d_rows)
+        _apart(d_weights, dy, rows, topk_weights, d_rows, spans=spans)
+    (ids, _), (pair_rows, _), (used, _) = spans
     _launch("moe_lora_unpermute_backward", dev, lib().moe_lora_unpermute_backward, T, top_k, H,
-            _row_dtype(dt, "rows"), _row_dtype(dy, "dy"), cap, _at(dy), _at(rows),
-            _at(align_out["sorted_pair_ids"]), _at(align_out["pair_rows"]),
-            _at(align_out["num_rows_padded"]), _at(topk_weights), _at(d_rows), _at(d_weights))
+            _row_dtype(dt, "rows"), _row_dtype(dy, "dy"), cap, _at(dy), _at(rows), ids, pair_rows, used,
+            _at(topk_weights), _at(d_rows), _at(d_weights))
     return d_rows, d_weights
 
 
@@ -872,8 +876,8 @@ def moe_lora_mx4_quantize(x: torch.Tensor, num_rows_used: Optional[torch.Tensor]
         _mx4_pair(codes, scales, "the output", dev)
         if codes.shape != (*lead, K // 2):
             raise ValueError(f"codes must be {(*lead, K // 2)}, got {tuple(codes.shape)}")
-        _apart(codes, x, scales)
-        _apart(scales, x)
+        _apart(codes, x, scales, num_rows_used)
+        _apart(scales, x, num_rows_used)
     if num_rows_used is not None:
         _need(num_rows_used, "num_rows_used", torch.int32, dev, 1)
     _launch("moe_lora_mx4_quantize", dev, lib().moe_lora_mx4_quantize, x.numel() // K, K, dt, _at(x),
@@ -927,16 +931,18 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
         xk = _mx4_pair(x, x_scales, "x", dev) if x.dim() == 2 else -1
     if x.dim() != 2 or xk != K:
         raise ValueError(f"x {tuple(x.shape)} does not match weights of {K} columns")
-    M, a = x.shape[0], Mx4GemmArgs()
+    M, a, spans = x.shape[0], Mx4GemmArgs(), ()
     if align_out is not None:
         a.block_m = int(align_out["block_m"])
         if a.block_m <= 0 or M % a.block_m:
             raise ValueError("x must hold whole tiles of block_m rows")
         _need(align_out["tile_expert"], "tile_expert", torch.int32, dev, M // a.block_m)
         a.tile_expert = align_out["tile_expert"].data_ptr()
+        spans = ((a.tile_expert, 4 * (M // a.block_m)),)
         if "pair_rows" in align_out:   # ids past the pairs are padding
             _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, M)
             a.sorted_pair_ids = align_out["sorted_pair_ids"].data_ptr()
+            spans += ((a.sorted_pair_ids, 4 * M),)
             a.num_pairs = _num_pairs(align_out)
     cols = N // 2 if silu_mul else N
     if out is None:
@@ -945,7 +951,7 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
         _need(out, "out", out_dtype, dev)
         if out.shape != (M, cols):
             raise ValueError(f"out must be {(M, cols)}, got {tuple(out.shape)}")
-        _apart(out, x, x_scales, w_codes, w_scales)
+        _apart(out, x, x_scales, w_codes, w_scales, spans=spans)
     if M == 0:
         return out
     a.struct_size = ctypes.sizeof(Mx4GemmArgs)

@@ -182,3 +182,55 @@ def test_products_of_more_workgroups_than_a_launch_holds():
     for rows, cols, bm in ((768, 1 << 24, 16), (131072, 130896, 16), (992, 1 << 24, 32),
                            (1056, 254200 * 64, 32), (960, 1 << 24, 64), (496, 1 << 24, 16)):
         assert call(rows, cols, bm) == binding.ERR_INVALID, (rows, cols, bm)
+
+
+def over(t, *shape, dtype=torch.float32):
+    """A tensor of `shape` whose memory ends inside that of `t`."""
+    n = max(t.numel() * t.element_size(), 64)
+    size = torch.zeros(*shape, dtype=dtype).nbytes
+    both = torch.zeros(size + n, dtype=torch.uint8)
+    at = size - 16      # `t` starts 16 bytes before the end of the other
+    moved = both[at:at + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+    return moved.as_subclass(_Dev), both[:size].view(dtype).view(*shape).as_subclass(_Dev)
+
+
+@pytest.mark.parametrize("shared", ["topk_weights", "sorted_pair_ids", "pair_rows", "num_rows_padded",
+                                    "tile_expert"])
+def test_outputs_overlap_no_input(recorder, shared):
+    """Every output against every array that the call reads beside the matrices."""
+    T, k, H, bf = 4, 2, 64, torch.bfloat16
+    al = align(T, k, pair_rows=True)
+    cap = al["capacity"]
+    w = dev(T, k)
+
+    def check(call, *shape, dtype=torch.float32):
+        moved, out = over(w if shared == "topk_weights" else al[shared], *shape, dtype=dtype)
+        lay, weights = (al, moved) if shared == "topk_weights" else (dict(al, **{shared: moved}), w)
+        with pytest.raises(ValueError, match="overlaps"):
+            call(out, lay, weights)
+
+    rows, tokens = dev(cap, H), dev(T, H)
+    calls = {
+        "permute": lambda: check(lambda o, a, _: binding.moe_lora_permute(tokens, a, k, out=o), cap, H),
+        "permute_backward": lambda: check(
+            lambda o, a, _: binding.moe_lora_permute_backward(rows, a, k, dx=o), T, H),
+        "unpermute": lambda: check(lambda o, a, v: binding.moe_lora_unpermute(rows, a, k, v, y=o), T, H),
+        "d_rows": lambda: check(lambda o, a, v: binding.moe_lora_unpermute_backward(
+            tokens, rows, a, k, v, d_rows=o), cap, H),
+        "d_weights": lambda: check(lambda o, a, v: binding.moe_lora_unpermute_backward(
+            tokens, rows, a, k, v, d_weights=o), T, k),
+        "gemm": lambda: check(lambda o, a, _: binding.moe_lora_mx4_gemm(
+            dev(cap, H, dtype=bf), *mx4(8, 32, H), align_out=a, out=o), cap, 32, dtype=bf),
+        "codes": lambda: check(lambda o, a, _: binding.moe_lora_mx4_quantize(
+            rows, a["num_rows_padded"], codes=o), cap, H // 2, dtype=torch.uint8),
+        "scales": lambda: check(lambda o, a, _: binding.moe_lora_mx4_quantize(
+            rows, a["num_rows_padded"], scales=o), cap, H // 32, dtype=torch.uint8),
+    }
+    rowwise = {"permute", "permute_backward", "unpermute", "d_rows", "d_weights"}
+    reads = {"topk_weights": {"unpermute", "d_rows", "d_weights"}, "pair_rows": rowwise,
+             "sorted_pair_ids": rowwise | {"gemm"},
+             "num_rows_padded": rowwise | {"codes", "scales"}, "tile_expert": {"gemm"}}[shared]
+    recorder.calls.clear()
+    for name in reads:
+        calls[name]()
+    assert not recorder.calls
