@@ -689,6 +689,16 @@ def _apart(out, *inputs, spans=()):
             raise ValueError("an output overlaps the layout")
 
 
+def _no_grad(where, *tensors):
+    """Autograd does not see these calls: where it is on, an input that requires a
+    gradient is refused rather than its gradient lost."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{where} is not recorded by autograd and an input requires a gradient: "
+                                 "call it under torch.no_grad() or in a torch.autograd.Function")
+
+
 def _matrix(t, name, dev=None):
     _need(t, name, None, dev)
     if t.dim() != 2:
@@ -706,8 +716,13 @@ def moe_lora_permute(x: torch.Tensor, align_out: Dict[str, torch.Tensor], top_k:
 
     Padding rows before ``num_rows_padded`` are zero; rows behind it are left as
     they are in ``out`` (undefined when it is not given).  ``align_out`` comes from
-    moe_lora_align with ``pair_rows=True``."""
+    moe_lora_align with ``pair_rows=True``.
+
+    Like all calls on rows it is for torch.no_grad() or the forward and backward of a
+    torch.autograd.Function: its gradient is moe_lora_permute_backward, and an x that
+    requires a gradient is refused where autograd is on."""
     _matrix(x, "x")
+    _no_grad("moe_lora_permute", x)
     dt = _row_dtype(x, "x", (torch.uint8,))
     T, cap, spans = _rows_layout(align_out, top_k, x.device)
     if x.shape[0] != T:
@@ -731,6 +746,7 @@ def moe_lora_permute_backward(d_rows: torch.Tensor, align_out: Dict[str, torch.T
     """Gradient of moe_lora_permute: dx [T, H], the sum of each token's rows of
     ``d_rows`` (fp32 sums; ``out_dtype`` defaults to the rows' dtype)."""
     _matrix(d_rows, "d_rows")
+    _no_grad("moe_lora_permute_backward", d_rows)
     T, cap, spans = _rows_layout(align_out, top_k, d_rows.device, d_rows.shape[0])
     H = d_rows.shape[1]
     if dx is None:
@@ -760,8 +776,11 @@ def moe_lora_unpermute(rows: torch.Tensor, align_out: Dict[str, torch.Tensor], t
                        y: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
     """y [T, H] = the sum over a token's top_k pairs of weight times row (fp32,
     in pair order, rounded once; no weights: ones).  Pairs without a row take no
-    part.  ``out_dtype`` defaults to the rows' dtype."""
+    part.  ``out_dtype`` defaults to the rows' dtype.  The gradients are those of
+    moe_lora_unpermute_backward; rows or weights that require one are refused where
+    autograd is on."""
     _matrix(rows, "rows")
+    _no_grad("moe_lora_unpermute", rows, topk_weights)
     T, cap, spans = _rows_layout(align_out, top_k, rows.device, rows.shape[0])
     H = rows.shape[1]
     if topk_weights is not None:
@@ -789,6 +808,7 @@ def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
     dy's).  Padding rows of d_rows are zero, rows behind ``num_rows_padded`` are
     left as they are."""
     _matrix(dy, "dy")
+    _no_grad("moe_lora_unpermute_backward", dy, rows, topk_weights)
     dev = dy.device
     T, cap, spans = _rows_layout(align_out, top_k, dev)
     H = dy.shape[1]
@@ -918,7 +938,8 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
     are in ``out`` (undefined when it is not given).  With ``pair_rows`` in align_out
     padding rows get zeros, whatever x and the weights hold.
     x: bfloat16, or MX4 codes [M, K/2] with ``x_scales`` [M, K/32].  ``out`` /
-    ``out_dtype``: bfloat16 (the default) or float32."""
+    ``out_dtype``: bfloat16 (the default) or float32.  There is no gradient: an x that
+    requires one is refused where autograd is on."""
     K = _mx4_pair(w_codes, w_scales, "w")
     dev = w_codes.device
     if w_codes.dim() != (2 if align_out is None else 3):
@@ -926,6 +947,7 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
     E, N = (1 if align_out is None else w_codes.shape[0]), w_codes.shape[-2]
     if x_scales is None:
         _need(x, "x", torch.bfloat16, dev)
+        _no_grad("moe_lora_mx4_gemm", x)
         xk = x.shape[-1] if x.dim() == 2 else -1
     else:
         xk = _mx4_pair(x, x_scales, "x", dev) if x.dim() == 2 else -1
@@ -982,10 +1004,12 @@ def run_mx4_layer(inputs: dict, activations: str = "bf16", block_m: Optional[int
     w_gate_up_mx4 [E, 2I, H], w_down_mx4 [E, H, I], each a (codes, scales) pair of
     moe_lora_mx4_quantize.
     ``activations``: "bf16", or "mx4" to quantise x and the activations between the
-    products as well."""
+    products as well.  For serving: there is no gradient, and x or topk_weights that
+    require one are refused where autograd is on."""
     if activations not in ("bf16", "mx4"):
         raise ValueError("activations must be 'bf16' or 'mx4'")
     x, ids, w = inputs["x"], inputs["topk_ids"], inputs["topk_weights"]
+    _no_grad("run_mx4_layer", x, w)
     T, k = ids.shape
     gu, down = inputs["w_gate_up_mx4"], inputs["w_down_mx4"]
     H, I = _mx4_pair(*gu, "w_gate_up"), _mx4_pair(*down, "w_down")

@@ -234,3 +234,48 @@ def test_outputs_overlap_no_input(recorder, shared):
     for name in reads:
         calls[name]()
     assert not recorder.calls
+
+
+def test_no_gradient_is_lost(recorder):
+    """Inputs that require a gradient are refused where autograd would record the call;
+    under no_grad, and in the forward of a Function, they are taken."""
+    al = align(4, 2, pair_rows=True)
+    cap, bf = al["capacity"], torch.bfloat16
+    want = lambda *s, dtype=torch.float32: dev(*s, dtype=dtype).requires_grad_()  # noqa: E731
+    tokens, rows, w = dev(4, 64), dev(cap, 64), dev(4, 2)
+    calls = [
+        lambda: binding.moe_lora_permute(want(4, 64), al, 2),
+        lambda: binding.moe_lora_permute_backward(want(cap, 64), al, 2),
+        lambda: binding.moe_lora_unpermute(want(cap, 64), al, 2, w),
+        lambda: binding.moe_lora_unpermute(rows, al, 2, want(4, 2)),
+        lambda: binding.moe_lora_unpermute_backward(want(4, 64), rows, al, 2, w),
+        lambda: binding.moe_lora_unpermute_backward(tokens, want(cap, 64), al, 2, w),
+        lambda: binding.moe_lora_unpermute_backward(tokens, rows, al, 2, want(4, 2)),
+        lambda: binding.moe_lora_mx4_gemm(want(cap, 64, dtype=bf), *mx4(8, 32, 64), align_out=al),
+        lambda: binding.run_mx4_layer(layer(x=want(5, 96, dtype=bf))),
+        lambda: binding.run_mx4_layer(layer(x=want(5, 96, dtype=bf)), "mx4"),
+        lambda: binding.run_mx4_layer(layer(topk_weights=want(5, 2)))]
+    recorder.calls.clear()
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    assert not recorder.calls
+    with torch.no_grad():
+        for call in calls:
+            call()
+    binding.moe_lora_mx4_quantize(want(4, 64))     # of a weight, for serving: codes have no gradient
+
+    class Permute(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return binding.moe_lora_permute(x, al, 2)
+
+        @staticmethod
+        def backward(ctx, d_rows):
+            return binding.moe_lora_permute_backward(d_rows.contiguous().as_subclass(_Dev), al, 2)
+
+    x = want(4, 64)
+    recorder.calls.clear()
+    Permute.apply(x).sum().backward()
+    assert [n for n, _ in recorder.calls] == ["moe_lora_permute", "moe_lora_permute_backward"]
+    assert x.grad.shape == x.shape
