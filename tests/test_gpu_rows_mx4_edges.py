@@ -97,3 +97,81 @@ def test_padding_rows_beside_weights_that_are_not_finite(kind, bm, tokens):
         keep = torch.ones(y.shape[1], dtype=torch.bool, device="cuda")
         keep[hit] = False
         assert torch.equal(y[:, keep], clean[:, keep])
+
+
+# ---------------------------------------------------------------------------
+# every variant of the product kernels
+# ---------------------------------------------------------------------------
+VARIANTS = [  # block_m (None: one weight for all rows), blocks or rows, N, K
+    (16, 37, 1040, 1056), (16, 33, 48, 96), (16, 64, 512, 16416), (48, 13, 1040, 544), (16, 33, 48, 16416),
+    (32, 33, 1040, 1056), (32, 33, 64, 160), (32, 64, 512, 16416), (96, 17, 1552, 288),
+    (16, 17, 2016, 288), (32, 17, 2016, 160), (None, 1, 32784, 96), (None, 20, 32784, 96),
+    (64, 2, 8176, 288), (64, 34, 256, 96), (64, 32, 512, 96), (64, 16, 1008, 16416),
+    (None, 64, 16384, 96), (None, 40, 16368, 32),
+    (None, 1, 48, 16416), (None, 20, 48, 16416), (None, 64, 48, 16416),
+    (None, 1, 48, 16384), (None, 20, 48, 16384), (None, 64, 48, 16384),
+    # more than 4096 tiles: the last round is not split
+    (64, 258, 4112, 96), (64, 242, 4352, 128), (128, 260, 4112, 32), (256, 242, 4128, 128),
+    (None, 61700, 4352, 32),
+]
+
+
+def variant(M, N, K, block_m, kind):
+    """What launch_mx4_gemm takes: ("stream", 16-row blocks, 16-column blocks, waves, groups of
+    rows in sixteens, scales in LDS) or ("tile", rows, last round split, scales by DMA)."""
+    up = lambda a, b: -(-a // b)  # noqa: E731
+
+    def takes(n):
+        return block_m % n == 0 if block_m else M > n // 2
+
+    def few(mb, nb, wide):
+        groups = up(M, 16 * mb)
+        full = groups * up(N, 16 * nb) >= 512
+        return "stream", mb, nb if full else 2, 4 if full else wide, groups >= 32, K <= 16384
+
+    if takes(64):
+        if up(M, 64) * up(N, 256) <= 64:
+            return few(4, 2, 8)
+        rows = 256 if takes(256) else 128 if takes(128) else 64
+        return "tile", rows, up(M, rows) * up(N, 256) <= 4096, kind == "bf16" and K % 128 == 0
+    return few(2, 4, 8) if takes(32) else few(1, 4, 16)
+
+
+@pytest.mark.parametrize("case", VARIANTS, ids=lambda c: f"b{c[0]}n{c[1]}N{c[2]}K{c[3]}")
+@pytest.mark.parametrize("kind", ["bf16", "mx4"])
+def test_variants(case, kind):
+    """Blocks of any number of rows that hold a pair, against the oracle (of more than 2^24
+    results a share of the rows, those at the borders of blocks and at the end among them)."""
+    bm, n, N, K = case
+    E, M = (3, bm * n) if bm else (1, n)
+    say(f"variant {case} {kind}: {variant(M, N, K, bm, kind)}")
+    g = torch.Generator().manual_seed(41)
+    experts, live = torch.zeros(M, dtype=torch.long), torch.ones(M, dtype=torch.bool)
+    al = None
+    if bm:
+        tiles = torch.randint(0, E, (n,), generator=g)
+        tiles[-1] = -1
+        experts = tiles.repeat_interleave(bm)
+        fill = torch.randint(0, bm + 1, (n, 1), generator=g)
+        fill[:3] = torch.tensor([[0], [bm], [1]])[:n]
+        live = (torch.arange(bm) < fill).view(-1) & (torch.rand(M, generator=g) < 0.95)
+        pairs = int(live.sum()) + 1
+        sid = torch.full((M,), pairs, dtype=torch.int32)
+        sid[live] = torch.randperm(pairs - 1, generator=g).int()
+        al = dict(block_m=bm, tile_expert=tiles.int().cuda(), sorted_pair_ids=sid.cuda(),
+                  pair_rows=torch.empty(pairs, dtype=torch.int32, device="cuda"))
+    wc, ws, w64 = weights(E, N, K, 42)
+    x, xs, x64 = activations(M, K, kind, 43)
+    at = torch.arange(M)
+    if M * N > 1 << 24:
+        at = at[(at % 61 == 0) | (at % (bm or 256) < 2) | (at >= M - 300)]
+    row_expert = torch.where(live, experts, -1)[at].numpy()
+    if al is None:
+        wc, ws = wc[0], ws[0]
+    for silu in (False, True) if N % 32 == 0 else (False,):
+        mark = torch.full((M, N // 2 if silu else N), -9.5, dtype=torch.bfloat16, device="cuda")
+        y = binding.moe_lora_mx4_gemm(x, wc, ws, x_scales=xs, align_out=al, silu_mul=silu, out=mark.clone())
+        check_product(np64(y[at.cuda()]), torch.bfloat16, x64[at.numpy()], w64, row_expert, silu, K,
+                      f"silu {silu}")
+        assert bool((y[(~live & (experts >= 0)).cuda()] == 0).all())
+        assert torch.equal(y[(experts < 0).cuda()], mark[(experts < 0).cuda()])

@@ -279,3 +279,25 @@ def test_no_gradient_is_lost(recorder):
     Permute.apply(x).sum().backward()
     assert [n for n, _ in recorder.calls] == ["moe_lora_permute", "moe_lora_permute_backward"]
     assert x.grad.shape == x.shape
+
+
+def test_every_variant_of_the_products_is_tested():
+    """The GPU cases reach each kernel that the sizes choose between, with the groups of rows
+    in order and in sixteens, scales in LDS and not, the last round split and not."""
+    import test_gpu_mx4 as plain
+    import test_gpu_rows_mx4_edges as edges
+    cases = [(c[0], *c[1:], None) for c in plain.DENSE]
+    cases += [(len(t) * bm, N, K, bm) for t, bm, N, K in plain.GROUPED]
+    cases += [(bm * n if bm else n, N, K, bm) for bm, n, N, K in edges.VARIANTS]
+    for kind in ("bf16", "mx4"):
+        got = {edges.variant(M, N, K, bm, kind) for M, N, K, bm in cases}
+        streams = {(v[1:4], "spread", v[4]) for v in got if v[0] == "stream"}
+        streams |= {(v[1:4], "staged", v[5]) for v in got if v[0] == "stream"}
+        sizes = [(1, 4, 4), (1, 2, 16), (2, 4, 4), (2, 2, 8), (4, 2, 4), (4, 2, 8)]
+        assert streams == {(s, what, is_so) for s in sizes for what in ("spread", "staged")
+                           for is_so in (False, True)}
+        tiles = {v[1:3] for v in got if v[0] == "tile"}
+        assert tiles == {(rows, split) for rows in (64, 128, 256) for split in (False, True)}
+        by_dma = {(v[1], v[3]) for v in got if v[0] == "tile"}
+        assert by_dma == {(rows, dma) for rows in (64, 128, 256)
+                          for dma in ((False, True) if kind == "bf16" else (False,))}
