@@ -175,3 +175,159 @@ def test_variants(case, kind):
                       f"silu {silu}")
         assert bool((y[(~live & (experts >= 0)).cuda()] == 0).all())
         assert torch.equal(y[(experts < 0).cuda()], mark[(experts < 0).cuda()])
+
+
+# ---------------------------------------------------------------------------
+# rows: short ones, unaligned ones, more than one launch takes at once
+# ---------------------------------------------------------------------------
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "u8": torch.uint8}
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+def values(shape, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    if dtype == torch.uint8:
+        return torch.randint(0, 256, shape, generator=g, dtype=dtype).cuda()
+    return torch.randn(*shape, generator=g).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f32"),
+                                       ("u8", "u8")])
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 5, 7, 8, 9, 11, 15, 16, 17, 23, 31])
+def test_short_rows(H, dtype, out):
+    """Rows shorter than 16 bytes go element by element, longer ones in pieces of 16 whose
+    last one overlaps; bounds as in test_gpu_rows."""
+    T, k, E = 70, 3, 7
+    al = binding.moe_lora_align(some_ids(T, k, E, 50) - (torch.arange(T * k, device="cuda").view(T, k) % 5 == 0).int()
+                                * 100, no_slots(T), None, E, 0, 16, pair_rows=True)
+    cap, used = al["capacity"], int(al["num_rows_padded"].cpu()[0])
+    pr = ro.pair_rows_of(al["sorted_pair_ids"][:cap].cpu().numpy(), T * k)
+    assert (pr < 0).any()
+    x = values((T, H), DT[dtype], 51)
+    mark = values((cap, H), DT[dtype], 52)
+    got = binding.moe_lora_permute(x, al, k, out=mark.clone())
+    assert np.array_equal(got[:used].float().cpu().numpy(), ro.permute(x.float().cpu().numpy(), pr, k, cap)[0][:used])
+    assert torch.equal(got[used:], mark[used:])
+    if dtype == "u8":
+        return
+    rows, w, dy = values((cap, H), DT[dtype], 53), values((T, k), torch.float32, 54), values((T, H), DT[out], 55)
+    ho, hr = HALF[DT[out]], HALF[DT[dtype]]
+    for weights_ in (w, None):
+        y = binding.moe_lora_unpermute(rows, al, k, weights_, out_dtype=DT[out])
+        ref, mag = ro.unpermute(np64(rows), pr, k, None if weights_ is None else np64(w))
+        assert np.all(np.abs(np64(y) - ref) <= k * 2.0 ** -24 * mag * (1 + ho) + ho * np.abs(ref))
+    d_rows, d_w = binding.moe_lora_unpermute_backward(dy, rows, al, k, w, d_rows=mark.clone())
+    ref, ref_w, mag_w = ro.unpermute_backward(np64(dy), np64(rows), pr, k, np64(w), cap)
+    assert np.all(np.abs(np64(d_rows) - ref)[:used] <= (2.0 ** -24 * (1 + hr) + hr) * np.abs(ref[:used]))
+    assert torch.equal(d_rows[used:], mark[used:])
+    assert np.all(np.abs(np64(d_w) - ref_w) <= (H + 1) * 2.0 ** -24 * mag_w)
+
+
+@pytest.mark.parametrize("H", [3, 9, 264, 1001])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_unaligned_pointers_change_no_bit(H, dt):
+    """Whatever its pointers are aligned to, a call takes the same pieces in the same order."""
+    T, k, E = 23, 2, 4
+    al = binding.moe_lora_align(some_ids(T, k, E, 60), no_slots(T), None, E, 0, 16, pair_rows=True)
+    cap, used = al["capacity"], int(al["num_rows_padded"].cpu()[0])
+
+    def odd(t, by):
+        return torch.cat((t.new_zeros(by), t.reshape(-1)))[by:].view(t.shape)
+
+    x, rows, w = values((T, H), dt, 61), values((cap, H), dt, 62), values((T, k), torch.float32, 63)
+    want = (binding.moe_lora_permute(x, al, k)[:used], binding.moe_lora_unpermute(rows, al, k, w),
+            binding.moe_lora_permute_backward(rows, al, k),
+            *binding.moe_lora_unpermute_backward(x, rows, al, k, w))
+    for by in (1, 3):
+        xo, ro_, wo = odd(x, by), odd(rows, by), odd(w, by)
+        got = (binding.moe_lora_permute(xo, al, k, out=odd(rows, by))[:used],
+               binding.moe_lora_unpermute(ro_, al, k, wo, y=odd(x, by)),
+               binding.moe_lora_permute_backward(ro_, al, k, dx=odd(x, by)),
+               *binding.moe_lora_unpermute_backward(xo, ro_, al, k, wo, d_rows=odd(rows, by), d_weights=odd(w, by)))
+        for i, (a, b) in enumerate(zip(got, want)):
+            n = used if i in (0, 3) else len(a)
+            assert torch.equal(a[:n], b[:n]), (by, i)
+
+
+def test_tokens_of_more_than_one_round():
+    """More tokens than one launch has workgroups (2^22): every one of them, with some that
+    have no row."""
+    T, H = (1 << 22) + 1037, 5
+    say("tokens of more than one round")
+    g = torch.Generator(device="cuda").manual_seed(70)
+    perm = torch.randperm(T, generator=g, device="cuda").int()
+    gone = torch.arange(T, device="cuda") % 1000 == 3
+    pr = torch.where(gone, -1, perm)
+    ids = torch.full((T,), T, dtype=torch.int32, device="cuda")
+    ids[perm[~gone].long()] = torch.arange(T, dtype=torch.int32, device="cuda")[~gone]
+    al = dict(sorted_pair_ids=ids, pair_rows=pr, capacity=T,
+              num_rows_padded=torch.tensor([T], dtype=torch.int32, device="cuda"))
+    x = torch.randn(T, H, generator=g, device="cuda")
+    w = torch.rand(T, 1, generator=g, device="cuda")
+    want = torch.zeros(T, H, device="cuda")
+    want[perm[~gone].long()] = x[~gone]
+    rows = binding.moe_lora_permute(x, al, 1, out=torch.full_like(x, 9.0))
+    assert torch.equal(rows, want)
+    there = x * ~gone.view(-1, 1)
+    assert torch.equal(binding.moe_lora_unpermute(rows, al, 1, w), there * w)     # one product each
+    assert torch.equal(binding.moe_lora_permute_backward(rows, al, 1), there)
+    d_rows, d_w = binding.moe_lora_unpermute_backward(x, rows, al, 1, w, d_rows=torch.full_like(x, 9.0))
+    want[perm[~gone].long()] = (x * w)[~gone]
+    assert torch.equal(d_rows, want)
+    ref = (x.double() * there.double()).sum(1, keepdim=True)
+    assert bool(((d_w.double() - ref).abs() <= (H + 1) * 2.0 ** -24 * ref).all())    # a sum of squares
+
+
+def test_padding_of_more_than_one_round():
+    """More rows than one launch's workgroups look at (2^20 x 16): padding among them and at
+    the end gets zeros, rows behind num_rows_padded stay."""
+    R, used = (1 << 24) + 5000, (1 << 24) + 4711
+    say("padding of more than one round")
+    ids = torch.full((R,), 3, dtype=torch.int32, device="cuda")
+    at = torch.tensor([7, 1 << 23, (1 << 24) + 4600], device="cuda")
+    ids[at] = torch.arange(3, dtype=torch.int32, device="cuda")
+    al = dict(sorted_pair_ids=ids, pair_rows=at.int(), capacity=R,
+              num_rows_padded=torch.tensor([used], dtype=torch.int32, device="cuda"))
+    x = torch.tensor([[1.0], [2.0], [3.0]], device="cuda")
+    want = torch.zeros(R, 1, device="cuda")
+    want[at] = x
+    want[used:] = 9.0
+    assert torch.equal(binding.moe_lora_permute(x, al, 1, out=torch.full_like(want, 9.0)), want)
+    assert torch.equal(binding.moe_lora_unpermute_backward(x, None, al, 1, d_rows=torch.full_like(want, 9.0))[0], want)
+
+
+# ---------------------------------------------------------------------------
+# quantisation
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("part", range(8))
+def test_quantise_each_finite_bf16_value(part):
+    """Every finite bf16 value as a block's largest, beside smaller ones of both signs."""
+    v = (torch.arange(part, 0x7F80, 8, dtype=torch.int32) << 16).view(torch.float32)
+    x = v.view(-1, 1) * torch.linspace(-1, 1, 32).view(1, -1)
+    x[:, 0] = -v
+    x = x.bfloat16()
+    codes, scales = binding.moe_lora_mx4_quantize(x.cuda())
+    rc, rs = ro.mx4_quantize(x.double().numpy())
+    assert np.array_equal(scales.cpu().numpy(), rs) and np.array_equal(codes.cpu().numpy(), rc)
+
+
+def test_quantise_more_than_one_round():
+    """More values than one launch takes at once (2^20 x 256 x 4 units of 8): every row as
+    its pattern says, there and back."""
+    rows, cols, period = (1 << 20) + 77, 8224, 16
+    say("quantise more than one round")
+    assert rows * cols > 1 << 33
+    pattern = values((period, cols), torch.bfloat16, 80)
+    x = pattern.repeat(-(-rows // period), 1)[:rows]
+    codes, scales = binding.moe_lora_mx4_quantize(x)
+    rc, rs = binding.moe_lora_mx4_quantize(pattern)
+    assert np.array_equal(rc.cpu().numpy(), ro.mx4_quantize(np64(pattern))[0])
+    for got, want in ((codes, rc), (scales, rs)):
+        for r in range(0, rows, period << 10):
+            part = got[r:r + (period << 10)]
+            assert torch.equal(part, want.repeat(-(-len(part) // period), 1)[:len(part)]), r
+    back = binding.moe_lora_mx4_dequantize(codes, scales)
+    want = binding.moe_lora_mx4_dequantize(rc, rs)
+    for r in range(0, rows, period << 10):
+        part = back[r:r + (period << 10)]
+        assert torch.equal(part, want.repeat(-(-len(part) // period), 1)[:len(part)]), r
