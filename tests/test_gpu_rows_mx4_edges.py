@@ -182,6 +182,7 @@ def test_variants(case, kind):
 # ---------------------------------------------------------------------------
 DT = {"f32": torch.float32, "bf16": torch.bfloat16, "u8": torch.uint8}
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+INT_MIN = -(1 << 31)
 
 
 def values(shape, dtype, seed):
@@ -331,3 +332,85 @@ def test_quantise_more_than_one_round():
     for r in range(0, rows, period << 10):
         part = back[r:r + (period << 10)]
         assert torch.equal(part, want.repeat(-(-len(part) // period), 1)[:len(part)]), r
+
+
+# ---------------------------------------------------------------------------
+# calls that the documentation allows
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["bf16", "mx4"])
+@pytest.mark.parametrize("bm,n,N", [(16, 9, 96), (32, 40, 1040), (64, 9, 96), (64, 40, 528), (128, 40, 528),
+                                    (192, 24, 528), (256, 35, 2064)])
+def test_tiles_of_other_experts(bm, n, N, kind):
+    """Tiles of an expert that the weights do not hold, in the middle, at the start and at the
+    end: their rows stay as they were, the others are theirs."""
+    E, K = 3, 160
+    say(f"tiles of other experts {kind} block_m {bm} x {n}")
+    g = torch.Generator().manual_seed(90)
+    tiles = torch.randint(-1, E + 2, (n,), generator=g)
+    tiles[0], tiles[1], tiles[-1] = E, 1, INT_MIN
+    al = dict(block_m=bm, tile_expert=tiles.int().cuda())
+    wc, ws, w64 = weights(E, N, K, 91)
+    x, xs, x64 = activations(n * bm, K, kind, 92)
+    row_expert = torch.where((tiles >= 0) & (tiles < E), tiles, -1).numpy().repeat(bm)
+    mark = torch.full((n * bm, N), -9.5, dtype=torch.float32, device="cuda")
+    y = binding.moe_lora_mx4_gemm(x, wc, ws, x_scales=xs, align_out=al, out=mark.clone())
+    check_product(np64(y), torch.float32, x64, w64, row_expert, False, K, "other experts")
+    other = torch.from_numpy(row_expert < 0).cuda()
+    assert torch.equal(y[other], mark[other])
+
+
+def test_an_expert_named_twice_by_a_token():
+    """Both pairs have a row of their own, and both count."""
+    T, k, E, H = 50, 4, 4, 96
+    ids = torch.randint(0, E, (T, k), generator=torch.Generator().manual_seed(93)).int().cuda()
+    al = binding.moe_lora_align(ids, no_slots(T), None, E, 0, 16, pair_rows=True)
+    x, w = values((T, H), torch.float32, 94), values((T, k), torch.float32, 95)
+    pr = al["pair_rows"]
+    assert len(set(pr.tolist())) == T * k and bool((pr >= 0).all())
+    rows = binding.moe_lora_permute(x, al, k)
+    assert torch.equal(rows[pr.long()].view(T, k, H), x.unsqueeze(1).expand(T, k, H))
+    y = binding.moe_lora_unpermute(rows, al, k, w)
+    ref = np64(x) * np64(w).sum(1, keepdims=True)
+    mag = np.abs(np64(x)) * np.abs(np64(w)).sum(1, keepdims=True)
+    assert np.all(np.abs(np64(y) - ref) <= (k + 1) * 2.0 ** -24 * mag)
+
+
+@pytest.mark.parametrize("activations_", ["bf16", "mx4"])
+def test_layer_captured_and_on_two_streams(activations_):
+    """run_mx4_layer replayed from a graph with new tokens, experts and weights, beside its own
+    eager calls, and on two streams at once."""
+    T, k, E, H, I = 150, 2, 6, 256, 96  # noqa: E741
+    guc, gus, _ = weights(E, 2 * I, H, 96)
+    dc, ds, _ = weights(E, H, I, 97)
+
+    def batch(seed):
+        return dict(x=values((T, H), torch.bfloat16, seed), topk_ids=some_ids(T, k, E, seed),
+                    topk_weights=values((T, k), torch.float32, seed + 1))
+
+    layer = dict(w_gate_up_mx4=(guc, gus), w_down_mx4=(dc, ds))
+    now = dict(batch(100), **layer)
+    binding.run_mx4_layer(now, activations_)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = binding.run_mx4_layer(now, activations_)
+    for i in range(4):
+        for name, t in batch(110 + i).items():
+            now[name].copy_(t)
+        want = binding.run_mx4_layer(now, activations_)
+        torch.cuda.synchronize()
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
+    batches = [dict(batch(120 + i), **layer) for i in range(2)]
+    want = [binding.run_mx4_layer(b, activations_) for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(binding.run_mx4_layer(batches[i], activations_))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, want[i]) for i in range(2) for a in got[i])
