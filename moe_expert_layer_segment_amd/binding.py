@@ -651,32 +651,33 @@ def _row_dtype(t, name, also=()):
     raise TypeError(f"unsupported dtype of {name}: {dtype}")
 
 
-def _num_pairs(align_out):
-    """Pairs of the batch: pair_rows may be a buffer of more."""
-    n = align_out.get("num_pairs")
-    return align_out["pair_rows"].numel() if n is None else int(n)
-
-
 def _rows_layout(align_out, top_k, dev, num_rows=None):
-    """(tokens, rows of the layout, spans of sorted_pair_ids, pair_rows and
-    num_rows_padded) after checking its arrays."""
+    """(tokens, rows of the layout) after checking its arrays."""
     if "pair_rows" not in align_out:
         raise ValueError("the layout has no pair_rows (moe_lora_align(..., pair_rows=True))")
-    pairs, cap = _num_pairs(align_out), int(align_out["capacity"])
-    pr, ids, used = align_out["pair_rows"], align_out["sorted_pair_ids"], align_out["num_rows_padded"]
+    # pair_rows may be a buffer of more than the batch's pairs
+    pr, pairs, cap = align_out["pair_rows"], align_out.get("num_pairs"), int(align_out["capacity"])
     _need(pr, "pair_rows", torch.int32, dev, pairs)
-    _need(ids, "sorted_pair_ids", torch.int32, dev, cap)
-    _need(used, "num_rows_padded", torch.int32, dev, 1)
+    if pairs is None:
+        pairs = pr.numel()
+    _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, cap)
+    _need(align_out["num_rows_padded"], "num_rows_padded", torch.int32, dev, 1)
     if top_k <= 0 or (cap > 0 and pairs % top_k):
         raise ValueError("pair_rows is not [T, top_k]")
     if num_rows is not None and num_rows != cap:
         raise ValueError(f"the layout has {cap} rows, got {num_rows}")
-    return (pairs // top_k if cap > 0 else 0), cap, (
-        (ids.data_ptr(), 4 * cap), (pr.data_ptr(), 4 * pairs), (used.data_ptr(), 4))
+    return (pairs // top_k if cap > 0 else 0), cap
 
 
-def _apart(out, *inputs, spans=()):
-    """Outputs must not share memory with inputs: tensors, and ``spans`` of (address, bytes)."""
+def _layout_at(align_out):
+    """Addresses of sorted_pair_ids, pair_rows and num_rows_padded."""
+    return (align_out["sorted_pair_ids"].data_ptr(), align_out["pair_rows"].data_ptr(),
+            align_out["num_rows_padded"].data_ptr())
+
+
+def _apart(out, *inputs):
+    """Outputs must not share memory with inputs; returns the output's first address and the
+    one behind it."""
     lo = out.data_ptr()
     hi = lo + out.nbytes
     for t in inputs:
@@ -684,19 +685,24 @@ def _apart(out, *inputs, spans=()):
             p = t.data_ptr()
             if lo < p + t.nbytes and p < hi:
                 raise ValueError("an output overlaps an input")
-    for p, n in spans:
-        if lo < p + n and p < hi:
-            raise ValueError("an output overlaps the layout")
+    return lo, hi
 
 
-def _no_grad(where, *tensors):
-    """Autograd does not see these calls: where it is on, an input that requires a
-    gradient is refused rather than its gradient lost."""
+def _apart_from_layout(span, at, cap, pairs):
+    """The same of an output's addresses and the arrays of the layout, at _layout_at."""
+    lo, hi = span
+    ids, pair_rows, used = at
+    if (lo < ids + 4 * cap and ids < hi) or (lo < pair_rows + 4 * pairs and pair_rows < hi) or \
+            (lo < used + 4 and used < hi):
+        raise ValueError("an output overlaps the layout")
+
+
+def _requires_grad(where):
+    """For a call with an input that requires a gradient: autograd does not see these
+    calls, and where it is on, the call is refused rather than the gradient lost."""
     if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError(f"{where} is not recorded by autograd and an input requires a gradient: "
-                                 "call it under torch.no_grad() or in a torch.autograd.Function")
+        raise ValueError(f"{where} is not recorded by autograd and an input requires a gradient: "
+                         "call it under torch.no_grad() or in a torch.autograd.Function")
 
 
 def _matrix(t, name, dev=None):
@@ -722,22 +728,22 @@ def moe_lora_permute(x: torch.Tensor, align_out: Dict[str, torch.Tensor], top_k:
     torch.autograd.Function: its gradient is moe_lora_permute_backward, and an x that
     requires a gradient is refused where autograd is on."""
     _matrix(x, "x")
-    _no_grad("moe_lora_permute", x)
+    if x.requires_grad:
+        _requires_grad("moe_lora_permute")
     dt = _row_dtype(x, "x", (torch.uint8,))
-    T, cap, spans = _rows_layout(align_out, top_k, x.device)
+    T, cap = _rows_layout(align_out, top_k, x.device)
     if x.shape[0] != T:
         raise ValueError(f"x has {x.shape[0]} rows, the layout {T} tokens")
-    H = x.shape[1]
+    H, at = x.shape[1], _layout_at(align_out)
     if out is None:
         out = torch.empty((cap, H), dtype=x.dtype, device=x.device)
     else:
         _need(out, "out", x.dtype, x.device)
         if out.shape != (cap, H):
             raise ValueError(f"out must be {(cap, H)}, got {tuple(out.shape)}")
-        _apart(out, x, spans=spans)
-    (ids, _), (pair_rows, _), (used, _) = spans
-    _launch("moe_lora_permute", x.device, lib().moe_lora_permute, T, top_k, H, dt, cap, _at(x), ids,
-            pair_rows, used, _at(out))
+        _apart_from_layout(_apart(out, x), at, cap, T * top_k)
+    _launch("moe_lora_permute", x.device, lib().moe_lora_permute, T, top_k, H, dt, cap, _at(x), *at,
+            _at(out))
     return out
 
 
@@ -746,23 +752,25 @@ def moe_lora_permute_backward(d_rows: torch.Tensor, align_out: Dict[str, torch.T
     """Gradient of moe_lora_permute: dx [T, H], the sum of each token's rows of
     ``d_rows`` (fp32 sums; ``out_dtype`` defaults to the rows' dtype)."""
     _matrix(d_rows, "d_rows")
-    _no_grad("moe_lora_permute_backward", d_rows)
-    T, cap, spans = _rows_layout(align_out, top_k, d_rows.device, d_rows.shape[0])
+    if d_rows.requires_grad:
+        _requires_grad("moe_lora_permute_backward")
+    T, cap = _rows_layout(align_out, top_k, d_rows.device, d_rows.shape[0])
     H = d_rows.shape[1]
     if dx is None:
         dx = torch.empty((T, H), dtype=out_dtype or d_rows.dtype, device=d_rows.device)
     else:
-        _token_out(dx, "dx", T, H, out_dtype, d_rows, spans=spans)
+        _token_out(dx, "dx", T, H, out_dtype, d_rows)
+        _apart_from_layout(_apart(dx, d_rows), _layout_at(align_out), cap, T * top_k)
     _launch("moe_lora_permute_backward", d_rows.device, lib().moe_lora_permute_backward, T, top_k, H,
-            _row_dtype(d_rows, "d_rows"), _row_dtype(dx, "dx"), cap, _at(d_rows), spans[1][0], _at(dx))
+            _row_dtype(d_rows, "d_rows"), _row_dtype(dx, "dx"), cap, _at(d_rows),
+            _at(align_out["pair_rows"]), _at(dx))
     return dx
 
 
-def _token_out(t, name, T, H, out_dtype, rows, *others, spans):
+def _token_out(t, name, T, H, out_dtype, rows):
     _need(t, name, out_dtype, rows.device)
     if t.shape != (T, H):
         raise ValueError(f"{name} must be {(T, H)}, got {tuple(t.shape)}")
-    _apart(t, rows, *others, spans=spans)
 
 
 def _pair_weights(w, T, top_k, dev, name="topk_weights"):
@@ -780,17 +788,19 @@ def moe_lora_unpermute(rows: torch.Tensor, align_out: Dict[str, torch.Tensor], t
     moe_lora_unpermute_backward; rows or weights that require one are refused where
     autograd is on."""
     _matrix(rows, "rows")
-    _no_grad("moe_lora_unpermute", rows, topk_weights)
-    T, cap, spans = _rows_layout(align_out, top_k, rows.device, rows.shape[0])
+    T, cap = _rows_layout(align_out, top_k, rows.device, rows.shape[0])
     H = rows.shape[1]
     if topk_weights is not None:
         _pair_weights(topk_weights, T, top_k, rows.device)
+    if rows.requires_grad or (topk_weights is not None and topk_weights.requires_grad):
+        _requires_grad("moe_lora_unpermute")
     if y is None:
         y = torch.empty((T, H), dtype=out_dtype or rows.dtype, device=rows.device)
     else:
-        _token_out(y, "y", T, H, out_dtype, rows, topk_weights, spans=spans)
+        _token_out(y, "y", T, H, out_dtype, rows)
+        _apart_from_layout(_apart(y, rows, topk_weights), _layout_at(align_out), cap, T * top_k)
     _launch("moe_lora_unpermute", rows.device, lib().moe_lora_unpermute, T, top_k, H,
-            _row_dtype(rows, "rows"), _row_dtype(y, "y"), cap, _at(rows), spans[1][0],
+            _row_dtype(rows, "rows"), _row_dtype(y, "y"), cap, _at(rows), _at(align_out["pair_rows"]),
             _at(topk_weights), _at(y))
     return y
 
@@ -808,9 +818,8 @@ def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
     dy's).  Padding rows of d_rows are zero, rows behind ``num_rows_padded`` are
     left as they are."""
     _matrix(dy, "dy")
-    _no_grad("moe_lora_unpermute_backward", dy, rows, topk_weights)
     dev = dy.device
-    T, cap, spans = _rows_layout(align_out, top_k, dev)
+    T, cap = _rows_layout(align_out, top_k, dev)
     H = dy.shape[1]
     if dy.shape[0] != T:
         raise ValueError(f"dy has {dy.shape[0]} rows, the layout {T} tokens")
@@ -820,13 +829,17 @@ def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
             raise ValueError(f"rows must be {(cap, H)}, got {tuple(rows.shape)}")
     if topk_weights is not None:
         _pair_weights(topk_weights, T, top_k, dev)
+    for t in (dy, rows, topk_weights):
+        if t is not None and t.requires_grad:
+            _requires_grad("moe_lora_unpermute_backward")
     dt = rows.dtype if rows is not None else rows_dtype or dy.dtype
     if d_rows is None:
         d_rows = torch.empty((cap, H), dtype=dt, device=dev)
     _need(d_rows, "d_rows", dt, dev)
     if d_rows.shape != (cap, H):
         raise ValueError(f"d_rows must be {(cap, H)}, got {tuple(d_rows.shape)}")
-    _apart(d_rows, dy, rows, topk_weights, spans=spans)
+    at = _layout_at(align_out)
+    _apart_from_layout(_apart(d_rows, dy, rows, topk_weights), at, cap, T * top_k)
     if rows is None or topk_weights is None:
         if d_weights is not None:
             raise ValueError("d_weights needs rows and topk_weights")
@@ -834,11 +847,10 @@ def moe_lora_unpermute_backward(dy: torch.Tensor, rows: Optional[torch.Tensor],
         d_weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     if d_weights is not None:
         _pair_weights(d_weights, T, top_k, dev, "d_weights")
-        _apart(d_weights, dy, rows, topk_weights, d_rows, spans=spans)
-    (ids, _), (pair_rows, _), (used, _) = spans
+        _apart_from_layout(_apart(d_weights, dy, rows, topk_weights, d_rows), at, cap, T * top_k)
     _launch("moe_lora_unpermute_backward", dev, lib().moe_lora_unpermute_backward, T, top_k, H,
-            _row_dtype(dt, "rows"), _row_dtype(dy, "dy"), cap, _at(dy), _at(rows), ids, pair_rows, used,
-            _at(topk_weights), _at(d_rows), _at(d_weights))
+            _row_dtype(dt, "rows"), _row_dtype(dy, "dy"), cap, _at(dy), _at(rows),
+            *at, _at(topk_weights), _at(d_rows), _at(d_weights))
     return d_rows, d_weights
 
 
@@ -887,6 +899,8 @@ def moe_lora_mx4_quantize(x: torch.Tensor, num_rows_used: Optional[torch.Tensor]
     if K <= 0 or K % 32:
         raise ValueError("the last axis of x must be a multiple of 32")
     lead, dev = tuple(x.shape[:-1]), x.device
+    if num_rows_used is not None:
+        _need(num_rows_used, "num_rows_used", torch.int32, dev, 1)
     given = codes is not None or scales is not None
     if codes is None:
         codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
@@ -898,8 +912,6 @@ def moe_lora_mx4_quantize(x: torch.Tensor, num_rows_used: Optional[torch.Tensor]
             raise ValueError(f"codes must be {(*lead, K // 2)}, got {tuple(codes.shape)}")
         _apart(codes, x, scales, num_rows_used)
         _apart(scales, x, num_rows_used)
-    if num_rows_used is not None:
-        _need(num_rows_used, "num_rows_used", torch.int32, dev, 1)
     _launch("moe_lora_mx4_quantize", dev, lib().moe_lora_mx4_quantize, x.numel() // K, K, dt, _at(x),
             _at(num_rows_used), _at(codes), _at(scales))
     return codes, scales
@@ -947,25 +959,27 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
     E, N = (1 if align_out is None else w_codes.shape[0]), w_codes.shape[-2]
     if x_scales is None:
         _need(x, "x", torch.bfloat16, dev)
-        _no_grad("moe_lora_mx4_gemm", x)
+        if x.requires_grad:
+            _requires_grad("moe_lora_mx4_gemm")
         xk = x.shape[-1] if x.dim() == 2 else -1
     else:
         xk = _mx4_pair(x, x_scales, "x", dev) if x.dim() == 2 else -1
     if x.dim() != 2 or xk != K:
         raise ValueError(f"x {tuple(x.shape)} does not match weights of {K} columns")
-    M, a, spans = x.shape[0], Mx4GemmArgs(), ()
+    M, a, layout = x.shape[0], Mx4GemmArgs(), ()
     if align_out is not None:
         a.block_m = int(align_out["block_m"])
         if a.block_m <= 0 or M % a.block_m:
             raise ValueError("x must hold whole tiles of block_m rows")
         _need(align_out["tile_expert"], "tile_expert", torch.int32, dev, M // a.block_m)
         a.tile_expert = align_out["tile_expert"].data_ptr()
-        spans = ((a.tile_expert, 4 * (M // a.block_m)),)
+        layout = (align_out["tile_expert"],)
         if "pair_rows" in align_out:   # ids past the pairs are padding
             _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, M)
             a.sorted_pair_ids = align_out["sorted_pair_ids"].data_ptr()
-            spans += ((a.sorted_pair_ids, 4 * M),)
-            a.num_pairs = _num_pairs(align_out)
+            layout += (align_out["sorted_pair_ids"],)
+            pairs = align_out.get("num_pairs")
+            a.num_pairs = align_out["pair_rows"].numel() if pairs is None else pairs
     cols = N // 2 if silu_mul else N
     if out is None:
         out = torch.empty((M, cols), dtype=out_dtype or torch.bfloat16, device=dev)
@@ -973,7 +987,7 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
         _need(out, "out", out_dtype, dev)
         if out.shape != (M, cols):
             raise ValueError(f"out must be {(M, cols)}, got {tuple(out.shape)}")
-        _apart(out, x, x_scales, w_codes, w_scales, spans=spans)
+        _apart(out, x, x_scales, w_codes, w_scales, *layout)
     if M == 0:
         return out
     a.struct_size = ctypes.sizeof(Mx4GemmArgs)
@@ -1009,7 +1023,8 @@ def run_mx4_layer(inputs: dict, activations: str = "bf16", block_m: Optional[int
     if activations not in ("bf16", "mx4"):
         raise ValueError("activations must be 'bf16' or 'mx4'")
     x, ids, w = inputs["x"], inputs["topk_ids"], inputs["topk_weights"]
-    _no_grad("run_mx4_layer", x, w)
+    if x.requires_grad or w.requires_grad:
+        _requires_grad("run_mx4_layer")
     T, k = ids.shape
     gu, down = inputs["w_gate_up_mx4"], inputs["w_down_mx4"]
     H, I = _mx4_pair(*gu, "w_gate_up"), _mx4_pair(*down, "w_down")

@@ -301,3 +301,20 @@ def test_every_variant_of_the_products_is_tested():
         by_dma = {(v[1], v[3]) for v in got if v[0] == "tile"}
         assert by_dma == {(rows, dma) for rows in (64, 128, 256)
                           for dma in ((False, True) if kind == "bf16" else (False,))}
+
+
+def test_what_is_no_tensor_is_a_type_error(recorder):
+    al = align(4, 2, pair_rows=True)
+    rows, tokens, bf = dev(al["capacity"], 64), dev(4, 64), torch.bfloat16
+    recorder.calls.clear()
+    for call in (lambda: binding.moe_lora_permute([1], al, 2),
+                 lambda: binding.moe_lora_permute_backward([1], al, 2),
+                 lambda: binding.moe_lora_unpermute(rows, al, 2, [1]),
+                 lambda: binding.moe_lora_unpermute_backward(tokens, [1], al, 2, dev(4, 2)),
+                 lambda: binding.moe_lora_unpermute_backward(tokens, rows, al, 2, 1.0),
+                 lambda: binding.moe_lora_mx4_quantize(rows, 3, codes=dev(len(rows), 32, dtype=torch.uint8)),
+                 lambda: binding.moe_lora_mx4_gemm([1], *mx4(8, 32, 64), align_out=al),
+                 lambda: binding.moe_lora_mx4_gemm(rows.to(bf), *mx4(8, 32, 64), align_out=al, out=1)):
+        with pytest.raises(TypeError):
+            call()
+    assert not recorder.calls
