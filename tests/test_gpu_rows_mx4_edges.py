@@ -199,19 +199,22 @@ def test_short_rows(H, dtype, out):
     """Rows shorter than 16 bytes go element by element, longer ones in pieces of 16 whose
     last one overlaps; bounds as in test_gpu_rows."""
     T, k, E = 70, 3, 7
-    al = binding.moe_lora_align(some_ids(T, k, E, 50) - (torch.arange(T * k, device="cuda").view(T, k) % 5 == 0).int()
-                                * 100, no_slots(T), None, E, 0, 16, pair_rows=True)
+    ids = some_ids(T, k, E, 50)
+    ids.view(-1)[::5] = -1
+    al = binding.moe_lora_align(ids, no_slots(T), None, E, 0, 16, pair_rows=True)
     cap, used = al["capacity"], int(al["num_rows_padded"].cpu()[0])
     pr = ro.pair_rows_of(al["sorted_pair_ids"][:cap].cpu().numpy(), T * k)
     assert (pr < 0).any()
     x = values((T, H), DT[dtype], 51)
     mark = values((cap, H), DT[dtype], 52)
     got = binding.moe_lora_permute(x, al, k, out=mark.clone())
-    assert np.array_equal(got[:used].float().cpu().numpy(), ro.permute(x.float().cpu().numpy(), pr, k, cap)[0][:used])
+    ref = ro.permute(x.float().cpu().numpy(), pr, k, cap)[0]
+    assert np.array_equal(got[:used].float().cpu().numpy(), ref[:used])
     assert torch.equal(got[used:], mark[used:])
     if dtype == "u8":
         return
-    rows, w, dy = values((cap, H), DT[dtype], 53), values((T, k), torch.float32, 54), values((T, H), DT[out], 55)
+    rows, dy = values((cap, H), DT[dtype], 53), values((T, H), DT[out], 55)
+    w = values((T, k), torch.float32, 54)
     ho, hr = HALF[DT[out]], HALF[DT[dtype]]
     for weights_ in (w, None):
         y = binding.moe_lora_unpermute(rows, al, k, weights_, out_dtype=DT[out])
@@ -244,7 +247,8 @@ def test_unaligned_pointers_change_no_bit(H, dt):
         got = (binding.moe_lora_permute(xo, al, k, out=odd(rows, by))[:used],
                binding.moe_lora_unpermute(ro_, al, k, wo, y=odd(x, by)),
                binding.moe_lora_permute_backward(ro_, al, k, dx=odd(x, by)),
-               *binding.moe_lora_unpermute_backward(xo, ro_, al, k, wo, d_rows=odd(rows, by), d_weights=odd(w, by)))
+               *binding.moe_lora_unpermute_backward(xo, ro_, al, k, wo, d_rows=odd(rows, by),
+                                                    d_weights=odd(w, by)))
         for i, (a, b) in enumerate(zip(got, want)):
             n = used if i in (0, 3) else len(a)
             assert torch.equal(a[:n], b[:n]), (by, i)
@@ -294,7 +298,8 @@ def test_padding_of_more_than_one_round():
     want[at] = x
     want[used:] = 9.0
     assert torch.equal(binding.moe_lora_permute(x, al, 1, out=torch.full_like(want, 9.0)), want)
-    assert torch.equal(binding.moe_lora_unpermute_backward(x, None, al, 1, d_rows=torch.full_like(want, 9.0))[0], want)
+    d_rows, _ = binding.moe_lora_unpermute_backward(x, None, al, 1, d_rows=torch.full_like(want, 9.0))
+    assert torch.equal(d_rows, want)
 
 
 # ---------------------------------------------------------------------------
@@ -414,3 +419,50 @@ def test_layer_captured_and_on_two_streams(activations_):
                 got[i].append(binding.run_mx4_layer(batches[i], activations_))
     torch.cuda.synchronize()
     assert all(torch.equal(a, want[i]) for i in range(2) for a in got[i])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mx4"])
+@pytest.mark.parametrize("bm,n", [(16, 3), (64, 3), (64, 5), (256, 3)])
+def test_weights_past_4_gib(kind, bm, n):
+    """The last experts of more than 4 GiB of codes and 256 MiB of scales: the bits of the same
+    call on those weights alone."""
+    E, N, K = 66, 8192, 16384
+    say(f"weights past 4 GiB {kind} block_m {bm} x {n}")
+    g = torch.Generator(device="cuda").manual_seed(130)
+    wc = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(120, 126, (E, N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    assert wc.numel() > 1 << 32
+    x, xs, _ = activations(n * bm, K, kind, 131)
+    tiles = torch.tensor([E - 1, 0, E - 2] + [E - 1] * (n - 3), dtype=torch.int32, device="cuda")
+    few = torch.tensor([0, E - 2, E - 1], device="cuda")
+    alone = torch.tensor([2, 0, 1] + [2] * (n - 3), dtype=torch.int32, device="cuda")
+    y, want = (binding.moe_lora_mx4_gemm(x, c, s, x_scales=xs, align_out=dict(block_m=bm, tile_expert=t))
+               for c, s, t in ((wc, ws, tiles), (wc[few], ws[few], alone)))
+    assert torch.equal(y, want) and bool(y.isfinite().all()) and float(y.abs().max()) > 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mx4"])
+@pytest.mark.parametrize("bm", [16, 64, 256, None])
+@pytest.mark.parametrize("what", ["out", "x"])
+def test_rows_past_4_gib(kind, bm, what):
+    """x or out of more than 4 GiB: rows from all over, against the oracle."""
+    dt = torch.bfloat16
+    M, N, K = (1 << 17, 16480, 32) if what == "out" else (1 << 18, 32, 9280 if kind == "bf16" else 33792)
+    say(f"rows past 4 GiB {kind} block_m {bm} {M} x {N} x {K}")
+    g = torch.Generator(device="cuda").manual_seed(132)
+    if kind == "bf16":
+        x, xs = torch.randn(M, K, generator=g, device="cuda").to(dt), None
+    else:
+        x = torch.randint(0, 256, (M, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+        xs = torch.randint(120, 126, (M, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    assert (M * N * 2 if what == "out" else x.nbytes) > 1 << 32
+    wc, ws, w64 = weights(1, N, K, 133)
+    al = None
+    if bm is None:
+        wc, ws = wc[0], ws[0]
+    else:
+        al = dict(block_m=bm, tile_expert=torch.zeros(M // bm, dtype=torch.int32, device="cuda"))
+    y = binding.moe_lora_mx4_gemm(x, wc, ws, x_scales=xs, align_out=al)
+    at = torch.cat((torch.arange(0, M, 1021), torch.arange(M - 70, M))).cuda()
+    x64 = np64(x[at]) if xs is None else ro.mx4_values(x[at].cpu().numpy(), xs[at].cpu().numpy())
+    check_product(np64(y[at]), dt, x64, w64, np.zeros(len(at), int), False, K, "rows")
