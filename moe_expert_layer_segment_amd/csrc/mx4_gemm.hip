@@ -74,7 +74,7 @@ __device__ __forceinline__ int64_t weight_row(const Mx4Gemm& p, int64_t cb) {
 
 // ---- few rows --------------------------------------------------------------
 // The weights are streamed from memory into registers, once, and bound the kernel.
-// A workgroup holds 16 MB rows and 16 NB columns; its WV waves take every WV-th group
+// A workgroup holds 16 MB rows and 16 NB columns; its WV waves take every WV-th
 // group of four blocks and add their sums through LDS.  Longer groups cost the registers
 // of another workgroup on the CU (7168 x 2048 of 32 experts, MX4 x, tiles of 32 rows:
 // 97 us with eight blocks, 84 with four).
