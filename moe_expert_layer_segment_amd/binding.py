@@ -279,10 +279,10 @@ def moe_lora_align(topk_ids: torch.Tensor, token_lora_mapping: torch.Tensor,
     """Bucket (token, expert) pairs by (expert, adapter); returns the align outputs.
 
     ``pair_rows``: also write ``pair_rows`` (int32 [T * k], the row of each pair or
-    -1), which moe_lora_permute and moe_lora_unpermute need; they are written whenever
-    ``out`` holds a buffer for them, so that none stay from a batch before.  Buffers in
-    ``out`` may be larger than this batch needs; ``num_pairs`` in the result says how many
-    pairs it has."""
+    -1), which moe_lora_permute and moe_lora_unpermute need.  None stay from a batch before:
+    where ``out`` holds a buffer for them they are written unasked, or the buffer leaves it
+    if it is too small.  Buffers in ``out`` may be larger than this batch needs;
+    ``num_pairs`` in the result says how many pairs it has."""
     dev = topk_ids.device
     T, k = topk_ids.shape
     _need(topk_ids, "topk_ids", torch.int32)
@@ -297,9 +297,13 @@ def moe_lora_align(topk_ids: torch.Tensor, token_lora_mapping: torch.Tensor,
             tile_lora=torch.empty(max(cap // block_m, 1), dtype=torch.int32, device=dev),
             expert_tile_offsets=torch.empty(num_experts + 1, dtype=torch.int32, device=dev),
             num_rows_padded=torch.empty(1, dtype=torch.int32, device=dev))
-    pair_rows = pair_rows or "pair_rows" in out
+    held = out.get("pair_rows")
+    if held is not None and not pair_rows:
+        pair_rows = held.numel() >= T * k
+        if not pair_rows:
+            del out["pair_rows"]
     if pair_rows:
-        if "pair_rows" not in out:
+        if held is None:
             out["pair_rows"] = torch.empty(max(T * k, 1), dtype=torch.int32, device=dev)
         _need(out["pair_rows"], "pair_rows", torch.int32, dev, T * k)
     for name, n in (("sorted_pair_ids", cap), ("tile_expert", cap // block_m),
@@ -655,11 +659,12 @@ def _rows_layout(align_out, top_k, dev, num_rows=None):
     """(tokens, rows of the layout) after checking its arrays."""
     if "pair_rows" not in align_out:
         raise ValueError("the layout has no pair_rows (moe_lora_align(..., pair_rows=True))")
-    # pair_rows may be a buffer of more than the batch's pairs
     pr, pairs, cap = align_out["pair_rows"], align_out.get("num_pairs"), int(align_out["capacity"])
-    _need(pr, "pair_rows", torch.int32, dev, pairs)
-    if pairs is None:
-        pairs = pr.numel()
+    _need(pr, "pair_rows", torch.int32, dev)
+    # pair_rows may be a buffer of more than the batch's pairs, or those of its first tokens
+    held = pr.numel()
+    if pairs is None or held < pairs:
+        pairs = held
     _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, cap)
     _need(align_out["num_rows_padded"], "num_rows_padded", torch.int32, dev, 1)
     if top_k <= 0 or (cap > 0 and pairs % top_k):
@@ -978,8 +983,8 @@ def moe_lora_mx4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
             _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, M)
             a.sorted_pair_ids = align_out["sorted_pair_ids"].data_ptr()
             layout += (align_out["sorted_pair_ids"],)
-            pairs = align_out.get("num_pairs")
-            a.num_pairs = align_out["pair_rows"].numel() if pairs is None else pairs
+            held = align_out["pair_rows"].numel()
+            a.num_pairs = min(align_out.get("num_pairs", held), held)
     cols = N // 2 if silu_mul else N
     if out is None:
         out = torch.empty((M, cols), dtype=out_dtype or torch.bfloat16, device=dev)
@@ -1030,13 +1035,13 @@ def run_mx4_layer(inputs: dict, activations: str = "bf16", block_m: Optional[int
     if activations not in ("bf16", "mx4"):
         raise ValueError("activations must be 'bf16' or 'mx4'")
     x, ids, w = inputs["x"], inputs["topk_ids"], inputs["topk_weights"]
-    if x.requires_grad or w.requires_grad:
+    if x.requires_grad or (w is not None and w.requires_grad):
         _requires_grad("run_mx4_layer")
     T, k = ids.shape
     gu, down = inputs["w_gate_up_mx4"], inputs["w_down_mx4"]
     H, I = _mx4_pair(*gu, "w_gate_up"), _mx4_pair(*down, "w_down")
     E = gu[0].shape[0]
-    if gu[0].shape != (E, 2 * I, H // 2) or down[0].shape != (E, H, I // 2) or x.shape != (T, H):
+    if gu[0].shape != (E, 2 * I, H // 2) or down[0].dim() != 3 or down[0].shape[0] != E or x.shape != (T, H):
         raise ValueError(f"x {tuple(x.shape)}, w_gate_up {tuple(gu[0].shape)} and w_down "
                          f"{tuple(down[0].shape)} are not of one layer of {T} tokens: codes "
                          "[E, 2I, H/2] and [E, H, I/2]")

@@ -79,10 +79,13 @@ def test_larger_buffers_keep_the_batch_s_pairs(recorder, T, k):
 
 
 def test_pairs_of_a_layout_made_by_hand(recorder):
-    """Without num_pairs the length of pair_rows counts; with it, pair_rows must hold them."""
+    """Without num_pairs the length of pair_rows counts, as it does where it is less."""
     al = dlayout()
     binding.moe_lora_permute(dev(4, 8), al, 2)
     assert recorder.args("moe_lora_permute")[:2] == [4, 2]
+    recorder.calls.clear()
+    binding.moe_lora_unpermute(dev(64, 8), dict(al, num_pairs=8, pair_rows=al["pair_rows"][:6]), 2)
+    assert recorder.args("moe_lora_unpermute")[:2] == [3, 2]     # the first tokens alone
     with pytest.raises(ValueError):
         binding.moe_lora_permute(dev(5, 8), dict(al, num_pairs=10), 2)
 
@@ -94,11 +97,14 @@ def test_a_reused_layout_keeps_no_pair_rows_of_another_batch(recorder):
     assert align(4, 2, out=al) is al
     assert recorder.args("moe_lora_align_pair_rows")[13].value == al["pair_rows"].data_ptr()
     assert al["num_pairs"] == 8
-    with pytest.raises(ValueError):
-        align(4, 2, out=dict(al, pair_rows=i32(7)))
     recorder.calls.clear()
     assert "pair_rows" not in align(4, 2)
     recorder.args("moe_lora_align")
+    recorder.calls.clear()
+    assert "pair_rows" not in align(4, 2, out=dict(al, pair_rows=i32(7)))   # unasked, too small
+    recorder.args("moe_lora_align")
+    with pytest.raises(ValueError):
+        align(4, 2, out=dict(al, pair_rows=i32(7)), pair_rows=True)
 
 
 def mx4(E, N, K):
@@ -116,9 +122,10 @@ def layer(T=5, k=2, E=8, H=96, I=64, **over):  # noqa: E741
 def test_mx4_layer_takes_weights_of_one_layer(recorder, activations):
     assert binding.run_mx4_layer(layer(), activations).shape == (5, 96)
     assert binding.run_mx4_layer(layer(T=0), activations).shape == (0, 96)
+    assert binding.run_mx4_layer(layer(w_down_mx4=mx4(8, 128, 64)), activations).shape == (5, 128)
+    assert binding.run_mx4_layer(layer(topk_weights=None), activations).shape == (5, 96)
     bad = [dict(w_down_mx4=mx4(7, 96, 64)),        # fewer experts: rows of the others stay unwritten
            dict(w_down_mx4=mx4(9, 96, 64)),
-           dict(w_down_mx4=mx4(8, 128, 64)),       # another hidden
            dict(w_down_mx4=mx4(8, 96, 32)),        # another inner width
            dict(w_gate_up_mx4=mx4(8, 64, 96)),     # the gate alone
            dict(w_gate_up_mx4=mx4(8, 128, 64)),
