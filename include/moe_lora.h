@@ -539,6 +539,142 @@ typedef struct moe_lora_mx4_gemm_args {
 
 int moe_lora_mx4_gemm(const moe_lora_mx4_gemm_args* args, void* stream);
 
+/*
+ * Rows in 8-bit integers: codes [num_rows, cols] int8 under one scale for each row,
+ * scales [num_rows] float32.  A value stands for code * scale.
+ *
+ *   scale = (largest magnitude of the row) / 127, rounded to fp32
+ *   code  = value / scale, to the nearest integer, ties to even, within [-127, 127]
+ *
+ * exactly: the same on every device.  A row that holds an infinity or a NaN gets the
+ * scale NaN and codes 0; a row of zeros (or of magnitudes whose scale is 0 in fp32) the
+ * scale 0 and codes 0.
+ *
+ * moe_lora_int8_quantize: x [num_rows, cols].  For weights the rows are the output
+ * channels of every expert.
+ *   num_rows_used  device int32, or NULL: rows from *num_rows_used on are skipped
+ *                  and their outputs left as they were (num_rows_padded of align).
+ * moe_lora_int8_dequantize: out = code * scale, rounded once to dtype.
+ * dtype (of x / out): F32 or BF16.  1 <= cols <= 2^24, num_rows * cols <= 2^40.  Any
+ * pointer aligned to its element works.
+ */
+int moe_lora_int8_quantize(int64_t num_rows, int32_t cols, int32_t dtype, const void* x,
+                           const int32_t* num_rows_used, int8_t* codes, float* scales,
+                           void* stream);
+int moe_lora_int8_dequantize(int64_t num_rows, int32_t cols, int32_t dtype, const int8_t* codes,
+                             const float* scales, void* out, void* stream);
+
+/*
+ * moe_lora_rms_norm_quantize -- the norm in front of the layer, with the residual's
+ * addition before it and 8-bit integers behind it:
+ *
+ *   h = x + residual,   n = h * weight / sqrt(mean(h^2) + eps)
+ *
+ *   x, residual   [num_tokens, hidden] in dtype; residual NULL: h = x.
+ *   weight        [hidden] in weight_dtype.
+ *   codes, scales n in 8-bit integers, as moe_lora_int8_quantize of n: of n unrounded, and
+ *                 n is that of h unrounded.
+ *   residual_out  [num_tokens, hidden] out, h in dtype; NULL: not written.  May be
+ *                 `residual` or `x` itself; no other output may overlap an input.
+ *   y             [num_tokens, hidden] out, n in y_dtype (for the router); NULL: not written.
+ * dtypes: F32 or BF16 each.  1 <= hidden <= 16384 (else MOE_LORA_ERR_UNSUPPORTED),
+ * eps >= 0 and finite.  Any pointer aligned to its element works.
+ */
+int moe_lora_rms_norm_quantize(int64_t num_tokens, int32_t hidden, int32_t dtype,
+                               int32_t weight_dtype, int32_t y_dtype, double eps, const void* x,
+                               const void* residual, const void* weight, int8_t* codes,
+                               float* scales, void* residual_out, void* y, void* stream);
+
+/*
+ * moe_lora_int8_gemm -- products of rows in 8-bit integers with weights in 8-bit
+ * integers, of rows in expert order or of all rows with one weight:
+ *
+ *   y[m, n] = (sum_k x[m, k] w_e[n, k]) * x_scale[m] * w_scale[e, n],   e = tile_expert[m / block_m]
+ *   out = y, or with silu_mul (out_features = 2 I; rows [0, I) of W are gate, [I, 2I)
+ *   up, as in w_gate_up)  out[m, i] = SiLU(y[m, i]) * y[m, I + i].
+ *
+ *   x        [num_rows, in_features] int8, x_scale [num_rows] float32.
+ *   w        [num_experts, out_features, in_features] int8, w_scale [num_experts,
+ *            out_features] float32.
+ *   tile_expert [num_rows / block_m] of moe_lora_align for this block_m; num_rows is a
+ *            multiple of block_m.  Rows of tiles whose entry is outside [0,
+ *            num_experts) (-1 past the end) are left as they were.  NULL: one weight
+ *            (num_experts == 1) for every row, any num_rows.
+ *   sorted_pair_ids [num_rows] of moe_lora_align and num_pairs = num_tokens * top_k, or
+ *            NULL.  With them padding rows (entries outside [0, num_pairs)) get zeros,
+ *            whatever x, the scales and W hold.
+ *   top_k    0, or > 0 to read x where the tokens lie: x is [num_tokens, in_features],
+ *            x_scale [num_tokens], and row m reads token sorted_pair_ids[m] / top_k.  Needs
+ *            sorted_pair_ids, num_pairs <= num_tokens * top_k, and num_tokens *
+ *            in_features < 2^32.
+ *   out      [num_rows, out_features] (silu_mul: out_features / 2), BF16 or F32.
+ *
+ * Sums are int32 and exact; y is the sum rounded to fp32, times the two scales in that
+ * order, and out rounds once more to its type.  A row's result depends on that row alone.
+ * block_m as for moe_lora_mx4_gemm.  in_features: a multiple of 16, at most 131056 (2^17 -
+ * 16); out_features: a multiple of 16 (32 with silu_mul), at most 2^24; num_rows / 16 *
+ * out_features / 64 < 2^24 (else MOE_LORA_ERR_UNSUPPORTED).  x, w and out 16-byte aligned.
+ * No workspace.
+ */
+typedef struct moe_lora_int8_gemm_args {
+  size_t struct_size; /* sizeof(moe_lora_int8_gemm_args) */
+  int32_t out_dtype;  /* MOE_LORA_BF16 or MOE_LORA_F32 */
+  int32_t silu_mul;
+  int64_t num_rows;
+  int32_t out_features, in_features, num_experts, block_m;
+  const int8_t* x;
+  const float* x_scale;
+  const int8_t* w;
+  const float* w_scale;
+  const int32_t* tile_expert;
+  const int32_t* sorted_pair_ids;
+  int32_t num_pairs;
+  int32_t top_k;
+  int64_t num_tokens; /* rows of x with top_k */
+  void* out;
+} moe_lora_int8_gemm_args;
+
+int moe_lora_int8_gemm(const moe_lora_int8_gemm_args* args, void* stream);
+
+/*
+ * moe_lora_balance_loss -- pairs per expert and the loss that keeps them even.  Over the
+ * n tokens that take part, with p_t = softmax(logits_t):
+ *
+ *   counts[e]     = pairs (t, j) of these tokens with topk_ids[t, j] == e
+ *   mean_probs[e] = sum_t p_t[e] / n
+ *   loss          = num_experts / (n * top_k) * sum_e counts[e] * mean_probs[e]
+ *
+ *   logits      [num_tokens, num_experts] in dtype (F32 or BF16).  -inf switches an expert
+ *               off for a token (probability 0); in a row of -inf alone all are 0.
+ *   topk_ids    [num_tokens, top_k] int32 (moe_lora_route); ids outside [0, num_experts)
+ *               are counted nowhere.
+ *   token_mask  [num_tokens] bytes, 0 for tokens that take no part (padding; their logits and
+ *               ids may be anything), or NULL: all do.
+ *   loss [1], counts [num_experts] int32, mean_probs [num_experts], num_valid [1] int32 (n)  out.
+ *   workspace   >= moe_lora_balance_loss_workspace_bytes(num_tokens, num_experts) bytes.
+ * With n = 0 everything is 0.  Sums over tokens are fp64, in an order that does not change.
+ *
+ * moe_lora_balance_loss_backward: the gradient for the logits (counts are constants),
+ *
+ *   d_logits[t, e] = d_loss * num_experts / (n^2 top_k) * p_t[e] * (counts[e] - sum_i p_t[i] counts[i])
+ *
+ * and 0 for tokens that take no part.  counts and num_valid are those of the forward pass,
+ * or their sums over the ranks of a data-parallel batch.
+ *   d_loss      [1] float32 device, or NULL for 1.
+ *   d_logits    [num_tokens, num_experts] out, in out_dtype.
+ * num_experts <= 1024, num_tokens * top_k < 2^30 (else MOE_LORA_ERR_UNSUPPORTED).
+ */
+size_t moe_lora_balance_loss_workspace_bytes(int32_t num_tokens, int32_t num_experts);
+int moe_lora_balance_loss(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t dtype,
+                          const void* logits, const int32_t* topk_ids, const uint8_t* token_mask,
+                          float* loss, int32_t* counts, float* mean_probs, int32_t* num_valid,
+                          void* workspace, size_t workspace_bytes, void* stream);
+int moe_lora_balance_loss_backward(int32_t num_tokens, int32_t num_experts, int32_t top_k,
+                                   int32_t dtype, int32_t out_dtype, const void* logits,
+                                   const uint8_t* token_mask, const int32_t* counts,
+                                   const int32_t* num_valid, const float* d_loss, void* d_logits,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -111,6 +111,24 @@ def _load(path: str) -> ctypes.CDLL:
                                           [ctypes.c_void_p] * 4)
     L.moe_lora_mx4_gemm.restype = ctypes.c_int
     L.moe_lora_mx4_gemm.argtypes = [ctypes.POINTER(Mx4GemmArgs), ctypes.c_void_p]
+    L.moe_lora_int8_quantize.restype = ctypes.c_int
+    L.moe_lora_int8_quantize.argtypes = ([ctypes.c_int64] + [ctypes.c_int32] * 2 +
+                                         [ctypes.c_void_p] * 5)
+    L.moe_lora_int8_dequantize.restype = ctypes.c_int
+    L.moe_lora_int8_dequantize.argtypes = ([ctypes.c_int64] + [ctypes.c_int32] * 2 +
+                                           [ctypes.c_void_p] * 4)
+    L.moe_lora_rms_norm_quantize.restype = ctypes.c_int
+    L.moe_lora_rms_norm_quantize.argtypes = ([ctypes.c_int64] + [ctypes.c_int32] * 4 +
+                                             [ctypes.c_double] + [ctypes.c_void_p] * 8)
+    L.moe_lora_int8_gemm.restype = ctypes.c_int
+    L.moe_lora_int8_gemm.argtypes = [ctypes.POINTER(Int8GemmArgs), ctypes.c_void_p]
+    L.moe_lora_balance_loss_workspace_bytes.restype = ctypes.c_size_t
+    L.moe_lora_balance_loss_workspace_bytes.argtypes = [ctypes.c_int32] * 2
+    L.moe_lora_balance_loss.restype = ctypes.c_int
+    L.moe_lora_balance_loss.argtypes = ([ctypes.c_int32] * 4 + [ctypes.c_void_p] * 8 +
+                                        [ctypes.c_size_t, ctypes.c_void_p])
+    L.moe_lora_balance_loss_backward.restype = ctypes.c_int
+    L.moe_lora_balance_loss_backward.argtypes = [ctypes.c_int32] * 5 + [ctypes.c_void_p] * 7
     L.moe_lora_forward_workspace_bytes.restype = ctypes.c_size_t
     L.moe_lora_forward_workspace_bytes.argtypes = [ctypes.POINTER(ForwardArgs)]
     L.moe_lora_forward.restype = ctypes.c_int
@@ -1060,3 +1078,360 @@ def run_mx4_layer(inputs: dict, activations: str = "bf16", block_m: Optional[int
         act = moe_lora_mx4_gemm(moe_lora_permute(x, al, k), *gu, align_out=al, silu_mul=True)
         z = moe_lora_mx4_gemm(act, *down, align_out=al, out_dtype=torch.float32)
     return moe_lora_unpermute(z, al, k, w, out_dtype=out_dtype or x.dtype)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit integers under one scale for each row
+# ---------------------------------------------------------------------------
+class Int8GemmArgs(ctypes.Structure):
+    """Mirror of ``moe_lora_int8_gemm_args``."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("out_dtype", ctypes.c_int32), ("silu_mul", ctypes.c_int32),
+        ("num_rows", ctypes.c_int64),
+        ("out_features", ctypes.c_int32), ("in_features", ctypes.c_int32),
+        ("num_experts", ctypes.c_int32), ("block_m", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p),
+        ("w", ctypes.c_void_p), ("w_scale", ctypes.c_void_p),
+        ("tile_expert", ctypes.c_void_p), ("sorted_pair_ids", ctypes.c_void_p),
+        ("num_pairs", ctypes.c_int32), ("top_k", ctypes.c_int32),
+        ("num_tokens", ctypes.c_int64), ("out", ctypes.c_void_p),
+    ]
+
+
+def _int8_pair(codes, scales, name, dev=None):
+    """Checks codes [.., K] and scales [..]; returns K."""
+    _need(codes, f"{name} codes", torch.int8, dev)
+    _need(scales, f"{name} scales", torch.float32, codes.device)
+    if codes.dim() < 1 or scales.shape != codes.shape[:-1]:
+        raise ValueError(f"{name} must be codes [.., K] and scales [..], got {tuple(codes.shape)} "
+                         f"and {tuple(scales.shape)}")
+    return codes.shape[-1]
+
+
+def _int8_outputs(x, codes, scales, *inputs):
+    """Codes and scales for x [.., K], made or checked."""
+    shape, dev = tuple(x.shape), x.device
+    given = codes is not None or scales is not None
+    if codes is None:
+        codes = torch.empty(shape, dtype=torch.int8, device=dev)
+    if scales is None:
+        scales = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    if given:
+        _int8_pair(codes, scales, "the output", dev)
+        if codes.shape != shape:
+            raise ValueError(f"codes must be {shape}, got {tuple(codes.shape)}")
+        _apart(codes, x, scales, *inputs)
+        _apart(scales, x, *inputs)
+    return codes, scales
+
+
+def moe_lora_int8_quantize(x: torch.Tensor, num_rows_used: Optional[torch.Tensor] = None,
+                           codes: Optional[torch.Tensor] = None,
+                           scales: Optional[torch.Tensor] = None):
+    """(codes int8 [.., K], scales float32 [..]) of x [.., K], float32 or bfloat16: one
+    scale for each row.  Weights [E, N, K] get one for each output channel.
+
+    ``num_rows_used``: device int32 [1]; rows of x (all leading axes together) from
+    it on are skipped, their outputs left as they are (``num_rows_padded`` of
+    moe_lora_align).  There is no gradient: an x that requires one is refused where
+    autograd is on."""
+    _need(x, "x")
+    dt = _row_dtype(x, "x")
+    if x.requires_grad:
+        _requires_grad("moe_lora_int8_quantize")
+    K = x.shape[-1] if x.dim() else 0
+    if K <= 0:
+        raise ValueError("x must have a last axis")
+    if num_rows_used is not None:
+        _need(num_rows_used, "num_rows_used", torch.int32, x.device, 1)
+    codes, scales = _int8_outputs(x, codes, scales, num_rows_used)
+    _launch("moe_lora_int8_quantize", x.device, lib().moe_lora_int8_quantize, x.numel() // K, K, dt,
+            _at(x), _at(num_rows_used), _at(codes), _at(scales))
+    return codes, scales
+
+
+def moe_lora_int8_dequantize(codes: torch.Tensor, scales: torch.Tensor,
+                             out: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
+    """The values [.., K] that codes and scales stand for (bfloat16 unless ``out_dtype``
+    or ``out`` says float32)."""
+    K = _int8_pair(codes, scales, "x")
+    if out is None:
+        out = torch.empty(codes.shape, dtype=out_dtype or torch.bfloat16, device=codes.device)
+    else:
+        _need(out, "out", out_dtype, codes.device)
+        if out.shape != codes.shape:
+            raise ValueError(f"out must be {tuple(codes.shape)}, got {tuple(out.shape)}")
+        _apart(out, codes, scales)
+    if K == 0:
+        return out
+    _launch("moe_lora_int8_dequantize", codes.device, lib().moe_lora_int8_dequantize,
+            codes.numel() // K, K, _row_dtype(out, "out"), _at(codes), _at(scales), _at(out))
+    return out
+
+
+def moe_lora_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                               residual: Optional[torch.Tensor] = None, y_dtype=None,
+                               codes: Optional[torch.Tensor] = None,
+                               scales: Optional[torch.Tensor] = None,
+                               residual_out: Optional[torch.Tensor] = None,
+                               y: Optional[torch.Tensor] = None):
+    """h = x + residual; n = h * weight / sqrt(mean(h^2) + eps) in 8-bit integers: returns
+    (codes int8 [.., H], scales float32 [..], h, n).
+
+    x [.., H], float32 or bfloat16; ``residual`` like it.  ``weight`` [H], either type.
+    h is returned in x's dtype, and None without a residual; ``residual_out`` is where it goes
+    (the residual or x itself, to change it in place).  n is returned if ``y_dtype`` names its
+    dtype or ``y`` is given (for a router, which takes it unquantized), else None.  The codes are
+    those of n and h unrounded.  For serving: there is no gradient, and inputs that require one
+    are refused where autograd is on."""
+    _need(x, "x")
+    dt, dev = _row_dtype(x, "x"), x.device
+    H = x.shape[-1] if x.dim() else 0
+    if H <= 0:
+        raise ValueError("x must have a last axis")
+    _need(weight, "weight", None, dev)
+    wdt = _row_dtype(weight, "weight")
+    if weight.shape != (H,):
+        raise ValueError(f"weight must be [{H}], got {tuple(weight.shape)}")
+    if residual is not None:
+        _need(residual, "residual", x.dtype, dev)
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must be {tuple(x.shape)}, got {tuple(residual.shape)}")
+    for t in (x, weight, residual):
+        if t is not None and t.requires_grad:
+            _requires_grad("moe_lora_rms_norm_quantize")
+    codes, scales = _int8_outputs(x, codes, scales, weight, residual)
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out needs a residual")
+        _need(residual_out, "residual_out", x.dtype, dev)
+        if residual_out.shape != x.shape:
+            raise ValueError(f"residual_out must be {tuple(x.shape)}, got {tuple(residual_out.shape)}")
+        # in place: the same elements, or none of them
+        at = residual_out.data_ptr()
+        _apart(residual_out, None if x.data_ptr() == at else x,
+               None if residual.data_ptr() == at else residual, weight, codes, scales)
+    elif residual is not None:
+        residual_out = torch.empty_like(x)
+    if y is None:
+        if y_dtype is not None:
+            y = torch.empty(x.shape, dtype=y_dtype, device=dev)
+    else:
+        _need(y, "y", y_dtype, dev)
+        if y.shape != x.shape:
+            raise ValueError(f"y must be {tuple(x.shape)}, got {tuple(y.shape)}")
+        _apart(y, x, weight, residual, codes, scales, residual_out)
+    _launch("moe_lora_rms_norm_quantize", dev, lib().moe_lora_rms_norm_quantize, x.numel() // H, H, dt,
+            wdt, dt if y is None else _row_dtype(y, "y"), float(eps), _at(x), _at(residual), _at(weight),
+            _at(codes), _at(scales), _at(residual_out), _at(y))
+    return codes, scales, residual_out, y
+
+
+def moe_lora_int8_gemm(x: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor,
+                       w_scales: torch.Tensor, align_out: Optional[Dict[str, torch.Tensor]] = None,
+                       top_k: Optional[int] = None, silu_mul: bool = False,
+                       out: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
+    """x W^T of 8-bit integers, times the scales of x's rows and of the output channels;
+    ``silu_mul``: SiLU(gate) * up of the two halves of the output columns.
+
+    ``align_out`` None: w_codes [N, K], w_scales [N], x [M, K] and x_scales [M] of any M.
+    Otherwise w_codes [E, N, K], w_scales [E, N], and x [capacity, K] in expert order
+    (moe_lora_permute of the codes, and of the scales as [T, 1]); or, with ``top_k``, x [T, K] as
+    the tokens lie, each of which is read for its ``top_k`` pairs.  Rows behind the last used
+    tile are left as they are in ``out`` (undefined when it is not given).  With ``pair_rows``
+    in align_out, and with ``top_k``, padding rows get zeros, whatever x and the weights hold.
+    ``out`` / ``out_dtype``: bfloat16 (the default) or float32.  There is no gradient."""
+    K = _int8_pair(w_codes, w_scales, "w")
+    dev = w_codes.device
+    if w_codes.dim() != (2 if align_out is None else 3):
+        raise ValueError("w_codes must be [N, K], or [E, N, K] with align_out")
+    E, N = (1 if align_out is None else w_codes.shape[0]), w_codes.shape[-2]
+    if _int8_pair(x, x_scales, "x", dev) != K or x.dim() != 2:
+        raise ValueError(f"x {tuple(x.shape)} does not match weights of {K} columns")
+    M, a, layout = x.shape[0], Int8GemmArgs(), ()
+    if align_out is None:
+        if top_k is not None:
+            raise ValueError("top_k needs align_out")
+    else:
+        a.block_m = int(align_out["block_m"])
+        pairs = align_out.get("num_pairs")
+        held = align_out["pair_rows"].numel() if "pair_rows" in align_out else None
+        if held is not None:
+            pairs = held if pairs is None else min(pairs, held)
+        if top_k is not None:
+            if top_k <= 0 or pairs is None or pairs > M * top_k:
+                raise ValueError(f"x has {M} tokens, the layout {pairs} pairs of {top_k} a token")
+            a.top_k, a.num_tokens = top_k, M
+            M = int(align_out["capacity"])
+        if a.block_m <= 0 or M % a.block_m:
+            raise ValueError("x must hold whole tiles of block_m rows")
+        _need(align_out["tile_expert"], "tile_expert", torch.int32, dev, M // a.block_m)
+        a.tile_expert = align_out["tile_expert"].data_ptr()
+        layout = (align_out["tile_expert"],)
+        if held is not None or top_k is not None:   # ids past the pairs are padding
+            _need(align_out["sorted_pair_ids"], "sorted_pair_ids", torch.int32, dev, M)
+            a.sorted_pair_ids = align_out["sorted_pair_ids"].data_ptr()
+            layout += (align_out["sorted_pair_ids"],)
+            a.num_pairs = pairs
+    cols = N // 2 if silu_mul else N
+    if out is None:
+        out = torch.empty((M, cols), dtype=out_dtype or torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", out_dtype, dev)
+        if out.shape != (M, cols):
+            raise ValueError(f"out must be {(M, cols)}, got {tuple(out.shape)}")
+        _apart(out, x, x_scales, w_codes, w_scales, *layout)
+    if M == 0:
+        return out
+    a.struct_size = ctypes.sizeof(Int8GemmArgs)
+    a.out_dtype = _row_dtype(out, "out")
+    a.num_rows, a.out_features, a.in_features, a.num_experts = M, N, K, E
+    a.silu_mul = int(bool(silu_mul))
+    a.x, a.x_scale, a.w, a.w_scale, a.out = (x.data_ptr(), x_scales.data_ptr(), w_codes.data_ptr(),
+                                             w_scales.data_ptr(), out.data_ptr())
+    _launch("moe_lora_int8_gemm", dev, lib().moe_lora_int8_gemm, ctypes.byref(a))
+    return out
+
+
+def run_int8_layer(inputs: dict, block_m: Optional[int] = None, out_dtype=None) -> torch.Tensor:
+    """The MoE layer without adapters on expert weights and activations in 8-bit integers:
+    align -> gate_up product of the tokens with SiLU * up -> quantize -> down product ->
+    unpermute.
+
+    ``inputs``: topk_ids, topk_weights, the weights w_gate_up_int8 [E, 2I, H] and
+    w_down_int8 [E, H, I], each a (codes, scales) pair of moe_lora_int8_quantize, and the
+    tokens: x_int8, a (codes [T, H], scales [T]) pair of moe_lora_rms_norm_quantize or
+    moe_lora_int8_quantize, or x [T, H] float32 or bfloat16, which is quantized first.
+    Returns y [T, H] in ``out_dtype`` (x's dtype, or bfloat16).  For serving: there is no
+    gradient, and x or topk_weights that require one are refused where autograd is on."""
+    ids, w = inputs["topk_ids"], inputs["topk_weights"]
+    x = inputs.get("x_int8")
+    if x is None:
+        if inputs["x"].requires_grad:
+            _requires_grad("run_int8_layer")
+        out_dtype = out_dtype or inputs["x"].dtype
+        x = moe_lora_int8_quantize(inputs["x"])
+    if w is not None and w.requires_grad:
+        _requires_grad("run_int8_layer")
+    T, k = ids.shape
+    gu, down = inputs["w_gate_up_int8"], inputs["w_down_int8"]
+    H, I = _int8_pair(*gu, "w_gate_up"), _int8_pair(*down, "w_down")
+    E = gu[0].shape[0]
+    if gu[0].shape != (E, 2 * I, H) or down[0].shape != (E, H, I) or x[0].shape != (T, H):
+        raise ValueError(f"x {tuple(x[0].shape)}, w_gate_up {tuple(gu[0].shape)} and w_down "
+                         f"{tuple(down[0].shape)} are not of one layer of {T} tokens: codes "
+                         "[E, 2I, H] and [E, H, I]")
+    if block_m is None:
+        block_m = mx4_block_m(T, k, E)
+    slots = torch.full((max(T, 1),), -1, dtype=torch.int32, device=ids.device)
+    al = moe_lora_align(ids, slots, None, E, 0, block_m, pair_rows=True)
+    act = moe_lora_int8_gemm(*x, *gu, align_out=al, top_k=k, silu_mul=True)
+    codes, scales = moe_lora_int8_quantize(act, al["num_rows_padded"])
+    z = moe_lora_int8_gemm(codes, scales, *down, align_out=al, out_dtype=torch.float32)
+    return moe_lora_unpermute(z, al, k, w, out_dtype=out_dtype or torch.bfloat16)
+
+
+# ---------------------------------------------------------------------------
+# balance loss of the router
+# ---------------------------------------------------------------------------
+def moe_lora_balance_loss_workspace_bytes(num_tokens: int, num_experts: int) -> int:
+    return int(lib().moe_lora_balance_loss_workspace_bytes(num_tokens, num_experts))
+
+
+def _token_mask(mask, T, dev):
+    if mask is None:
+        return
+    _need(mask, "token_mask", None, dev)
+    if mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"token_mask must be bool or uint8, got {mask.dtype}")
+    if mask.numel() != T:
+        raise ValueError(f"token_mask must be [{T}], got {tuple(mask.shape)}")
+
+
+def moe_lora_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
+                          token_mask: Optional[torch.Tensor] = None,
+                          out: Optional[Dict[str, torch.Tensor]] = None,
+                          workspace: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+    """Pairs per expert and the router's balance loss E / (n k) sum_e counts_e mean_probs_e,
+    over the n tokens that ``token_mask`` (bool or uint8 [T]; None: all) lets take part.
+
+    logits [T, E] float32 or bfloat16, topk_ids int32 [T, k] (moe_lora_route); ids outside
+    [0, E) count nowhere.  Returns loss float32 [1], counts int32 [E], mean_probs float32 [E],
+    num_valid int32 [1] (n) and top_k; ``out`` may hold the first four.
+
+    Its gradient is moe_lora_balance_loss_backward: logits that require one are refused where
+    autograd is on, the call belongs into a torch.autograd.Function."""
+    _matrix(logits, "logits")
+    dt, dev = _row_dtype(logits, "logits"), logits.device
+    if logits.requires_grad:
+        _requires_grad("moe_lora_balance_loss")
+    T, E = logits.shape
+    _need(topk_ids, "topk_ids", torch.int32, dev)
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+        raise ValueError(f"topk_ids must be [{T}, k], got {tuple(topk_ids.shape)}")
+    _token_mask(token_mask, T, dev)
+    shapes = dict(loss=(torch.float32, 1), counts=(torch.int32, E), mean_probs=(torch.float32, E),
+                  num_valid=(torch.int32, 1))
+    given = out is not None
+    stats = dict(out) if given else {}
+    for name, (dtype, n) in shapes.items():
+        if stats.get(name) is None:
+            stats[name] = torch.empty(n, dtype=dtype, device=dev)
+        elif stats[name].shape != (n,):
+            raise ValueError(f"{name} must be [{n}], got {tuple(stats[name].shape)}")
+        if given:
+            _need(stats[name], name, dtype, dev)
+    wsb = moe_lora_balance_loss_workspace_bytes(T, E)
+    if workspace is None:
+        workspace = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, dev, wsb)
+    if given:
+        for name in shapes:
+            _apart(stats[name], logits, topk_ids, token_mask, workspace,
+                   *(stats[n] for n in shapes if n != name))
+    _launch("moe_lora_balance_loss", dev, lib().moe_lora_balance_loss, T, E, topk_ids.shape[1], dt,
+            _at(logits), _at(topk_ids), _at(token_mask), _at(stats["loss"]), _at(stats["counts"]),
+            _at(stats["mean_probs"]), _at(stats["num_valid"]), _at(workspace), workspace.numel())
+    stats["top_k"] = topk_ids.shape[1]
+    return stats
+
+
+def moe_lora_balance_loss_backward(d_loss: Optional[torch.Tensor], logits: torch.Tensor,
+                                   stats: Dict[str, torch.Tensor],
+                                   token_mask: Optional[torch.Tensor] = None,
+                                   d_logits: Optional[torch.Tensor] = None,
+                                   out_dtype=None) -> torch.Tensor:
+    """Gradient of moe_lora_balance_loss for the logits: d_logits [T, E] in the logits' dtype
+    unless ``out_dtype`` or ``d_logits`` says otherwise.
+
+    ``d_loss``: device float32 [1], or None for 1.  ``stats``: what the forward call returned;
+    of a batch spread over ranks, with counts and num_valid summed over them (then the ranks'
+    gradients are those of the whole batch's loss)."""
+    _matrix(logits, "logits")
+    dt, dev = _row_dtype(logits, "logits"), logits.device
+    T, E = logits.shape
+    for t in (logits, d_loss):
+        if t is not None and t.requires_grad:
+            _requires_grad("moe_lora_balance_loss_backward")
+    if d_loss is not None:
+        _need(d_loss, "d_loss", torch.float32, dev)
+        if d_loss.numel() != 1:
+            raise ValueError(f"d_loss must be one number, got {tuple(d_loss.shape)}")
+    _need(stats["counts"], "counts", torch.int32, dev)
+    if stats["counts"].shape != (E,):
+        raise ValueError(f"counts must be [{E}], got {tuple(stats['counts'].shape)}")
+    _need(stats["num_valid"], "num_valid", torch.int32, dev, 1)
+    _token_mask(token_mask, T, dev)
+    if d_logits is None:
+        d_logits = torch.empty((T, E), dtype=out_dtype or logits.dtype, device=dev)
+    else:
+        _need(d_logits, "d_logits", out_dtype, dev)
+        if d_logits.shape != (T, E):
+            raise ValueError(f"d_logits must be {(T, E)}, got {tuple(d_logits.shape)}")
+        _apart(d_logits, logits, d_loss, stats["counts"], stats["num_valid"], token_mask)
+    _launch("moe_lora_balance_loss_backward", dev, lib().moe_lora_balance_loss_backward, T, E,
+            int(stats["top_k"]), dt, _row_dtype(d_logits, "d_logits"), _at(logits), _at(token_mask),
+            _at(stats["counts"]), _at(stats["num_valid"]), _at(d_loss), _at(d_logits))
+    return d_logits

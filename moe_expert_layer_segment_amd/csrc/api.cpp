@@ -483,4 +483,156 @@ int moe_lora_mx4_gemm(const moe_lora_mx4_gemm_args* a, void* stream) {
   return hip_status(launch_mx4_gemm(p, static_cast<hipStream_t>(stream)));
 }
 
+// ---- 8-bit integers --------------------------------------------------------
+
+static int int8_shape(int64_t num_rows, int32_t cols, int32_t dtype, int64_t max_cols) {
+  if (num_rows < 0 || cols <= 0) return MOE_LORA_ERR_INVALID;
+  if (!float_dtype(dtype) || cols > max_cols || num_rows > (int64_t(1) << 40) / cols)
+    return MOE_LORA_ERR_UNSUPPORTED;
+  return MOE_LORA_OK;
+}
+
+static bool off_by_word(const void* ptr) { return off_by_element(ptr, MOE_LORA_F32); }
+
+int moe_lora_int8_quantize(int64_t num_rows, int32_t cols, int32_t dtype, const void* x,
+                           const int32_t* num_rows_used, int8_t* codes, float* scales,
+                           void* stream) {
+  const int st = int8_shape(num_rows, cols, dtype, kMaxCols);
+  if (st != MOE_LORA_OK) return st;
+  if (num_rows == 0) return MOE_LORA_OK;
+  if (!x || !codes || !scales || off_by_element(x, dtype) || off_by_word(scales) || off_by_word(num_rows_used))
+    return MOE_LORA_ERR_INVALID;
+  Int8Rows p = {};
+  p.num_rows = num_rows; p.cols = cols;
+  p.x_f32 = dtype == MOE_LORA_F32;
+  p.x = x; p.rows_used = num_rows_used; p.codes = codes; p.scales = scales;
+  return hip_status(launch_int8_rows(p, static_cast<hipStream_t>(stream)));
+}
+
+int moe_lora_int8_dequantize(int64_t num_rows, int32_t cols, int32_t dtype, const int8_t* codes,
+                             const float* scales, void* out, void* stream) {
+  const int st = int8_shape(num_rows, cols, dtype, kMaxCols);
+  if (st != MOE_LORA_OK) return st;
+  if (num_rows == 0) return MOE_LORA_OK;
+  if (!out || !codes || !scales || off_by_element(out, dtype) || off_by_word(scales))
+    return MOE_LORA_ERR_INVALID;
+  return hip_status(launch_int8_dequantize(dtype == MOE_LORA_F32, num_rows, cols, codes, scales,
+                                           out, static_cast<hipStream_t>(stream)));
+}
+
+int moe_lora_rms_norm_quantize(int64_t num_tokens, int32_t hidden, int32_t dtype,
+                               int32_t weight_dtype, int32_t y_dtype, double eps, const void* x,
+                               const void* residual, const void* weight, int8_t* codes,
+                               float* scales, void* residual_out, void* y, void* stream) {
+  const int st = int8_shape(num_tokens, hidden, dtype, kMaxNormCols);
+  if (st != MOE_LORA_OK) return st;
+  if (!float_dtype(weight_dtype) || (y && !float_dtype(y_dtype))) return MOE_LORA_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0) || eps > 3.4e38) return MOE_LORA_ERR_INVALID;
+  if (num_tokens == 0) return MOE_LORA_OK;
+  if (!x || !weight || !codes || !scales || off_by_element(x, dtype) || off_by_element(residual, dtype) ||
+      off_by_element(weight, weight_dtype) || off_by_word(scales) || off_by_element(residual_out, dtype) ||
+      (y && off_by_element(y, y_dtype)))
+    return MOE_LORA_ERR_INVALID;
+  Int8Rows p = {};
+  p.num_rows = num_tokens; p.cols = hidden;
+  p.x_f32 = dtype == MOE_LORA_F32;
+  p.weight_f32 = weight_dtype == MOE_LORA_F32;
+  p.y_f32 = y_dtype == MOE_LORA_F32;
+  p.x = x; p.weight = weight; p.residual = residual; p.eps = eps;
+  p.residual_out = residual_out; p.y = y; p.codes = codes; p.scales = scales;
+  return hip_status(launch_int8_rows(p, static_cast<hipStream_t>(stream)));
+}
+
+constexpr int64_t kMaxInt8K = (int64_t(1) << 17) - 16;   // sums of products stay within int32
+
+int moe_lora_int8_gemm(const moe_lora_int8_gemm_args* a, void* stream) {
+  if (!a || a->struct_size < sizeof(moe_lora_int8_gemm_args)) return MOE_LORA_ERR_INVALID;
+  if (!float_dtype(a->out_dtype)) return MOE_LORA_ERR_UNSUPPORTED;
+  if (a->num_rows < 0 || a->out_features <= 0 || a->in_features <= 0 || a->num_experts <= 0 ||
+      a->top_k < 0 || a->num_tokens < 0)
+    return MOE_LORA_ERR_INVALID;
+  if (a->in_features % 16 || a->out_features % (a->silu_mul ? 32 : 16) ||
+      a->in_features > kMaxInt8K || a->out_features > kMaxCols || a->num_rows > kMaxRows)
+    return MOE_LORA_ERR_UNSUPPORTED;
+  if (a->tile_expert) {
+    if (bad_block_m(a->block_m) || a->num_rows % a->block_m) return MOE_LORA_ERR_INVALID;
+  } else if (a->num_experts != 1) {
+    return MOE_LORA_ERR_INVALID;   // rows of several experts need their tiles
+  }
+  if (a->sorted_pair_ids && (!a->tile_expert || a->num_pairs < 0)) return MOE_LORA_ERR_INVALID;
+  // threads of one launch are counted in 32 bits: 256 to 16 rows x 64 columns at the least
+  if ((a->num_rows + 15) / 16 * ((a->out_features + 63) / 64) >= (int64_t(1) << 24))
+    return MOE_LORA_ERR_UNSUPPORTED;
+  if (a->num_rows == 0) return MOE_LORA_OK;
+  if (a->top_k > 0) {
+    // some token is there for the padding rows to name, and offsets within x are 32 bits
+    if (!a->sorted_pair_ids || a->num_tokens <= 0 || a->num_pairs / a->top_k > a->num_tokens ||
+        (a->num_pairs / a->top_k == a->num_tokens && a->num_pairs % a->top_k))
+      return MOE_LORA_ERR_INVALID;
+    if (a->num_tokens > kMaxRows || a->num_tokens * a->in_features >= kMaxOffsetBytes)
+      return MOE_LORA_ERR_UNSUPPORTED;
+  }
+  if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->out || misaligned(a->x) ||
+      misaligned(a->w) || misaligned(a->out) || off_by_word(a->x_scale) || off_by_word(a->w_scale))
+    return MOE_LORA_ERR_INVALID;
+  Int8Gemm p;
+  p.M = a->num_rows; p.N = a->out_features; p.K = a->in_features; p.E = a->num_experts;
+  p.BM = a->tile_expert ? a->block_m : 0;
+  p.out_f32 = a->out_dtype == MOE_LORA_F32;
+  p.silu_mul = a->silu_mul != 0;
+  p.x = a->x; p.x_scale = a->x_scale; p.w = a->w; p.w_scale = a->w_scale;
+  p.tile_expert = a->tile_expert; p.out = a->out;
+  p.row_ids = a->sorted_pair_ids; p.num_ids = a->num_pairs;
+  p.top_k = a->top_k;
+  return hip_status(launch_int8_gemm(p, static_cast<hipStream_t>(stream)));
+}
+
+// ---- balance loss ----------------------------------------------------------
+
+static int balance_shape(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t dtype) {
+  if (num_tokens < 0 || num_experts <= 0 || top_k <= 0) return MOE_LORA_ERR_INVALID;
+  if (!float_dtype(dtype) || num_experts > kMaxBalanceExperts || (int64_t)num_tokens * top_k > INT32_MAX / 2)
+    return MOE_LORA_ERR_UNSUPPORTED;
+  return MOE_LORA_OK;
+}
+
+size_t moe_lora_balance_loss_workspace_bytes(int32_t num_tokens, int32_t num_experts) {
+  if (balance_shape(num_tokens, num_experts, 1, MOE_LORA_F32) != MOE_LORA_OK) return 0;
+  return balance_ws_bytes(num_tokens, num_experts);
+}
+
+int moe_lora_balance_loss(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t dtype,
+                          const void* logits, const int32_t* topk_ids, const uint8_t* token_mask,
+                          float* loss, int32_t* counts, float* mean_probs, int32_t* num_valid,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = balance_shape(num_tokens, num_experts, top_k, dtype);
+  if (st != MOE_LORA_OK) return st;
+  if (!loss || !counts || !mean_probs || !num_valid || (num_tokens > 0 && (!logits || !topk_ids)) ||
+      off_by_element(logits, dtype))
+    return MOE_LORA_ERR_INVALID;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 8 ||
+      workspace_bytes < balance_ws_bytes(num_tokens, num_experts))
+    return MOE_LORA_ERR_WORKSPACE;
+  const Balance b = {num_tokens, num_experts, top_k, dtype == MOE_LORA_F32, logits, topk_ids, token_mask};
+  return hip_status(launch_balance_loss(b, loss, counts, mean_probs, num_valid, workspace,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int moe_lora_balance_loss_backward(int32_t num_tokens, int32_t num_experts, int32_t top_k,
+                                   int32_t dtype, int32_t out_dtype, const void* logits,
+                                   const uint8_t* token_mask, const int32_t* counts,
+                                   const int32_t* num_valid, const float* d_loss, void* d_logits,
+                                   void* stream) {
+  const int st = balance_shape(num_tokens, num_experts, top_k, dtype);
+  if (st != MOE_LORA_OK) return st;
+  if (!float_dtype(out_dtype)) return MOE_LORA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return MOE_LORA_OK;
+  if (!logits || !counts || !num_valid || !d_logits || off_by_element(logits, dtype) ||
+      off_by_element(d_logits, out_dtype))
+    return MOE_LORA_ERR_INVALID;
+  const Balance b = {num_tokens, num_experts, top_k, dtype == MOE_LORA_F32, logits, nullptr, token_mask};
+  return hip_status(launch_balance_loss_backward(b, out_dtype == MOE_LORA_F32, counts, num_valid,
+                                                 d_loss, d_logits, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -100,6 +100,56 @@ inline int64_t mx4_stream_blocks(int64_t num_rows, int64_t out_features, int32_t
   return mx4_stream_groups((num_rows + rows - 1) / rows) * ((out_features + 63) / 64);
 }
 
+// ---- 8-bit integers --------------------------------------------------------
+struct Int8Rows {
+  int64_t num_rows, cols;
+  bool x_f32, weight_f32, y_f32;
+  const void* x;                     // [num_rows, cols]
+  const int32_t* rows_used;          // null, or rows from *rows_used on are skipped
+  // the norm (weight null: x is quantized as it is)
+  const void* weight;                // [cols]
+  const void* residual;              // [num_rows, cols] or null
+  double eps;
+  void* residual_out;                // null, or x + residual
+  void* y;                           // null, or the norm
+  int8_t* codes;                     // [num_rows, cols]
+  float* scales;                     // [num_rows]
+};
+constexpr int64_t kMaxNormCols = 16384;   // a row in the registers of a workgroup
+hipError_t launch_int8_rows(const Int8Rows& p, hipStream_t stream);
+hipError_t launch_int8_dequantize(bool out_f32, int64_t num_rows, int64_t cols, const int8_t* codes,
+                                  const float* scales, void* out, hipStream_t stream);
+struct Int8Gemm {
+  int64_t M, N, K, E, BM;            // BM: rows of a tile_expert entry
+  bool out_f32, silu_mul;
+  const int8_t* x;                   // [M, K], or [T, K] with top_k
+  const float* x_scale;              // [M] or [T]
+  const int8_t* w;                   // [E, N, K]
+  const float* w_scale;              // [E, N]
+  const int32_t* tile_expert;        // [M / BM], null: one weight for all rows
+  const int32_t* row_ids;            // [M], null, or rows outside [0, num_ids) are pads
+  int32_t num_ids;
+  int32_t top_k;                     // > 0: row m reads row row_ids[m] / top_k of x
+  void* out;                         // [M, N], or [M, N / 2] with silu_mul
+};
+hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t stream);
+
+// ---- balance loss ----------------------------------------------------------
+struct Balance {
+  int32_t T, E, k;
+  bool logits_f32;
+  const void* logits;                // [T, E]
+  const int32_t* topk_ids;           // [T, k]
+  const uint8_t* mask;               // [T] or null: nonzero takes part
+};
+constexpr int64_t kMaxBalanceExperts = 1024;   // 16 registers of a wave
+size_t balance_ws_bytes(int64_t T, int64_t E);
+hipError_t launch_balance_loss(const Balance& b, float* loss, int32_t* counts, float* mean_probs,
+                               int32_t* num_valid, void* workspace, hipStream_t stream);
+hipError_t launch_balance_loss_backward(const Balance& b, bool out_f32, const int32_t* counts,
+                                        const int32_t* num_valid, const float* d_loss, void* d_logits,
+                                        hipStream_t stream);
+
 // ---- forward ---------------------------------------------------------------
 // expert weights as fp8 e4m3 codes with 128 x 128 block scales (dtype bf16)
 constexpr int kWeightFp8 = 2;
