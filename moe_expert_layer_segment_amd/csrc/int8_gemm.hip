@@ -181,11 +181,361 @@ static hipError_t stream(const Int8Gemm& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// ---- many rows -------------------------------------------------------------
+// Tiles of TM rows x 256 weight rows, K in steps of 128 values: rows of 128 bytes in LDS, of x
+// and of the weights alike, in two buffers.  Four waves, one to a SIMD, so that a wave has 512
+// registers: 256 of them hold the sums of 128 x 128 outputs, and a step of 64 K values takes 16
+// fragments (256 bytes a lane) for 64 MFMAs, half the LDS reads of eight waves with 128 x 64.
+//
+// A step multiplies one set of fragments while the other is read for the step that follows, the
+// reads and the DMAs spread over the MFMAs.  After the first step of a K tile all of the tile is
+// in registers: a barrier, ahead of which every wave has waited for its DMAs of the next tile,
+// frees its buffer and admits the next one.
+//
+// LDS rows are eight 16-byte chunks.  Lane group g takes chunk 2g + h of its row in step h, from
+// place (2g + h) ^ (bits 3, 1, 2 of the row's number): no two of 16 lanes read one bank, and a
+// DMA's lanes, which fill places in order, still read whole 64-byte pieces.
+constexpr int kTileN = 256;
+constexpr int kStep = 128;   // bytes of K in an LDS row
+
+// this wave's DMA and LDS reads are done, then every wave's
+__device__ __forceinline__ void wait_all_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// 8 neighbouring columns
+__device__ __forceinline__ void store_out(const Int8Gemm& p, int64_t at, floatx4 v, floatx4 w) {
+  if (p.out_f32) {
+    store_out(p, at, v);
+    store_out(p, at + 4, w);
+  } else {
+    bf16x8 o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = (bf16_t)(i < 4 ? v[i] : w[i - 4]);
+    *reinterpret_cast<bf16x8*>(static_cast<bf16_t*>(p.out) + at) = o;
+  }
+}
+
+constexpr int tile_lds(int tm) { return 2 * (tm + kTileN) * kStep; }
+
+// c0..c3 += a0..a3 * b, in place
+__device__ __forceinline__ void mfma_four(int4v& c0, int4v& c1, int4v& c2, int4v& c3, int4v a0, int4v a1,
+                                          int4v a2, int4v a3, int4v b) {
+  asm volatile(
+      "s_nop 1\n\t"
+      "v_mfma_i32_16x16x64_i8 %0, %4, %8, %0\n\t"
+      "v_mfma_i32_16x16x64_i8 %1, %5, %8, %1\n\t"
+      "v_mfma_i32_16x16x64_i8 %2, %6, %8, %2\n\t"
+      "v_mfma_i32_16x16x64_i8 %3, %7, %8, %3"
+      : "+a"(c0), "+a"(c1), "+a"(c2), "+a"(c3)
+      : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "v"(b));
+}
+
+// rows [m0, m0 + TM) of expert e, weight rows from 16 cb0 on; rows before m0 + skip are left to
+// another workgroup, rows from m0 + rows on do not exist
+template <int TM>
+__device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t m0, int64_t cb0,
+                                          int64_t e, int rows, int skip) {
+  constexpr int WN = TM == 64 ? 4 : 2, WM = 4 / WN;             // waves over columns and rows
+  constexpr int MB = TM / WM / 16, NB = kTileN / WN / 16;       // 16-row blocks of a wave
+  constexpr int XSEG = TM / 8 / 4, WSEG = kTileN / 8 / 4;       // a wave's DMAs of 8 rows for a K tile
+  constexpr int XPART = TM * kStep, STAGE = XPART + kTileN * kStep;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+  const int wm = wave / WN, wn = wave % WN;
+  const int tiles = (int)((p.K + kStep - 1) / kStep);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  auto swz = [](int row) { return (row >> 1 & 4) | (row & 2) | (row >> 2 & 1); };
+  // LDS row n of the weights holds row spot(n) of the tile: rows 4q..4q + 3 of two blocks of 16
+  // lie side by side, and so do the outputs that a lane has of the two
+  auto spot = [](int n) { return n / 32 * 32 + n % 16 / 4 * 8 + n / 16 % 2 * 4 + n % 4; };
+  // weight row of LDS row n; with silu_mul blocks of gate and of up rows alternate, and side by
+  // side lie those of two gate or two up blocks.  What would lie behind the last column repeats
+  // the last.
+  const int out_cols = (int)(p.silu_mul ? p.N / 2 : p.N), col0 = (int)cb0 * (p.silu_mul ? 8 : 16);
+  auto w_col = [&](int n) {
+    const int col = p.silu_mul ? spot(n / 64 * 32 + n / 32 % 2 * 16 + n % 16) : spot(n);
+    return min(col, out_cols - 1 - col0);
+  };
+  auto is_up = [&](int n) { return p.silu_mul && n / 16 % 2; };
+
+  // This lane's row in each of its DMAs: 8 rows of 128 bytes, lane l the chunk at place l % 8 of
+  // row l / 8.  Offsets are 32 bits, of x from its start (where the rows of a pair's tokens lie
+  // anywhere) or from the tile's first row, of the weights from the tile's first gate or up row.
+  constexpr int DMAS = XSEG + WSEG;
+  static_assert(XSEG % 2 == 0 && WSEG % 2 == 0, "even segments of 8 rows have one swizzle, odd ones the other");
+  uint32_t off[DMAS];
+  const int8_t* const x_base = p.x + (p.top_k > 0 ? 0 : m0 * p.K);
+  const int8_t* const w_base = p.w + (e * p.N + col0) * p.K;
+  const int8_t* const up_base = w_base + out_cols * p.K;
+  auto lds_row = [&](int i) { return i < XSEG ? (wave * XSEG + i) * 8 : (wave * WSEG + i - XSEG) * 8; };
+#pragma unroll
+  for (int i = 0; i < DMAS; ++i) {
+    const int row = lds_row(i) + lane / 8;
+    int64_t src = i < XSEG ? min(row, rows - 1) : w_col(row);
+    if (i < XSEG && p.top_k > 0) {
+      const int32_t id = p.row_ids[m0 + src];
+      src = id >= 0 && id < p.num_ids ? (uint32_t)id / (uint32_t)p.top_k : 0;
+    }
+    off[i] = (uint32_t)(src * p.K);
+  }
+  // byte of the row that this lane fetches of K tile t, in even and in odd segments; behind the
+  // row's end the first one instead, whose products are left out
+  auto byte_of = [&](int t, int odd) {
+    const uint32_t at = (uint32_t)t * kStep + ((lane % 8) ^ swz(odd * 8 + lane / 8)) * 16;
+    return at < (uint32_t)p.K ? at : 0;
+  };
+  struct Bytes { uint32_t even, odd; };
+  auto issue = [&](Bytes at, int place, int i) {
+    const int row = lds_row(i);
+    const uint32_t to = lds0 + place * STAGE + (i < XSEG ? 0 : XPART) + row * kStep;
+    // a segment of 8 rows is gate or up as a whole
+    dma16(i < XSEG ? x_base : is_up(row) ? up_base : w_base, off[i] + (i % 2 ? at.odd : at.even), to);
+  };
+
+  int4v acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = int4v{0, 0, 0, 0};
+  // places of this lane's row of a wave's first block; a block is 16 rows further
+  const int x_at = (wm * MB * 16 + r) * kStep, w_at = XPART + (wn * NB * 16 + r) * kStep;
+  const int c_at[2] = {((2 * g) ^ swz(r)) * 16, ((2 * g + 1) ^ swz(r)) * 16};
+  int4v xf[2][MB], wf[2][NB];
+  auto read_x = [&](int place, auto H, auto I) {
+    constexpr int h = decltype(H)::value, i = decltype(I)::value;
+    xf[h][i] = *reinterpret_cast<const int4v*>(lds + (place * STAGE + x_at + c_at[h]) + i * 16 * kStep);
+  };
+  auto read_w = [&](int place, auto H, auto J) {
+    constexpr int h = decltype(H)::value, j = decltype(J)::value;
+    wf[h][j] = *reinterpret_cast<const int4v*>(lds + (place * STAGE + w_at + c_at[h]) + j * 16 * kStep);
+  };
+  constexpr std::integral_constant<int, 0> first{};
+  constexpr std::integral_constant<int, 1> second{};
+  // the MFMAs of step H; beside each block of x rows one of the other step's fragments of x and
+  // its share of those of the weights are read from `place` (read), and DMAs go out (send)
+  constexpr int WPER = (NB + MB - 1) / MB, DPER = (DMAS + MB - 1) / MB;
+  auto step = [&](auto H, int place, auto read, auto&& send) {
+    constexpr int h = decltype(H)::value;
+    std::integral_constant<int, 1 - h> other;
+    static_for<MB>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      if constexpr (decltype(read)::value) {
+        read_x(place, other, I);
+        static_for<NB>([&](auto J) {
+          if constexpr (decltype(J)::value / WPER == i) read_w(place, other, J);
+        });
+      }
+      send(I);
+      static_for<NB / 4>([&](auto J) {
+        constexpr int j = 4 * decltype(J)::value;
+        mfma_four(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3], wf[h][j], wf[h][j + 1], wf[h][j + 2],
+                  wf[h][j + 3], xf[h][i]);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  auto nothing = [](auto) {};
+  auto bytes_of = [&](int t) { return Bytes{byte_of(t, 0), byte_of(t, 1)}; };
+
+  static_for<DMAS>([&](auto D) { issue(bytes_of(0), 0, decltype(D)::value); });
+  wait_all_barrier();
+  if (tiles > 1) static_for<DMAS>([&](auto D) { issue(bytes_of(1), 1, decltype(D)::value); });
+  static_for<MB>([&](auto I) { read_x(0, first, I); });
+  static_for<NB>([&](auto J) { read_w(0, first, J); });
+  int place = 0;
+  for (int t = 0; t + 1 < tiles; ++t, place ^= 1) {
+    step(first, place, std::true_type{}, nothing);
+    wait_all_barrier();
+    const Bytes at = bytes_of(t + 2);
+    const bool sends = t + 2 < tiles;
+    step(second, place ^ 1, std::true_type{}, [&](auto I) {
+      if (!sends) return;
+      static_for<DPER>([&](auto D) {
+        constexpr int d = decltype(I)::value * DPER + decltype(D)::value;
+        if constexpr (d < DMAS) issue(at, place, d);
+      });
+    });
+  }
+  // the last tile, whose chunks may lie behind the end of the rows
+  auto cut = [&](auto H) {
+    constexpr int h = decltype(H)::value;
+    const bool in = ((int64_t)(tiles - 1) * 8 + 2 * g + h) * 16 < p.K;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) wf[h][j] = in ? wf[h][j] : int4v{0, 0, 0, 0};
+  };
+  cut(first);
+  step(first, place, std::true_type{}, nothing);
+  cut(second);
+  step(second, 0, std::false_type{}, nothing);
+  // the last products are done before what follows reads them
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) asm volatile("" : "+a"(acc[i][j]));
+
+  // the scales of this lane's rows and columns
+  float xs[MB];
+  floatx4 ws[NB];
+  uint32_t live = 0;
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    const int row = min((wm * MB + i) * 16 + r, rows - 1);
+    int64_t src = m0 + row;
+    bool holds = true;
+    if (p.row_ids) {
+      const int32_t id = p.row_ids[m0 + row];
+      holds = id >= 0 && id < p.num_ids;
+      if (p.top_k > 0) src = holds ? (uint32_t)id / (uint32_t)p.top_k : 0;
+    }
+    live |= (uint32_t)holds << i;
+    xs[i] = p.x_scale[src];
+  }
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int n = (wn * NB + j) * 16 + 4 * g;   // 4 columns from there on; N is a multiple of 16
+    const float* at = p.w_scale + e * p.N + col0 + min(w_col(n), out_cols - 4 - col0) + (is_up(n) ? out_cols : 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) ws[j][q] = at[q];
+  }
+
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    const int row = (wm * MB + i) * 16 + r;
+    if (row >= rows || row < skip) continue;
+    const bool holds = live >> i & 1;
+    const int64_t at = (m0 + row) * out_cols + col0;
+    auto y = [&](int j) {
+      floatx4 v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = holds ? (float)acc[i][j][q] * xs[i] * ws[j][q] : 0.0f;
+      return v;
+    };
+    if (p.silu_mul) {
+#pragma unroll
+      for (int j = 0; j < NB; j += 4) {
+        const int col = (wn * NB + j) * 8 + 8 * g;
+        if (col0 + col >= out_cols) continue;
+        floatx4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const floatx4 gate = y(j + 2 * h), up = y(j + 2 * h + 1);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[h][q] = silu_near(gate[q]) * up[q];
+        }
+        store_out(p, at + col, v[0], v[1]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NB; j += 2) {
+        const int col = (wn * NB + j) * 16 + 8 * g;
+        if (col0 + col >= out_cols) continue;
+        store_out(p, at + col, y(j), y(j + 1));
+      }
+    }
+  }
+}
+
+// Workgroups of the last, incomplete round of 256 (one to a CU) take a half or a quarter of a
+// tile's rows each, where that fills the round no more than once; a workgroup whose rows end
+// early with padding takes a smaller tile.
+//
+// Patches of (32 / pn) x pn tiles go round the eight XCDs (workgroup b runs on XCD b % 8), so
+// the 32 workgroups that an XCD holds share rows and weights in its L2.
+constexpr int kRound = 256;
+constexpr int64_t kTailTiles = 16 * kRound;   // with more, a share of a round does not count
+
+// per_entry: tiles of an entry of tile_expert (three of 64 rows for block_m = 192)
+template <int TOP>
+__global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_tiles, int n_tiles, int pn,
+                                                           int n_patches, int per_entry, int tail) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds(TOP)];
+  const int lane = threadIdx.x & 63;
+  const int pm = 32 / pn;
+  int patch = (int)(blockIdx.x / 256) * 8 + (int)(blockIdx.x % 8);
+  const int in = (int)(blockIdx.x / 8) % 32;
+  int used = m_tiles, whole = m_tiles, pieces = 1;   // tiles with rows; those taken whole
+  if (tail) {
+    if (p.tile_expert) {
+      used = 0;   // from the end, where the entries without an expert are
+      for (int t0 = (m_tiles - 1) / 64 * 64; t0 >= 0 && used == 0; t0 -= 64) {
+        const int t = t0 + lane;
+        const int te = t < m_tiles ? p.tile_expert[(uint32_t)t / (uint32_t)per_entry] : -1;
+        const uint64_t has = __ballot(te >= 0 && te < p.E);
+        if (has) used = t0 + 64 - __clzll(has);
+      }
+      used = __builtin_amdgcn_readfirstlane(used);
+    }
+    whole = used * n_tiles / kRound * kRound / n_tiles / pm * pm;
+    const int rest = (used - whole) * n_tiles;
+    if (TOP == 256 && 4 * rest <= kRound) pieces = 4;
+    else if (TOP >= 128 && 2 * rest <= kRound) pieces = 2;
+    else whole = used;
+  }
+  const int whole_patches = (whole + pm - 1) / pm * n_patches;
+  const bool part = patch >= whole_patches;
+  if (part) patch -= whole_patches;
+  const int mt = patch / n_patches * pm + in % pm, nt = patch % n_patches * pn + in / pm;
+  if (nt >= n_tiles || mt >= (part ? (used - whole) * pieces : whole)) return;
+  const int span = part ? TOP / pieces : TOP;
+  const int64_t m0 = part ? (int64_t)whole * TOP + (int64_t)mt * span : (int64_t)mt * TOP;
+  const int64_t cb0 = (int64_t)nt * (kTileN / 16);
+  int64_t e = 0;
+  if (p.tile_expert) {
+    e = __builtin_amdgcn_readfirstlane(p.tile_expert[(uint32_t)(part ? whole + mt / pieces : mt) / (uint32_t)per_entry]);
+    if (e < 0 || e >= p.E) return;
+  }
+  const int rows = (int)min((int64_t)span, p.M - m0);
+  if (rows <= 0) return;
+  int live = rows;   // up to the last row that holds a pair
+  if (p.row_ids) {
+    live = 0;
+    for (int r0 = (rows - 1) / 64 * 64; r0 >= 0 && live == 0; r0 -= 64) {
+      const int32_t id = p.row_ids[m0 + min(r0 + lane, rows - 1)];
+      const uint64_t has = __ballot(r0 + lane < rows && id >= 0 && id < p.num_ids);
+      if (has) live = r0 + 64 - __clzll(has);
+    }
+    live = __builtin_amdgcn_readfirstlane(live);
+  }
+  // the rows behind the tile that these take hold no pair
+  const int done = live > 128 ? 256 : live > 64 ? 128 : live > 0 ? 64 : 0;
+  const int cols = (int)(p.silu_mul ? p.N / 2 : p.N), col0 = (int)cb0 * (p.silu_mul ? 8 : 16);
+  const int width = min(p.silu_mul ? kTileN / 2 : kTileN, cols - col0);
+  for (int row = done + threadIdx.x / 64; row < rows; row += 4)
+    if (lane * 4 < width) store_out(p, (m0 + row) * cols + col0 + lane * 4, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
+  const int some = min(rows, done);
+  if (TOP == 256 && done == 256) int8_tile<TOP>(p, lds, m0, cb0, e, some, 0);
+  else if (TOP >= 128 && done == 128) int8_tile<TOP >= 128 ? 128 : 64>(p, lds, m0, cb0, e, some, 0);
+  else if (done == 64) int8_tile<64>(p, lds, m0, cb0, e, some, 0);
+}
+
+template <int TM>
+static hipError_t tiled(const Int8Gemm& p, hipStream_t stream) {
+  const int64_t m_tiles = ceil_div(p.M, TM), n_tiles = ceil_div(p.N, kTileN);
+  int pn = 8;
+  while (pn > n_tiles) pn /= 2;
+  const int64_t n_patches = ceil_div(n_tiles, pn);
+  const bool tail = m_tiles * n_tiles <= kTailTiles;
+  // parts of tiles fill a round at most: 16 patches, and one more for each part of the
+  // columns in which their rows end
+  const int64_t patches = ceil_div(m_tiles, 32 / pn) * n_patches + (tail ? 16 + 2 * n_patches : 0);
+  hipLaunchKernelGGL(int8_tile_kernel<TM>, dim3((unsigned)(ceil_div(patches, 8) * 256)), dim3(256), 0, stream, p,
+                     (int)m_tiles, (int)n_tiles, pn, (int)n_patches,
+                     (int)(p.tile_expert ? p.BM / TM : 1), (int)tail);
+  return hipGetLastError();
+}
+
 hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t s) {
   // rows of a workgroup: within one tile_expert entry, or those there are
   const int64_t rows = p.tile_expert ? p.BM : p.M;
   auto takes = [&](int64_t n) { return p.tile_expert ? rows % n == 0 : rows > n / 2; };
-  if (takes(64)) return stream<4, 2, 4>(p, s);
+  if (takes(64)) {
+    if (ceil_div(p.M, 64) * ceil_div(p.N, kTileN) <= 64) return stream<4, 2, 4>(p, s);
+    if (takes(256)) return tiled<256>(p, s);
+    if (takes(128)) return tiled<128>(p, s);
+    return tiled<64>(p, s);
+  }
   if (takes(32)) return stream<2, 4, 4>(p, s);
   return stream<1, 4, 4>(p, s);
 }
