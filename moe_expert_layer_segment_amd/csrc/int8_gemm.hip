@@ -218,17 +218,33 @@ __device__ __forceinline__ void store_out(const Int8Gemm& p, int64_t at, floatx4
 
 constexpr int tile_lds(int tm) { return 2 * (tm + kTileN) * kStep; }
 
-// c0..c3 += a0..a3 * b, in place
-__device__ __forceinline__ void mfma_four(int4v& c0, int4v& c1, int4v& c2, int4v& c3, int4v a0, int4v a1,
-                                          int4v a2, int4v a3, int4v b) {
+// c += a * b, in place.  (As a builtin the compiler moves a quarter of the sums from registers to
+// registers in every round of the K loop.)  It does not see that a matrix instruction's operands
+// want two wait states behind another vector instruction that wrote them, and its sums more of
+// them before they are read: the K loop's operands are written by LDS reads alone, and `settle`
+// stands wherever else they, or the sums, change hands.
+__device__ __forceinline__ void mfma_in_place(int4v& c, int4v a, int4v b) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
+// a uniform address, in scalar registers
+__device__ __forceinline__ uint64_t uniform_address(const void* p) {
+  const uint64_t g = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)g);   // (an int, which would extend its sign)
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(g >> 32));
+  return (uint64_t)hi << 32 | lo;
+}
+// as dma16 from a uniform_address, without keeping M0, which nothing else here uses.  (s_nop: the
+// base may come from a vector instruction, which wants five wait states ahead of the load.)
+__device__ __forceinline__ void dma16_m0(uint64_t base, uint32_t goff, uint32_t lds_addr) {
   asm volatile(
-      "s_nop 1\n\t"
-      "v_mfma_i32_16x16x64_i8 %0, %4, %8, %0\n\t"
-      "v_mfma_i32_16x16x64_i8 %1, %5, %8, %1\n\t"
-      "v_mfma_i32_16x16x64_i8 %2, %6, %8, %2\n\t"
-      "v_mfma_i32_16x16x64_i8 %3, %7, %8, %3"
-      : "+a"(c0), "+a"(c1), "+a"(c2), "+a"(c3)
-      : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "v"(b));
+      "s_mov_b32 m0, %[la]\n\t"
+      "s_nop 3\n\t"
+      "global_load_lds_dwordx4 %[go], %[gb]"
+      :
+      : [la] "s"(lds_addr), [go] "v"(goff), [gb] "s"(base)
+      : "memory", "m0");
 }
 
 // rows [m0, m0 + TM) of expert e, weight rows from 16 cb0 on; rows before m0 + skip are left to
@@ -244,7 +260,7 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
   const int r = lane & 15, g = lane >> 4;
   const int wm = wave / WN, wn = wave % WN;
   const int tiles = (int)((p.K + kStep - 1) / kStep);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
   auto swz = [](int row) { return (row >> 1 & 4) | (row & 2) | (row >> 2 & 1); };
   // LDS row n of the weights holds row spot(n) of the tile: rows 4q..4q + 3 of two blocks of 16
   // lie side by side, and so do the outputs that a lane has of the two
@@ -265,9 +281,9 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
   constexpr int DMAS = XSEG + WSEG;
   static_assert(XSEG % 2 == 0 && WSEG % 2 == 0, "even segments of 8 rows have one swizzle, odd ones the other");
   uint32_t off[DMAS];
-  const int8_t* const x_base = p.x + (p.top_k > 0 ? 0 : m0 * p.K);
-  const int8_t* const w_base = p.w + (e * p.N + col0) * p.K;
-  const int8_t* const up_base = w_base + out_cols * p.K;
+  const uint64_t x_base = uniform_address(p.x + (p.top_k > 0 ? 0 : m0 * p.K));
+  const uint64_t w_base = uniform_address(p.w + (e * p.N + col0) * p.K);
+  const uint64_t up_base = w_base + (p.silu_mul ? out_cols * p.K : 0);
   auto lds_row = [&](int i) { return i < XSEG ? (wave * XSEG + i) * 8 : (wave * WSEG + i - XSEG) * 8; };
 #pragma unroll
   for (int i = 0; i < DMAS; ++i) {
@@ -279,18 +295,26 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
     }
     off[i] = (uint32_t)(src * p.K);
   }
-  // byte of the row that this lane fetches of K tile t, in even and in odd segments; behind the
-  // row's end the first one instead, whose products are left out
-  auto byte_of = [&](int t, int odd) {
-    const uint32_t at = (uint32_t)t * kStep + ((lane % 8) ^ swz(odd * 8 + lane / 8)) * 16;
-    return at < (uint32_t)p.K ? at : 0;
+  // its chunk of a K tile, in even and in odd segments
+  const uint32_t chunk[2] = {(uint32_t)((lane % 8) ^ swz(lane / 8)) * 16, (uint32_t)((lane % 8) ^ swz(8 + lane / 8)) * 16};
+#pragma unroll
+  for (int i = 0; i < DMAS; ++i) off[i] += chunk[i % 2];
+  // chunks of the last K tile that lie behind the rows' end: the rows' first ones instead, whose
+  // products are left out
+  auto last_tile = [&]() {
+    const uint32_t at = (uint32_t)(tiles - 1) * kStep;
+#pragma unroll
+    for (int i = 0; i < DMAS; ++i) off[i] -= at + chunk[i % 2] < (uint32_t)p.K ? 0 : chunk[i % 2];
   };
-  struct Bytes { uint32_t even, odd; };
-  auto issue = [&](Bytes at, int place, int i) {
+  struct Bases { uint64_t x, w, up; };
+  auto bases_of = [&](int t) {
+    return Bases{x_base + (uint64_t)t * kStep, w_base + (uint64_t)t * kStep, up_base + (uint64_t)t * kStep};
+  };
+  auto issue = [&](const Bases& at, int place, int i) {
     const int row = lds_row(i);
     const uint32_t to = lds0 + place * STAGE + (i < XSEG ? 0 : XPART) + row * kStep;
     // a segment of 8 rows is gate or up as a whole
-    dma16(i < XSEG ? x_base : is_up(row) ? up_base : w_base, off[i] + (i % 2 ? at.odd : at.even), to);
+    dma16_m0(i < XSEG ? at.x : is_up(row) ? at.up : at.w, off[i], to);
   };
 
   int4v acc[MB][NB];
@@ -312,64 +336,72 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
   };
   constexpr std::integral_constant<int, 0> first{};
   constexpr std::integral_constant<int, 1> second{};
-  // the MFMAs of step H; beside each block of x rows one of the other step's fragments of x and
-  // its share of those of the weights are read from `place` (read), and DMAs go out (send)
-  constexpr int WPER = (NB + MB - 1) / MB, DPER = (DMAS + MB - 1) / MB;
+  // The MFMAs of step H.  Between them, at an even pace, the fragments of the other step are read
+  // from `place` (read), and DMAs go out (send).
+  constexpr int SLOTS = MB * NB, READS = MB + NB;
+  static_assert(READS <= SLOTS && DMAS <= SLOTS, "a slot behind each MFMA");
   auto step = [&](auto H, int place, auto read, auto&& send) {
     constexpr int h = decltype(H)::value;
     std::integral_constant<int, 1 - h> other;
-    static_for<MB>([&](auto I) {
-      constexpr int i = decltype(I)::value;
-      if constexpr (decltype(read)::value) {
-        read_x(place, other, I);
-        static_for<NB>([&](auto J) {
-          if constexpr (decltype(J)::value / WPER == i) read_w(place, other, J);
-        });
+    static_for<SLOTS>([&](auto S) {
+      constexpr int s = decltype(S)::value, i = s / NB, j = s % NB;
+      mfma_in_place(acc[i][j], wf[h][j], xf[h][i]);
+      // the n-th of READS lies behind MFMA n SLOTS / READS; those of the weights come first
+      constexpr int n = (s * READS + SLOTS - 1) / SLOTS;
+      if constexpr (decltype(read)::value && n < READS && n * SLOTS / READS == s) {
+        if constexpr (n < NB) read_w(place, other, std::integral_constant<int, n < NB ? n : 0>{});
+        else read_x(place, other, std::integral_constant<int, n < NB ? 0 : n - NB>{});
       }
-      send(I);
-      static_for<NB / 4>([&](auto J) {
-        constexpr int j = 4 * decltype(J)::value;
-        mfma_four(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3], wf[h][j], wf[h][j + 1], wf[h][j + 2],
-                  wf[h][j + 3], xf[h][i]);
-      });
+      send(S);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
   auto nothing = [](auto) {};
-  auto bytes_of = [&](int t) { return Bytes{byte_of(t, 0), byte_of(t, 1)}; };
 
-  static_for<DMAS>([&](auto D) { issue(bytes_of(0), 0, decltype(D)::value); });
+  static_for<DMAS>([&](auto D) {
+    if (decltype(D)::value == 0 && tiles == 1) last_tile();
+    issue(bases_of(0), 0, decltype(D)::value);
+  });
   wait_all_barrier();
-  if (tiles > 1) static_for<DMAS>([&](auto D) { issue(bytes_of(1), 1, decltype(D)::value); });
+  if (tiles > 1) {
+    if (tiles == 2) last_tile();
+    static_for<DMAS>([&](auto D) { issue(bases_of(1), 1, decltype(D)::value); });
+  }
   static_for<MB>([&](auto I) { read_x(0, first, I); });
   static_for<NB>([&](auto J) { read_w(0, first, J); });
-  int place = 0;
-  for (int t = 0; t + 1 < tiles; ++t, place ^= 1) {
-    step(first, place, std::true_type{}, nothing);
-    wait_all_barrier();
-    const Bytes at = bytes_of(t + 2);
-    const bool sends = t + 2 < tiles;
-    step(second, place ^ 1, std::true_type{}, [&](auto I) {
-      if (!sends) return;
-      static_for<DPER>([&](auto D) {
-        constexpr int d = decltype(I)::value * DPER + decltype(D)::value;
-        if constexpr (d < DMAS) issue(at, place, d);
-      });
-    });
-  }
-  // the last tile, whose chunks may lie behind the end of the rows
+  // chunks of the last K tile that lie behind the end of the rows
   auto cut = [&](auto H) {
     constexpr int h = decltype(H)::value;
     const bool in = ((int64_t)(tiles - 1) * 8 + 2 * g + h) * 16 < p.K;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) wf[h][j] = in ? wf[h][j] : int4v{0, 0, 0, 0};
+    for (int j = 0; j < NB; ++j) {
+      wf[h][j] = in ? wf[h][j] : int4v{0, 0, 0, 0};
+      asm volatile("" : "+v"(wf[h][j]));
+    }
+    settle();
   };
-  cut(first);
-  step(first, place, std::true_type{}, nothing);
-  cut(second);
-  step(second, 0, std::false_type{}, nothing);
+  settle();
+  // one loop for every tile, the last ones too: where the sums pass from one piece of code to
+  // another the compiler moves them.  (What the last tile reads ahead is not used.)
+  int place = 0;
+#pragma unroll 1
+  for (int t = 0; t < tiles; ++t, place ^= 1) {
+    if (t + 1 == tiles) cut(first);
+    step(first, place, std::true_type{}, nothing);
+    wait_all_barrier();
+    if (t + 1 == tiles) cut(second);
+    if (t + 3 == tiles) last_tile();
+    const Bases at = bases_of(t + 2);
+    const bool sends = t + 2 < tiles;
+    step(second, place ^ 1, std::true_type{}, [&](auto S) {
+      constexpr int s = decltype(S)::value, d = (s * DMAS + SLOTS - 1) / SLOTS;
+      if constexpr (d < DMAS && d * SLOTS / DMAS == s) {
+        if (sends) issue(at, place, d);
+      }
+    });
+  }
   // the last products are done before what follows reads them
-  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  settle();
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
