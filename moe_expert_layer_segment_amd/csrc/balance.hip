@@ -9,57 +9,70 @@
 // counts are constants to the gradient.  A row of logits that are all -inf has p = 0, and with
 // n = 0 everything is 0.  Logits of tokens outside the mask are never read.
 //
-// One wave per token, experts lane, lane + 64, .. in its registers.  p is fp32, from the
-// difference to the largest logit with its rounding error (two fp32 numbers); a wave adds its
-// tokens up in fp64 registers, a workgroup its waves through LDS, and the workgroups' sums go
-// through memory to one more that adds them in order: no atomics but integer ones on LDS, so
-// results do not change from run to run.  Few tokens are one workgroup, and one launch.
+// One wave per token, V experts to a lane: neighbours where V divides their number, so that a
+// load brings them all, else every 64th.  p is fp32, from the difference to the largest logit
+// with its rounding error (two fp32 numbers); a wave adds its tokens up in fp64 registers, a
+// workgroup its waves through LDS, and the workgroups' sums go through memory to others that add
+// them in order: no floating-point atomics, so results do not change from run to run.  Few tokens
+// are one workgroup, and one launch.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
 #include "kernels.hpp"
+#include "vec.hpp"
+#include "wave.hpp"
 
 namespace moelora {
 
 static constexpr int kBalThreads = 1024, kBalWaves = kBalThreads / 64;
-static constexpr int kBalBlocks = 128;        // whose sums the last workgroup adds
+static constexpr int kBalBlocks = 256;        // whose sums are added by the finish
+static constexpr int kFinishWide = 32;        // experts of one of its workgroups
+static constexpr int kFinishGroups = (int)kMaxBalanceExperts / kFinishWide;
 static constexpr int kBalSingle = 256;        // tokens that one workgroup takes alone
 
 struct BalanceWs {
   double* sums;       // [blocks][E]
   int32_t* counts;    // [blocks][E]
   int32_t* valid;     // [blocks]
+  double* dots;       // [kFinishGroups] parts of sum_e counts_e P_e
+  int32_t* done;      // workgroups that have written theirs
 };
 static BalanceWs balance_ws(void* ws, int64_t E) {
   BalanceWs w;
   w.sums = static_cast<double*>(ws);
   w.counts = reinterpret_cast<int32_t*>(w.sums + kBalBlocks * E);
   w.valid = w.counts + kBalBlocks * E;
+  w.dots = reinterpret_cast<double*>(w.valid + kBalBlocks);
+  w.done = reinterpret_cast<int32_t*>(w.dots + kFinishGroups);
   return w;
 }
 size_t balance_ws_bytes(int64_t T, int64_t E) {
-  return T <= kBalSingle ? 16 : (size_t)kBalBlocks * ((size_t)E * 12 + 4);
+  return T <= kBalSingle ? 16 : (size_t)kBalBlocks * ((size_t)E * 12 + 4) + kFinishGroups * 8 + 8;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
-}
-template <typename F>
-__device__ __forceinline__ F wave_sum(F v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+// expert i of a lane
+template <int V, bool NEXT>
+__device__ __forceinline__ int expert_of(int i) {
+  const int lane = threadIdx.x & 63;
+  return NEXT ? lane * V + i : lane + 64 * i;
 }
 
-// v[i]: logit of expert lane + 64 i, -inf behind the last, to its probability
+// 2^x of z + lo, where z log2(e) is rounded once and the rest makes it good
+__device__ __forceinline__ float exp_of(float z, float lo) {
+  const float kLog2e = 1.4426950408889634f, kRest = 1.925963033500887e-8f, kLn2 = 0.6931471805599453f;
+  const float t = z * kLog2e;
+  const float rest = __builtin_fmaf(lo, kLog2e, __builtin_fmaf(z, kRest, __builtin_fmaf(z, kLog2e, -t)));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, rest * kLn2, e);
+}
+
+// logits of a lane, -inf behind the last, to their probabilities
 template <int V>
 __device__ __forceinline__ void softmax(float (&v)[V]) {
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-  m = wave_max(m);
+  m = wave_max(m, -INFINITY);
   if (m == -INFINITY) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = v[i] == -INFINITY ? 0.0f : v[i];   // NaN stays
@@ -68,25 +81,55 @@ __device__ __forceinline__ void softmax(float (&v)[V]) {
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    // z + lo = v - m exactly where both are finite
+    // z + lo = v - m exactly; far below the largest logit (-inf, which has no lo) p is 0
     const float z = v[i] - m;
     const float back = z + m;
-    const float lo = (v[i] - back) - ((z - (back - m)));
-    const float e = expf(z);
-    v[i] = lo == lo ? __builtin_fmaf(e, lo, e) : e;
+    const float lo = (v[i] - back) - (z - (back - m));
+    v[i] = z < -200.0f ? 0.0f : exp_of(z, lo);
     sum += v[i];
   }
-  sum = wave_sum(sum);
-  const float per = 1.0f / sum;
+  const float per = __builtin_amdgcn_rcpf(wave_sum(sum));
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] *= per;
 }
 
-template <typename T, int V>
+template <typename T, int V, bool NEXT>
 __device__ __forceinline__ void load_logits(const T* row, int E, float (&v)[V]) {
-  const int lane = threadIdx.x & 63;
+  if constexpr (NEXT) {
+    constexpr int W = V < kWide<T> ? V : kWide<T>;   // of one load
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = lane + 64 * i < E ? (float)row[lane + 64 * i] : -INFINITY;
+    for (int i = 0; i < V; ++i) v[i] = -INFINITY;
+    if (expert_of<V, true>(0) < E) {
+#pragma unroll
+      for (int i = 0; i < V; i += W) {
+        float part[W];
+        load_floats<T, W>(row + expert_of<V, true>(i), part);
+#pragma unroll
+        for (int q = 0; q < W; ++q) v[i + q] = part[q];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = expert_of<V, false>(i) < E ? (float)row[expert_of<V, false>(i)] : -INFINITY;
+  }
+}
+template <typename O, int V, bool NEXT>
+__device__ __forceinline__ void store_logits(O* row, int E, const float (&v)[V]) {
+  if constexpr (NEXT) {
+    constexpr int W = V < kWide<O> ? V : kWide<O>;
+    if (expert_of<V, true>(0) >= E) return;
+#pragma unroll
+    for (int i = 0; i < V; i += W) {
+      float part[W];
+#pragma unroll
+      for (int q = 0; q < W; ++q) part[q] = v[i + q];
+      store_floats<O, W>(row + expert_of<V, true>(i), part);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (expert_of<V, false>(i) < E) row[expert_of<V, false>(i)] = (O)v[i];
+  }
 }
 
 struct BalanceOut {
@@ -117,48 +160,76 @@ __device__ __forceinline__ void finish(int E, int k, int32_t n, const double* su
   }
 }
 
-template <typename T, int V>
+template <typename T, int V, bool NEXT>
 __global__ void __launch_bounds__(kBalThreads)
 balance_kernel(Balance b, BalanceWs ws, BalanceOut out) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int E = b.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  double* const sums = reinterpret_cast<double*>(lds);              // [E]
-  int32_t* const counts = reinterpret_cast<int32_t*>(sums + E);     // [E]
+  double* const sums = reinterpret_cast<double*>(lds);              // [4][E]
+  int32_t* const counts = reinterpret_cast<int32_t*>(sums + 4 * E); // [E]
   __shared__ int32_t valid[kBalWaves];
   __shared__ double part[kBalWaves];
-  for (int e = threadIdx.x; e < E; e += kBalThreads) {
-    sums[e] = 0.0;
-    counts[e] = 0;
-  }
+  for (int e = threadIdx.x; e < E; e += kBalThreads) counts[e] = 0;
   __syncthreads();
   double acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.0;
   int32_t n = 0;
+  // U tokens of a wave at a time, all loaded before the first is worked on
+  constexpr int U = V <= 4 ? 4 : V == 8 ? 2 : 1;
   const int64_t waves = (int64_t)gridDim.x * kBalWaves;
-  for (int64_t t = (int64_t)blockIdx.x * kBalWaves + wave; t < b.T; t += waves) {
-    if (b.mask && !b.mask[t]) continue;
-    ++n;
-    for (int j = lane; j < b.k; j += 64) {
-      const int32_t e = b.topk_ids[t * b.k + j];
-      if (e >= 0 && e < E) atomicAdd(&counts[e], 1);
-    }
-    float v[V];
-    load_logits<T, V>(static_cast<const T*>(b.logits) + t * E, E, v);
-    softmax<V>(v);
+  for (int64_t t0 = (int64_t)blockIdx.x * kBalWaves + wave; t0 < b.T; t0 += waves * U) {
+    bool live[U];
+    float v[U][V];
+    int32_t id[U];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += (double)v[i];
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + u * waves;
+      live[u] = t < b.T && (!b.mask || b.mask[t]);
+      id[u] = -1;
+      if (live[u]) {
+        load_logits<T, V, NEXT>(static_cast<const T*>(b.logits) + t * E, E, v[u]);
+        if (lane < b.k) id[u] = b.topk_ids[t * b.k + lane];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!live[u]) continue;
+      ++n;
+      if (id[u] >= 0 && id[u] < E) atomicAdd(&counts[id[u]], 1);
+      for (int j = lane + 64; j < b.k; j += 64) {
+        const int32_t e = b.topk_ids[(t0 + u * waves) * b.k + j];
+        if (e >= 0 && e < E) atomicAdd(&counts[e], 1);
+      }
+      softmax<V>(v[u]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += (double)v[u][i];
+    }
   }
   if (lane == 0) valid[wave] = n;
-  // wave after wave: the order of the sums is fixed
-  for (int w = 0; w < kBalWaves; ++w) {
-    if (w == wave) {
+  // the upper waves' sums to the lower ones, four waves at a time: their order is fixed
+#pragma unroll
+  for (int top = kBalWaves; top > 1; top = top > 4 ? top - 4 : top / 2) {
+    const int from = top > 4 ? top - 4 : top / 2, many = top - from;
+    if (wave >= from && wave < top) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (lane + 64 * i < E) sums[lane + 64 * i] += acc[i];
+        if (expert_of<V, NEXT>(i) < E) sums[(wave - from) * E + expert_of<V, NEXT>(i)] = acc[i];
+    }
+    __syncthreads();
+    if (wave >= from - many && wave < from) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (expert_of<V, NEXT>(i) < E) acc[i] += sums[(wave - from + many) * E + expert_of<V, NEXT>(i)];
     }
     __syncthreads();
   }
+  if (wave == 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (expert_of<V, NEXT>(i) < E) sums[expert_of<V, NEXT>(i)] = acc[i];
+  }
+  __syncthreads();
   n = 0;
   for (int w = 0; w < kBalWaves; ++w) n += valid[w];
   if (gridDim.x == 1) {
@@ -169,34 +240,73 @@ balance_kernel(Balance b, BalanceWs ws, BalanceOut out) {
     ws.sums[(int64_t)blockIdx.x * E + e] = sums[e];
     ws.counts[(int64_t)blockIdx.x * E + e] = counts[e];
   }
-  if (threadIdx.x == 0) ws.valid[blockIdx.x] = n;
+  if (threadIdx.x == 0) {
+    ws.valid[blockIdx.x] = n;
+    if (blockIdx.x == 0) ws.done[0] = 0;
+  }
 }
 
+// A workgroup adds up kFinishWide experts, thread (part, expert) the workgroups part, part + 32,
+// ..: one alone, which fetches what 128 CUs wrote at the pace of one CU, took 17 us of 44 (16384
+// tokens, 256 experts).  The one that is done last adds the parts of the loss, in order.
 __global__ void __launch_bounds__(kBalThreads)
 balance_finish_kernel(int E, int k, int blocks, BalanceWs ws, BalanceOut out) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  double* const sums = reinterpret_cast<double*>(lds);
-  int32_t* const counts = reinterpret_cast<int32_t*>(sums + E);
-  __shared__ double part[kBalWaves];
-  for (int e = threadIdx.x; e < E; e += kBalThreads) {
-    double s = 0.0;
-    int32_t c = 0;
-    for (int q = 0; q < blocks; ++q) {
+  constexpr int kParts = kBalThreads / kFinishWide;
+  __shared__ double sums[kParts][kFinishWide];
+  __shared__ int32_t many[kParts][kFinishWide];
+  __shared__ bool last;
+  const int in = threadIdx.x % kFinishWide, part = threadIdx.x / kFinishWide;
+  const int e = blockIdx.x * kFinishWide + in;
+  double s = 0.0;
+  int32_t c = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int q = part; q < blocks; q += kParts) {
       s += ws.sums[(int64_t)q * E + e];
       c += ws.counts[(int64_t)q * E + e];
     }
-    sums[e] = s;
-    counts[e] = c;
   }
+  sums[part][in] = s;
+  many[part][in] = c;
   int32_t n = 0;
-  for (int q = 0; q < blocks; ++q) n += ws.valid[q];
+  for (int q = threadIdx.x & 63; q < blocks; q += 64) n += ws.valid[q];
+  n = wave_sum(n);
   __syncthreads();
-  finish(E, k, n, sums, counts, out, part);
+  if (threadIdx.x < 64) {   // the first wave: 32 experts, its other lanes nothing
+    double dot = 0.0;
+    if (part == 0 && e < E) {
+      for (int q = 1; q < kParts; ++q) {
+        s += sums[q][in];
+        c += many[q][in];
+      }
+      const double mean = n > 0 ? s / (double)n : 0.0;
+      out.mean_probs[e] = (float)mean;
+      out.counts[e] = c;
+      dot = (double)c * mean;
+    }
+    dot = wave_sum(dot);
+    if (threadIdx.x == 0) {
+      ws.dots[blockIdx.x] = dot;
+      __threadfence();
+      last = atomicAdd(ws.done, 1) == (int32_t)gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!last || threadIdx.x >= 64) return;
+  __threadfence();
+  double all = 0.0;
+  for (int q = threadIdx.x; q < (int)gridDim.x; q += 64)
+    all += __hip_atomic_load(&ws.dots[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  all = wave_sum(all);
+  if (threadIdx.x == 0) {
+    out.loss[0] = n > 0 ? (float)(all * (double)E / ((double)n * (double)k)) : 0.0f;
+    out.num_valid[0] = n;
+  }
 }
 
 static constexpr int kBackThreads = 256, kBackWaves = kBackThreads / 64;
 
-template <typename T, typename O, int V>
+template <typename T, typename O, int V, bool NEXT>
 __global__ void __launch_bounds__(kBackThreads)
 balance_backward_kernel(Balance b, const int32_t* __restrict__ counts, const int32_t* __restrict__ num_valid,
                         const float* __restrict__ d_loss, O* __restrict__ d_logits) {
@@ -205,36 +315,49 @@ balance_backward_kernel(Balance b, const int32_t* __restrict__ counts, const int
   const double g = n > 0 ? (d_loss ? (double)d_loss[0] : 1.0) * (double)E / ((double)n * (double)n * (double)b.k) : 0.0;
   float c[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) c[i] = lane + 64 * i < E ? (float)counts[lane + 64 * i] : 0.0f;
+  for (int i = 0; i < V; ++i) c[i] = expert_of<V, NEXT>(i) < E ? (float)counts[expert_of<V, NEXT>(i)] : 0.0f;
+  constexpr int U = V <= 4 ? 2 : 1;
   const int64_t waves = (int64_t)gridDim.x * kBackWaves;
-  for (int64_t t = (int64_t)blockIdx.x * kBackWaves + wave; t < b.T; t += waves) {
-    O* const to = d_logits + t * E;
-    if (b.mask && !b.mask[t]) {
+  for (int64_t t0 = (int64_t)blockIdx.x * kBackWaves + wave; t0 < b.T; t0 += waves * U) {
+    bool live[U];
+    float p[U][V];
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (lane + 64 * i < E) to[lane + 64 * i] = (O)0.0f;
-      continue;
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + u * waves;
+      live[u] = t < b.T && (!b.mask || b.mask[t]);
+      if (live[u]) load_logits<T, V, NEXT>(static_cast<const T*>(b.logits) + t * E, E, p[u]);
     }
-    float p[V];
-    load_logits<T, V>(static_cast<const T*>(b.logits) + t * E, E, p);
-    softmax<V>(p);
-    double dot = 0.0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) dot = __builtin_fma((double)p[i], (double)c[i], dot);
-    dot = wave_sum(dot);
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + u * waves;
+      if (t >= b.T) break;
+      double dot = 0.0;
+      if (live[u]) {
+        softmax<V>(p[u]);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 64 * i < E) to[lane + 64 * i] = (O)(float)(g * (double)p[i] * ((double)c[i] - dot));
+        for (int i = 0; i < V; ++i) dot = __builtin_fma((double)p[u][i], (double)c[i], dot);
+        dot = wave_sum(dot);
+      }
+      float d[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] = live[u] ? (float)(g * (double)p[u][i] * ((double)c[i] - dot)) : 0.0f;
+      store_logits<O, V, NEXT>(d_logits + t * E, E, d);
+    }
   }
 }
 
+// go(experts of a lane, whether they are neighbours)
 template <typename F>
 static hipError_t for_experts(int E, F&& go) {
-  if (E <= 64) return go(std::integral_constant<int, 1>{});
-  if (E <= 128) return go(std::integral_constant<int, 2>{});
-  if (E <= 256) return go(std::integral_constant<int, 4>{});
-  if (E <= 512) return go(std::integral_constant<int, 8>{});
-  return go(std::integral_constant<int, 16>{});
+  auto with = [&](auto per) {
+    if (decltype(per)::value > 1 && E % decltype(per)::value == 0) return go(per, std::true_type{});
+    return go(per, std::false_type{});
+  };
+  if (E <= 64) return go(std::integral_constant<int, 1>{}, std::false_type{});
+  if (E <= 128) return with(std::integral_constant<int, 2>{});
+  if (E <= 256) return with(std::integral_constant<int, 4>{});
+  if (E <= 512) return with(std::integral_constant<int, 8>{});
+  return with(std::integral_constant<int, 16>{});
 }
 
 hipError_t launch_balance_loss(const Balance& b, float* loss, int32_t* counts, float* mean_probs,
@@ -242,17 +365,19 @@ hipError_t launch_balance_loss(const Balance& b, float* loss, int32_t* counts, f
   const BalanceWs ws = balance_ws(workspace, b.E);
   const BalanceOut out = {loss, counts, mean_probs, num_valid};
   const int blocks = b.T <= kBalSingle ? 1 : (int)std::min<int64_t>(ceil_div(b.T, kBalWaves), kBalBlocks);
-  const size_t lds = (size_t)b.E * 12;
-  const hipError_t st = for_experts(b.E, [&](auto per) {
+  const size_t lds = (size_t)b.E * 36;
+  const hipError_t st = for_experts(b.E, [&](auto per, auto next) {
     constexpr int V = decltype(per)::value;
+    constexpr bool N = decltype(next)::value;
     if (b.logits_f32)
-      hipLaunchKernelGGL((balance_kernel<float, V>), dim3(blocks), dim3(kBalThreads), lds, stream, b, ws, out);
+      hipLaunchKernelGGL((balance_kernel<float, V, N>), dim3(blocks), dim3(kBalThreads), lds, stream, b, ws, out);
     else
-      hipLaunchKernelGGL((balance_kernel<bf16_t, V>), dim3(blocks), dim3(kBalThreads), lds, stream, b, ws, out);
+      hipLaunchKernelGGL((balance_kernel<bf16_t, V, N>), dim3(blocks), dim3(kBalThreads), lds, stream, b, ws, out);
     return hipGetLastError();
   });
   if (st != hipSuccess || blocks == 1) return st;
-  hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(kBalThreads), lds, stream, b.E, b.k, blocks, ws, out);
+  hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)ceil_div(b.E, kFinishWide)), dim3(kBalThreads), 0, stream,
+                     b.E, b.k, blocks, ws, out);
   return hipGetLastError();
 }
 
@@ -260,19 +385,20 @@ hipError_t launch_balance_loss_backward(const Balance& b, bool out_f32, const in
                                         const int32_t* num_valid, const float* d_loss, void* d_logits,
                                         hipStream_t stream) {
   const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(b.T, kBackWaves), 256 * 8);
-  return for_experts(b.E, [&](auto per) {
+  return for_experts(b.E, [&](auto per, auto next) {
     constexpr int V = decltype(per)::value;
+    constexpr bool N = decltype(next)::value;
     auto go = [&](auto kernel, auto* to) {
       hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kBackThreads), 0, stream, b, counts, num_valid, d_loss, to);
     };
     float* f = static_cast<float*>(d_logits);
     bf16_t* h = static_cast<bf16_t*>(d_logits);
     if (b.logits_f32) {
-      if (out_f32) go(balance_backward_kernel<float, float, V>, f);
-      else go(balance_backward_kernel<float, bf16_t, V>, h);
+      if (out_f32) go(balance_backward_kernel<float, float, V, N>, f);
+      else go(balance_backward_kernel<float, bf16_t, V, N>, h);
     } else {
-      if (out_f32) go(balance_backward_kernel<bf16_t, float, V>, f);
-      else go(balance_backward_kernel<bf16_t, bf16_t, V>, h);
+      if (out_f32) go(balance_backward_kernel<bf16_t, float, V, N>, f);
+      else go(balance_backward_kernel<bf16_t, bf16_t, V, N>, h);
     }
     return hipGetLastError();
   });

@@ -19,66 +19,75 @@
 #include "common.hpp"
 #include "kernels.hpp"
 #include "vec.hpp"
+#include "wave.hpp"
 
 namespace moelora {
 
 static constexpr double kCodes = 127.0;
-static constexpr uint64_t kInfBits = uint64_t(0x7FF) << 52;   // magnitudes as integers: finite < infinity < NaN
-
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int off) {
-  const uint32_t lo = __shfl_xor((uint32_t)v, off, 64), hi = __shfl_xor((uint32_t)(v >> 32), off, 64);
-  return (uint64_t)hi << 32 | lo;
-}
 
 // scale of a row with largest magnitude `top`, and what its values are multiplied by to become
 // codes (0 where all codes are 0)
 struct RowScale {
   float scale;
   double per;
+  bool clamp;
 };
 __device__ __forceinline__ RowScale row_scale(double top) {
   RowScale s;
   s.scale = (float)(top / kCodes);
   s.per = s.scale > 0.0f ? 1.0 / (double)s.scale : 0.0;
-  if (!(top < __builtin_inf())) s = {__builtin_nanf(""), 0.0};
+  if (!(top < __builtin_inf())) s = {__builtin_nanf(""), 0.0, false};
+  s.clamp = s.scale < 0x1p-126f;
   return s;
 }
 
-// Nearest integer of the quotient v / scale of two fp32 values, from the product with the
-// rounded 1 / scale: the quotient is half an integer or at least 2^-27 away from one, so
-// rounded to multiples of 2^-36 first it is what the exact one would be.
-// (The norm's values are no quotients of that kind.)
+// Nearest integer of v * per, in the low bits of what is returned.  SNAP, for the quotient of two
+// fp32 values by per = the rounded 1 / scale: that quotient is half an integer or at least 2^-27
+// away from one, so rounded to multiples of 2^-36 first it is what the exact one would be.  The
+// rounding is that of additions: ties to even.
 template <bool SNAP>
-__device__ __forceinline__ int32_t code_of(double q) {
-  constexpr double kSnap = 1.5 * 65536.0;   // its last bit is 2^-36
-  if constexpr (SNAP) q = (q + kSnap) - kSnap;
-  return min(max((int32_t)__builtin_rint(q), -127), 127);
+__device__ __forceinline__ uint32_t code_of(double v, double per) {
+  constexpr double kSnap = 1.5 * 65536.0;              // its last bit is 2^-36
+  constexpr double kInt = 1.5 * 4503599627370496.0;    // its last bit is 1
+  const double q = SNAP ? __builtin_fma(v, per, kSnap) + (kInt - kSnap) : __builtin_fma(v, per, kInt);
+  return (uint32_t)__builtin_bit_cast(uint64_t, q);
 }
 
-// codes of a piece, the first in the lowest byte
+// The codes of a piece.  A scale below fp32's normal numbers is that much off that codes past 127
+// come out (clamp).
 template <int V, typename F>
-__device__ __forceinline__ void store_codes(int8_t* to, F&& code) {
-  if constexpr (V == 1) {
-    *to = (int8_t)code(0);
-  } else {
-    typedef int8_t bytes __attribute__((ext_vector_type(V), aligned(1)));
-    bytes b;
+__device__ __forceinline__ void store_codes(int8_t* to, bool clamp, F&& code) {
+  uint32_t c[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) b[i] = (int8_t)code(i);
-    *reinterpret_cast<bytes*>(to) = b;
+  for (int i = 0; i < V; ++i) c[i] = code(i);
+  if (clamp) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = (uint32_t)min(max((int32_t)c[i], -127), 127);
+  }
+  if constexpr (V == 1) {
+    *to = (int8_t)c[0];
+  } else {
+    typedef uint32_t words __attribute__((ext_vector_type(V / 4), aligned(1)));
+    words w;
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const uint32_t lo = __builtin_amdgcn_perm(c[4 * i + 1], c[4 * i], 0x0C0C0400);
+      const uint32_t hi = __builtin_amdgcn_perm(c[4 * i + 3], c[4 * i + 2], 0x04000C0C);
+      const uint32_t both = lo | hi;
+      if constexpr (V == 4) w = both;
+      else w[i] = both;
+    }
+    __builtin_memcpy(to, &w, V);
   }
 }
 
-// The largest of `top` and the sum of `sum` over the G threads of a row (both over all waves of
-// the workgroup if G is more than a wave).  `buf`: two sets of 2 x waves words, taken in turn, so
-// that one barrier a row is enough.
-template <int G>
-__device__ __forceinline__ void over_row(uint64_t& top, double& sum, bool with_sum, uint64_t (*buf)[2]) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    top = max(top, shfl_xor64(top, off));
-    if (with_sum) sum += __builtin_bit_cast(double, shfl_xor64(__builtin_bit_cast(uint64_t, sum), off));
-  }
+// The largest of `top` and the sum of `sum` over the G threads of a row (over all waves of the
+// workgroup if G is more than a wave).  `buf`: a set of two, taken in turn, so that one barrier a
+// row is enough.
+template <int G, typename M>
+__device__ __forceinline__ void over_row(M& top, double& sum, bool with_sum, uint64_t (*buf)[2]) {
+  top = wave_max(top, M(0));
+  if (with_sum) sum = wave_sum(sum);
   if constexpr (G > 64) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
@@ -86,12 +95,12 @@ __device__ __forceinline__ void over_row(uint64_t& top, double& sum, bool with_s
       buf[wave][1] = __builtin_bit_cast(uint64_t, sum);
     }
     __syncthreads();
-    top = buf[0][0];
+    top = (M)buf[0][0];
     sum = __builtin_bit_cast(double, buf[0][1]);
 #pragma unroll
     for (int w = 1; w < G / 64; ++w) {
-      top = max(top, buf[w][0]);
-      sum += __builtin_bit_cast(double, buf[w][1]);
+      top = max(top, (M)buf[w][0]);
+      if (with_sum) sum += __builtin_bit_cast(double, buf[w][1]);
     }
   }
 }
@@ -165,7 +174,8 @@ int8_rows_kernel(Int8Rows p) {
       if constexpr (NORM) return h_of(u, i) * (double)w[i];
       return h_of(u, i);
     };
-    uint64_t top = 0;
+    // magnitudes as integers: finite < infinity < NaN
+    typename std::conditional<NORM, uint64_t, uint32_t>::type top = 0;
     double sum = 0.0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -175,11 +185,12 @@ int8_rows_kernel(Int8Rows p) {
       const int twice = (int)((lane + u * G) * V - place(u));
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const uint64_t mag = __builtin_bit_cast(uint64_t, value(u, i)) & ~(uint64_t(1) << 63);
-        top = max(top, mag);
         if constexpr (NORM) {
+          top = max(top, __builtin_bit_cast(uint64_t, value(u, i)) & ~(uint64_t(1) << 63));
           const double h = h_of(u, i);
           if (V == 1 || i >= twice) sum = __builtin_fma(h, h, sum);
+        } else {
+          top = max(top, __builtin_bit_cast(uint32_t, elem(vx[u], i)) & 0x7FFFFFFFu);
         }
       }
     }
@@ -192,15 +203,18 @@ int8_rows_kernel(Int8Rows p) {
     asm volatile("" : "+s"(again));
     double norm = 1.0;
     if constexpr (NORM) norm = 1.0 / __builtin_sqrt(sum / (double)n + p.eps);
-    const RowScale s = row_scale(__builtin_bit_cast(double, top) * norm);
+    RowScale s;
+    if constexpr (NORM) s = row_scale(__builtin_bit_cast(double, top) * norm);
+    else s = row_scale((double)__builtin_bit_cast(float, top));
     const double per = NORM ? norm * s.per : s.per;
     if (lane == 0) p.scales[row] = s.scale;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!in_row(u)) continue;
       weights(u);
-      store_codes<V>(p.codes + row * n + place(u),
-                     [&](int i) { return s.per > 0.0 ? code_of<!NORM>(value(u, i) * per) : 0; });
+      store_codes<V>(p.codes + row * n + place(u), s.clamp, [&](int i) {
+        return s.per > 0.0 ? code_of<!NORM>(value(u, i), per) : 0;
+      });
       if constexpr (NORM) {
         float out[V];
         if (p.residual_out) {
@@ -228,23 +242,23 @@ __global__ void __launch_bounds__(1024) int8_long_rows_kernel(Int8Rows p) {
   const T* const x = static_cast<const T*>(p.x);
   int turn = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
-    uint64_t top = 0;
+    uint32_t top = 0;
     for (int64_t u = threadIdx.x; u < units; u += 1024) {
       float v[V];
       load_floats<T, V>(x + row * n + piece_at<V>(u, n), v);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        top = max(top, __builtin_bit_cast(uint64_t, (double)v[i]) & ~(uint64_t(1) << 63));
+      for (int i = 0; i < V; ++i) top = max(top, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
     }
     double none = 0.0;
     over_row<1024>(top, none, false, buf[turn]);
-    const RowScale s = row_scale(__builtin_bit_cast(double, top));
+    const RowScale s = row_scale((double)__builtin_bit_cast(float, top));
     if (threadIdx.x == 0) p.scales[row] = s.scale;
     for (int64_t u = threadIdx.x; u < units; u += 1024) {
       const int64_t at = row * n + piece_at<V>(u, n);
       float v[V];
       load_floats<T, V>(x + at, v);
-      store_codes<V>(p.codes + at, [&](int i) { return s.per > 0.0 ? code_of<true>((double)v[i] * s.per) : 0; });
+      store_codes<V>(p.codes + at, s.clamp,
+                     [&](int i) { return s.per > 0.0 ? code_of<true>((double)v[i], s.per) : 0; });
     }
   }
 }
