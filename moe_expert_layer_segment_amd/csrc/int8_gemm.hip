@@ -123,16 +123,23 @@ int8_stream_kernel(Int8Gemm p, int row_groups, int col_groups) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) acc[mb][nb] = mfma_i8(f.w[nb][h], f.x[mb][h], acc[mb][nb]);
   };
+  // a group is fetched while the one before is multiplied
   const int whole = chunks / (4 * H);
-  Group f;
+  Group f[2];
   int s = wave;
-  for (; s < whole; s += WV) {
-    load(f, s, std::false_type{});
-    multiply(f);
+  if (s < whole) load(f[0], s, std::false_type{});
+  while (s < whole) {
+    if (s + WV < whole) load(f[1], s + WV, std::false_type{});
+    multiply(f[0]);
+    s += WV;
+    if (s >= whole) break;
+    if (s + WV < whole) load(f[0], s + WV, std::false_type{});
+    multiply(f[1]);
+    s += WV;
   }
   if (s * 4 * H < chunks) {   // the wave whose turn it is takes the end of the rows
-    load(f, s, std::true_type{});
-    multiply(f);
+    load(f[0], s, std::true_type{});
+    multiply(f[0]);
   }
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
@@ -558,6 +565,15 @@ static hipError_t tiled(const Int8Gemm& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// A workgroup of 4 waves and 16 NB columns, or, where those would not fill the chip, of WIDE
+// waves and 16 columns (32 with silu_mul: a gate and an up block).
+template <int MB, int NB, int WIDE>
+static hipError_t few(const Int8Gemm& p, hipStream_t s) {
+  if (ceil_div(p.M, 16 * MB) * ceil_div(p.N, 16 * NB) >= 512) return stream<MB, NB, 4>(p, s);
+  if (p.silu_mul) return stream<MB, 2, WIDE>(p, s);
+  return stream<MB, 1, WIDE>(p, s);
+}
+
 hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t s) {
   // rows of a workgroup: within one tile_expert entry, or those there are
   const int64_t rows = p.tile_expert ? p.BM : p.M;
@@ -569,7 +585,7 @@ hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t s) {
     return tiled<64>(p, s);
   }
   if (takes(32)) return stream<2, 4, 4>(p, s);
-  return stream<1, 4, 4>(p, s);
+  return few<1, 4, 16>(p, s);
 }
 
 }  // namespace moelora
