@@ -538,7 +538,8 @@ int moe_lora_rms_norm_quantize(int64_t num_tokens, int32_t hidden, int32_t dtype
   p.x_f32 = dtype == MOE_LORA_F32;
   p.weight_f32 = weight_dtype == MOE_LORA_F32;
   p.y_f32 = y_dtype == MOE_LORA_F32;
-  p.x = x; p.weight = weight; p.residual = residual; p.eps = eps;
+  p.x = x; p.weight = weight; p.residual = residual;
+  p.eps = eps; p.per_col = 1.0 / hidden;
   p.residual_out = residual_out; p.y = y; p.codes = codes; p.scales = scales;
   return hip_status(launch_int8_rows(p, static_cast<hipStream_t>(stream)));
 }

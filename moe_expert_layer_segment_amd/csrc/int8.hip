@@ -23,22 +23,39 @@
 
 namespace moelora {
 
-static constexpr double kCodes = 127.0;
+// 1 / v and 1 / sqrt(v) of a positive normal number, to fp64's last bit or the one before: the
+// hardware's first guess and two steps of Newton's.  (Every wave of a row works them out: as
+// quotients and a root of fp64 they took 16384 x 7168 from 215 to
+// 228 us.)
+__device__ __forceinline__ double reciprocal(double v) {
+  double r = __builtin_amdgcn_rcp(v);
+  r = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
+}
+__device__ __forceinline__ double reciprocal_root(double v) {
+  double r = __builtin_amdgcn_rsq(v);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = __builtin_fma(__builtin_fma(-v * r, r, 1.0), 0.5 * r, r);
+  return r;
+}
 
-// scale of a row with largest magnitude `top`, and what its values are multiplied by to become
-// codes (0 where all codes are 0)
+// scale of a row, what its values are multiplied by to become codes (0 where all codes are 0),
+// and whether codes past 127 may come out: a scale below fp32's normal numbers is that much off
 struct RowScale {
   float scale;
   double per;
   bool clamp;
 };
-__device__ __forceinline__ RowScale row_scale(double top) {
+// of scale = largest magnitude / 127; not finite: `top` was not
+__device__ __forceinline__ RowScale row_scale(float scale, bool finite) {
   RowScale s;
-  s.scale = (float)(top / kCodes);
-  s.per = s.scale > 0.0f ? 1.0 / (double)s.scale : 0.0;
-  if (!(top < __builtin_inf())) s = {__builtin_nanf(""), 0.0, false};
+  s.scale = finite ? scale : __builtin_nanf("");
+  s.per = s.scale > 0.0f ? reciprocal((double)s.scale) : 0.0;
   s.clamp = s.scale < 0x1p-126f;
   return s;
+}
+__device__ __forceinline__ RowScale row_scale_of(uint32_t top) {   // magnitude as an integer
+  return row_scale(__builtin_bit_cast(float, top) / 127.0f, top < 0x7F800000u);
 }
 
 // Nearest integer of v * per, in the low bits of what is returned.  SNAP, for the quotient of two
@@ -53,8 +70,7 @@ __device__ __forceinline__ uint32_t code_of(double v, double per) {
   return (uint32_t)__builtin_bit_cast(uint64_t, q);
 }
 
-// The codes of a piece.  A scale below fp32's normal numbers is that much off that codes past 127
-// come out (clamp).
+// The codes of a piece
 template <int V, typename F>
 __device__ __forceinline__ void store_codes(int8_t* to, bool clamp, F&& code) {
   uint32_t c[V];
@@ -95,18 +111,17 @@ __device__ __forceinline__ void over_row(M& top, double& sum, bool with_sum, uin
       buf[wave][1] = __builtin_bit_cast(uint64_t, sum);
     }
     __syncthreads();
-    top = (M)buf[0][0];
-    sum = __builtin_bit_cast(double, buf[0][1]);
-#pragma unroll
-    for (int w = 1; w < G / 64; ++w) {
-      top = max(top, (M)buf[w][0]);
-      if (with_sum) sum += __builtin_bit_cast(double, buf[w][1]);
-    }
+    // every wave's, one to a lane: all of them in a thread are 64 registers of a large workgroup
+    const int lane = threadIdx.x & 63;
+    const bool in = lane < G / 64;
+    top = wave_max(in ? (M)buf[lane % (G / 64)][0] : M(0), M(0));
+    if (with_sum) sum = wave_sum(in ? __builtin_bit_cast(double, buf[lane % (G / 64)][1]) : 0.0);
   }
 }
 
-// What comes behind does not see through to where `v` was used before: it converts again what the
-// compiler would otherwise keep as fp64 from the first use on (256 registers instead of 90).
+// What comes behind does not see through to where `v` was used before: bf16 is widened again where
+// the compiler would keep it as fp32, in twice the registers, from the first use on (a row of 4096
+// to a wave: 76 registers, and 667 us instead of 535 for 229376 rows).
 template <typename P>
 __device__ __forceinline__ void forget(P& v) {
   if constexpr (sizeof(P) == 16) {
@@ -118,13 +133,12 @@ __device__ __forceinline__ void forget(P& v) {
 }
 
 // G threads to a row of n elements, U pieces of V elements to a thread.
-template <typename T, int V, int G, int U, bool NORM>
+template <typename T, int V, int G, int U>
 __global__ void __launch_bounds__(G > 256 ? G : 256)
 int8_rows_kernel(Int8Rows p) {
   constexpr int kPer = (G > 256 ? G : 256) / G;   // rows of a workgroup
   __shared__ uint64_t buf[2][G / 64][2];
-  // a row's base is uniform and its places are 32 bits: an address of 64 bits for each piece of
-  // each array would cost half the waves
+  // a row's base is uniform and its places are 32 bits
   const uint32_t n = (uint32_t)p.cols, lane = threadIdx.x % G;
   const int64_t rows = p.rows_used ? min((int64_t)max(p.rows_used[0], 0), p.num_rows) : p.num_rows;
   auto in_row = [&](int u) { return (lane + u * G) * V < n; };
@@ -139,95 +153,123 @@ int8_rows_kernel(Int8Rows p) {
     const int64_t row = first + (kPer > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / G) : 0);
     if (kPer > 1 && row >= rows) return;   // a whole wave, and no barrier with G = 64
     const T* const x = static_cast<const T*>(p.x) + row * n;
-    typename Vec<T, V>::type vx[U], vr[NORM ? U : 1];
+    typename Vec<T, V>::type v[U];
+    uint32_t top = 0;   // magnitudes as integers: finite < infinity < NaN
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (in_row(u)) vx[u] = load_vec<T, V>(x + place(u));
-    }
-    if constexpr (NORM) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) vr[u] = {};
-      if (p.residual) {
-        const T* const res = static_cast<const T*>(p.residual) + row * n;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (in_row(u)) vr[u] = load_vec<T, V>(res + place(u));
-        }
-      }
-    }
-    auto h_of = [&](int u, int i) -> double {
-      const double h = (double)elem(vx[u], i);
-      if constexpr (NORM) return h + (double)elem(vr[u], i);
-      return h;
-    };
-    // The weights stay in the L1: in registers over the rows they would cost waves.
-    float w[V];
-    uint32_t again = 0;   // for the second time: not known to be 0
-    auto weights = [&](int u) {
-      if constexpr (NORM) {
-        if (p.weight_f32) load_floats<float, V>(static_cast<const float*>(p.weight) + (place(u) + again), w);
-        else load_floats<bf16_t, V>(static_cast<const bf16_t*>(p.weight) + (place(u) + again), w);
-      }
-    };
-    // what is quantized, but for the factor 1 / sqrt(..) of the row
-    auto value = [&](int u, int i) -> double {
-      if constexpr (NORM) return h_of(u, i) * (double)w[i];
-      return h_of(u, i);
-    };
-    // magnitudes as integers: finite < infinity < NaN
-    typename std::conditional<NORM, uint64_t, uint32_t>::type top = 0;
-    double sum = 0.0;
+    for (int u = 0; u < U; ++u)
+      if (in_row(u)) v[u] = load_vec<T, V>(x + place(u));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!in_row(u)) continue;
-      weights(u);
-      // elements that the last piece of a row repeats
-      const int twice = (int)((lane + u * G) * V - place(u));
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if constexpr (NORM) {
-          top = max(top, __builtin_bit_cast(uint64_t, value(u, i)) & ~(uint64_t(1) << 63));
-          const double h = h_of(u, i);
-          if (V == 1 || i >= twice) sum = __builtin_fma(h, h, sum);
-        } else {
-          top = max(top, __builtin_bit_cast(uint32_t, elem(vx[u], i)) & 0x7FFFFFFFu);
-        }
-      }
+      for (int i = 0; i < V; ++i) top = max(top, __builtin_bit_cast(uint32_t, elem(v[u], i)) & 0x7FFFFFFFu);
     }
-    over_row<G>(top, sum, NORM, buf[turn]);
+    double none = 0.0;
+    over_row<G>(top, none, false, buf[turn]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      forget(vx[u]);
-      if constexpr (NORM) forget(vr[u]);
-    }
-    asm volatile("" : "+s"(again));
-    double norm = 1.0;
-    if constexpr (NORM) norm = 1.0 / __builtin_sqrt(sum / (double)n + p.eps);
-    RowScale s;
-    if constexpr (NORM) s = row_scale(__builtin_bit_cast(double, top) * norm);
-    else s = row_scale((double)__builtin_bit_cast(float, top));
-    const double per = NORM ? norm * s.per : s.per;
+    for (int u = 0; u < U; ++u) forget(v[u]);
+    const RowScale s = row_scale_of(top);
     if (lane == 0) p.scales[row] = s.scale;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!in_row(u)) continue;
-      weights(u);
-      store_codes<V>(p.codes + row * n + place(u), s.clamp, [&](int i) {
-        return s.per > 0.0 ? code_of<!NORM>(value(u, i), per) : 0;
-      });
-      if constexpr (NORM) {
+      store_codes<V>(p.codes + row * n + place(u), s.clamp,
+                     [&](int i) { return s.per > 0.0 ? code_of<true>((double)elem(v[u], i), s.per) : 0; });
+    }
+  }
+}
+
+// The same of the norm.  h * weight stays in registers, as fp64, from the sums to the codes: made
+// again from x and the residual it costs as much as all that follows (16384 x 7168: 247 -> 229 us).
+template <typename T, int V, int G, int U>
+__global__ void __launch_bounds__(G > 256 ? G : 256)
+int8_norm_kernel(Int8Rows p) {
+  constexpr int kPer = (G > 256 ? G : 256) / G;
+  __shared__ uint64_t buf[2][G / 64][2];
+  const uint32_t n = (uint32_t)p.cols, lane = threadIdx.x % G;
+  auto in_row = [&](int u) { return (lane + u * G) * V < n; };
+  auto place = [&](int u) { return min((lane + u * G) * V, n - V); };
+  int turn = 0;
+  for (int64_t first = (int64_t)blockIdx.x * kPer; first < p.num_rows;
+       first += (int64_t)gridDim.x * kPer, turn ^= 1) {
+    const int64_t row = first + (kPer > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / G) : 0);
+    if (kPer > 1 && row >= p.num_rows) return;
+    const T* const x = static_cast<const T*>(p.x) + row * n;
+    typename Vec<T, V>::type vx[U], vr[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (in_row(u)) vx[u] = load_vec<T, V>(x + place(u));
+#pragma unroll
+    for (int u = 0; u < U; ++u) vr[u] = {};
+    if (p.residual) {
+      const T* const res = static_cast<const T*>(p.residual) + row * n;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (in_row(u)) vr[u] = load_vec<T, V>(res + place(u));
+    }
+    // Where residual_out is the residual (or x) the last piece of a row may repeat elements that
+    // another wave is about to change.
+    if (G > 64 && p.residual_out && n % V) __syncthreads();
+    double value[U][V];   // what is quantized, but for the factor 1 / sqrt(..) of the row
+    uint64_t top = 0;
+    double sum = 0.0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!in_row(u)) continue;
+      float fx[V], fr[V], w[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (V == 1) {
+          fx[i] = (float)vx[u];
+          fr[i] = (float)vr[u];
+        } else {
+          fx[i] = (float)vx[u][i];
+          fr[i] = (float)vr[u][i];
+        }
+      }
+      if (p.weight_f32) load_floats<float, V>(static_cast<const float*>(p.weight) + place(u), w);
+      else load_floats<bf16_t, V>(static_cast<const bf16_t*>(p.weight) + place(u), w);
+      // elements that the last piece of a row repeats
+      const int twice = (int)((lane + u * G) * V - place(u));
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const double h = (double)fx[i] + (double)fr[i];
+        value[u][i] = h * (double)w[i];
+        top = max(top, __builtin_bit_cast(uint64_t, value[u][i]) & ~(uint64_t(1) << 63));
+        if (V == 1 || i >= twice) sum = __builtin_fma(h, h, sum);
+      }
+      if (p.residual_out) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) fx[i] += fr[i];
+        store_floats<T, V>(static_cast<T*>(p.residual_out) + row * n + place(u), fx);
+      }
+      if constexpr (G * U > 2048) {   // 128 registers: piece after piece, and not all widened first
+        for (int q = u + 1; q < U; ++q) {
+          forget(vx[q]);
+          forget(vr[q]);
+        }
+        asm volatile("" : "+v"(top), "+v"(sum));
+      }
+    }
+    over_row<G>(top, sum, true, buf[turn]);
+    const double square = sum * p.per_col + p.eps;
+    // 0, infinite and NaN sums have no steps to take
+    const double norm = square > 0.0 && square < __builtin_inf() ? reciprocal_root(square) : 1.0 / __builtin_sqrt(square);
+    const double most = __builtin_bit_cast(double, top) * norm;
+    const RowScale s = row_scale((float)(most * (1.0 / 127.0)), most < __builtin_inf());
+    const double per = norm * s.per;
+    if (lane == 0) p.scales[row] = s.scale;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!in_row(u)) continue;
+      store_codes<V>(p.codes + row * n + place(u), s.clamp,
+                     [&](int i) { return s.per > 0.0 ? code_of<false>(value[u][i], per) : 0; });
+      if (p.y) {
         float out[V];
-        if (p.residual_out) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) out[i] = elem(vx[u], i) + elem(vr[u], i);
-          store_floats<T, V>(static_cast<T*>(p.residual_out) + row * n + place(u), out);
-        }
-        if (p.y) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) out[i] = (float)(value(u, i) * norm);
-          if (p.y_f32) store_floats<float, V>(static_cast<float*>(p.y) + row * n + place(u), out);
-          else store_floats<bf16_t, V>(static_cast<bf16_t*>(p.y) + row * n + place(u), out);
-        }
+        for (int i = 0; i < V; ++i) out[i] = (float)(value[u][i] * norm);
+        if (p.y_f32) store_floats<float, V>(static_cast<float*>(p.y) + row * n + place(u), out);
+        else store_floats<bf16_t, V>(static_cast<bf16_t*>(p.y) + row * n + place(u), out);
       }
     }
   }
@@ -251,7 +293,7 @@ __global__ void __launch_bounds__(1024) int8_long_rows_kernel(Int8Rows p) {
     }
     double none = 0.0;
     over_row<1024>(top, none, false, buf[turn]);
-    const RowScale s = row_scale((double)__builtin_bit_cast(float, top));
+    const RowScale s = row_scale_of(top);
     if (threadIdx.x == 0) p.scales[row] = s.scale;
     for (int64_t u = threadIdx.x; u < units; u += 1024) {
       const int64_t at = row * n + piece_at<V>(u, n);
@@ -263,40 +305,55 @@ __global__ void __launch_bounds__(1024) int8_long_rows_kernel(Int8Rows p) {
   }
 }
 
-// blocks of one launch: enough to fill the chip, so that a workgroup keeps the norm's weights
-// over its rows
-static unsigned row_blocks(int64_t num_rows, int per, int waves) {
-  return (unsigned)std::min<int64_t>(ceil_div(num_rows, per), 256 * 32 / waves);
+// A workgroup to every row (or four), in their order: with as many as fill the chip, each taking
+// every 2048th row, 229376 rows of 4096 took 539 us instead of 512.  Threads of a launch are
+// counted in 32 bits, so past 2^20 workgroups they come round again.
+static unsigned row_blocks(int64_t num_rows, int per) {
+  return (unsigned)std::min<int64_t>(ceil_div(num_rows, per), int64_t(1) << 20);
 }
 
-template <typename T, bool NORM>
+template <typename K>
+static hipError_t go_rows(K kernel, int threads, int per, const Int8Rows& p, hipStream_t stream) {
+  hipLaunchKernelGGL(kernel, dim3(row_blocks(p.num_rows, per)), dim3(threads), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <typename T>
 static hipError_t launch_rows(const Int8Rows& p, hipStream_t stream) {
   constexpr int V = kWide<T>;
-  auto go = [&](auto kernel, int threads, int per) {
-    hipLaunchKernelGGL(kernel, dim3(row_blocks(p.num_rows, per, threads / 64)), dim3(threads), 0, stream, p);
-    return hipGetLastError();
-  };
   const int64_t units = ceil_div(p.cols, V);
-  if (p.cols < V) return go(int8_rows_kernel<T, 1, 64, 1, NORM>, 256, 4);
-  if (units <= 64) return go(int8_rows_kernel<T, V, 64, 1, NORM>, 256, 4);
-  if (units <= 128) return go(int8_rows_kernel<T, V, 64, 2, NORM>, 256, 4);
-  if (units <= 256) return go(int8_rows_kernel<T, V, 256, 1, NORM>, 256, 1);
-  if (units <= 512) return go(int8_rows_kernel<T, V, 256, 2, NORM>, 256, 1);
-  if (units <= 1024) return go(int8_rows_kernel<T, V, 256, 4, NORM>, 256, 1);
-  if (units <= 4096) return go(int8_rows_kernel<T, V, 1024, 4, NORM>, 1024, 1);
-  if constexpr (!NORM) return go(int8_long_rows_kernel<T, V>, 1024, 1);
-  return hipErrorInvalidValue;
+  if (p.cols < V) return go_rows(int8_rows_kernel<T, 1, 64, 1>, 256, 4, p, stream);
+  if (units <= 128) return go_rows(int8_rows_kernel<T, V, 64, 2>, 256, 4, p, stream);
+  // a wave to a row, so no barrier (229376 rows of 4096: 585 us with 256 threads, 535)
+  if (units <= 512) return go_rows(int8_rows_kernel<T, V, 64, 8>, 256, 4, p, stream);
+  if (units <= 1024) return go_rows(int8_rows_kernel<T, V, 256, 4>, 256, 1, p, stream);
+  if (units <= 4096) return go_rows(int8_rows_kernel<T, V, 1024, 4>, 1024, 1, p, stream);
+  return go_rows(int8_long_rows_kernel<T, V>, 1024, 1, p, stream);
+}
+
+template <typename T>
+static hipError_t launch_norm(const Int8Rows& p, hipStream_t stream) {
+  constexpr int V = kWide<T>;
+  const int64_t units = ceil_div(p.cols, V);   // 4096 at the most
+  if (p.cols < V) return go_rows(int8_norm_kernel<T, 1, 64, 1>, 256, 4, p, stream);
+  if (units <= 128) return go_rows(int8_norm_kernel<T, V, 64, 2>, 256, 4, p, stream);
+  if (units <= 256) return go_rows(int8_norm_kernel<T, V, 256, 1>, 256, 1, p, stream);
+  if (units <= 512) return go_rows(int8_norm_kernel<T, V, 256, 2>, 256, 1, p, stream);
+  if (units <= 1024) return go_rows(int8_norm_kernel<T, V, 512, 2>, 512, 1, p, stream);
+  if (V == 8 || units <= 2048) return go_rows(int8_norm_kernel<T, V, 1024, 2>, 1024, 1, p, stream);
+  return go_rows(int8_norm_kernel<float, 4, 1024, 4>, 1024, 1, p, stream);
 }
 
 hipError_t launch_int8_rows(const Int8Rows& p, hipStream_t stream) {
-  if (p.weight) return p.x_f32 ? launch_rows<float, true>(p, stream) : launch_rows<bf16_t, true>(p, stream);
-  return p.x_f32 ? launch_rows<float, false>(p, stream) : launch_rows<bf16_t, false>(p, stream);
+  if (p.weight) return p.x_f32 ? launch_norm<float>(p, stream) : launch_norm<bf16_t>(p, stream);
+  return p.x_f32 ? launch_rows<float>(p, stream) : launch_rows<bf16_t>(p, stream);
 }
 
 static constexpr int kFlatThreads = 256;
 
-// V codes to a thread.  Threads of a launch lie `step` apart, step_rows rows and step_units
-// pieces, so that only the first place takes a division.
+// V codes to a unit, 16 bytes of values.  Threads lie step_rows rows and step_units units apart,
+// so that only the first place takes a division.  (Four units at once to a thread: 61 -> 68 us for
+// 16384 x 7168 to bf16.  Stores past the caches, which leave the codes in them: 61 -> 52.)
 template <typename T, int V>
 __global__ void __launch_bounds__(kFlatThreads)
 int8_dequantize_kernel(int64_t num_rows, int64_t n, int64_t units, int64_t step_rows, int64_t step_units,
@@ -311,7 +368,7 @@ int8_dequantize_kernel(int64_t num_rows, int64_t n, int64_t units, int64_t step_
     load_floats<int8_t, V>(codes + at, v);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] *= s;
-    store_floats<T, V>(out + at, v);
+    store_floats<T, V, true>(out + at, v);
     row += step_rows;
     unit += step_units;
     if (unit >= units) {
@@ -333,8 +390,12 @@ hipError_t launch_int8_dequantize(bool out_f32, int64_t num_rows, int64_t cols, 
   };
   float* f = static_cast<float*>(out);
   bf16_t* b = static_cast<bf16_t*>(out);
-  if (cols < 8) return out_f32 ? go(int8_dequantize_kernel<float, 1>, f, 1) : go(int8_dequantize_kernel<bf16_t, 1>, b, 1);
-  return out_f32 ? go(int8_dequantize_kernel<float, 8>, f, 8) : go(int8_dequantize_kernel<bf16_t, 8>, b, 8);
+  if (out_f32) {
+    if (cols < 4) return go(int8_dequantize_kernel<float, 1>, f, 1);
+    return go(int8_dequantize_kernel<float, 4>, f, 4);
+  }
+  if (cols < 8) return go(int8_dequantize_kernel<bf16_t, 1>, b, 1);
+  return go(int8_dequantize_kernel<bf16_t, 8>, b, 8);
 }
 
 }  // namespace moelora

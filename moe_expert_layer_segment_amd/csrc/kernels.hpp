@@ -109,7 +109,7 @@ struct Int8Rows {
   // the norm (weight null: x is quantized as it is)
   const void* weight;                // [cols]
   const void* residual;              // [num_rows, cols] or null
-  double eps;
+  double eps, per_col;               // per_col: 1 / cols
   void* residual_out;                // null, or x + residual
   void* y;                           // null, or the norm
   int8_t* codes;                     // [num_rows, cols]
