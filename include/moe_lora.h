@@ -651,7 +651,8 @@ int moe_lora_int8_gemm(const moe_lora_int8_gemm_args* args, void* stream);
  *   token_mask  [num_tokens] bytes, 0 for tokens that take no part (padding; their logits and
  *               ids may be anything), or NULL: all do.
  *   loss [1], counts [num_experts] int32, mean_probs [num_experts], num_valid [1] int32 (n)  out.
- *   workspace   >= moe_lora_balance_loss_workspace_bytes(num_tokens, num_experts) bytes.
+ *   workspace   >= moe_lora_balance_loss_workspace_bytes(num_tokens, num_experts) bytes,
+ *               8-byte aligned; NULL where that is 0 (few tokens).
  * With n = 0 everything is 0.  Sums over tokens are fp64, in an order that does not change.
  *
  * moe_lora_balance_loss_backward: the gradient for the logits (counts are constants),

@@ -1111,18 +1111,19 @@ def _int8_pair(codes, scales, name, dev=None):
 
 def _int8_outputs(x, codes, scales, *inputs):
     """Codes and scales for x [.., K], made or checked."""
+    if codes is None and scales is None:
+        return (torch.empty_like(x, dtype=torch.int8),
+                x.new_empty(x.shape[:-1], dtype=torch.float32))
     shape, dev = tuple(x.shape), x.device
-    given = codes is not None or scales is not None
     if codes is None:
-        codes = torch.empty(shape, dtype=torch.int8, device=dev)
+        codes = torch.empty_like(x, dtype=torch.int8)
     if scales is None:
-        scales = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    if given:
-        _int8_pair(codes, scales, "the output", dev)
-        if codes.shape != shape:
-            raise ValueError(f"codes must be {shape}, got {tuple(codes.shape)}")
-        _apart(codes, x, scales, *inputs)
-        _apart(scales, x, *inputs)
+        scales = x.new_empty(shape[:-1], dtype=torch.float32)
+    _int8_pair(codes, scales, "the output", dev)
+    if codes.shape != shape:
+        raise ValueError(f"codes must be {shape}, got {tuple(codes.shape)}")
+    _apart(codes, x, scales, *inputs)
+    _apart(scales, x, *inputs)
     return codes, scales
 
 
@@ -1157,7 +1158,7 @@ def moe_lora_int8_dequantize(codes: torch.Tensor, scales: torch.Tensor,
     or ``out`` says float32)."""
     K = _int8_pair(codes, scales, "x")
     if out is None:
-        out = torch.empty(codes.shape, dtype=out_dtype or torch.bfloat16, device=codes.device)
+        out = torch.empty_like(codes, dtype=out_dtype or torch.bfloat16)
     else:
         _need(out, "out", out_dtype, codes.device)
         if out.shape != codes.shape:
@@ -1198,9 +1199,8 @@ def moe_lora_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float
         _need(residual, "residual", x.dtype, dev)
         if residual.shape != x.shape:
             raise ValueError(f"residual must be {tuple(x.shape)}, got {tuple(residual.shape)}")
-    for t in (x, weight, residual):
-        if t is not None and t.requires_grad:
-            _requires_grad("moe_lora_rms_norm_quantize")
+    if x.requires_grad or weight.requires_grad or (residual is not None and residual.requires_grad):
+        _requires_grad("moe_lora_rms_norm_quantize")
     codes, scales = _int8_outputs(x, codes, scales, weight, residual)
     if residual_out is not None:
         if residual is None:
@@ -1216,7 +1216,7 @@ def moe_lora_rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float
         residual_out = torch.empty_like(x)
     if y is None:
         if y_dtype is not None:
-            y = torch.empty(x.shape, dtype=y_dtype, device=dev)
+            y = torch.empty_like(x, dtype=y_dtype)
     else:
         _need(y, "y", y_dtype, dev)
         if y.shape != x.shape:
@@ -1371,29 +1371,31 @@ def moe_lora_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
     if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
         raise ValueError(f"topk_ids must be [{T}, k], got {tuple(topk_ids.shape)}")
     _token_mask(token_mask, T, dev)
-    shapes = dict(loss=(torch.float32, 1), counts=(torch.int32, E), mean_probs=(torch.float32, E),
-                  num_valid=(torch.int32, 1))
-    given = out is not None
-    stats = dict(out) if given else {}
-    for name, (dtype, n) in shapes.items():
-        if stats.get(name) is None:
-            stats[name] = torch.empty(n, dtype=dtype, device=dev)
-        elif stats[name].shape != (n,):
-            raise ValueError(f"{name} must be [{n}], got {tuple(stats[name].shape)}")
-        if given:
-            _need(stats[name], name, dtype, dev)
+    if out is None:
+        f, i = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
+        stats = dict(loss=torch.empty(1, **f), counts=torch.empty(E, **i),
+                     mean_probs=torch.empty(E, **f), num_valid=torch.empty(1, **i))
+    else:
+        stats = {}
+        for name, dtype, n in (("loss", torch.float32, 1), ("counts", torch.int32, E),
+                               ("mean_probs", torch.float32, E), ("num_valid", torch.int32, 1)):
+            t = out.get(name)
+            if t is None:
+                t = torch.empty(n, dtype=dtype, device=dev)
+            _need(t, name, dtype, dev)
+            if t.shape != (n,):
+                raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+            _apart(t, logits, topk_ids, token_mask, workspace, *stats.values())
+            stats[name] = t
     wsb = moe_lora_balance_loss_workspace_bytes(T, E)
     if workspace is None:
-        workspace = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
     else:
         _need(workspace, "workspace", torch.uint8, dev, wsb)
-    if given:
-        for name in shapes:
-            _apart(stats[name], logits, topk_ids, token_mask, workspace,
-                   *(stats[n] for n in shapes if n != name))
     _launch("moe_lora_balance_loss", dev, lib().moe_lora_balance_loss, T, E, topk_ids.shape[1], dt,
             _at(logits), _at(topk_ids), _at(token_mask), _at(stats["loss"]), _at(stats["counts"]),
-            _at(stats["mean_probs"]), _at(stats["num_valid"]), _at(workspace), workspace.numel())
+            _at(stats["mean_probs"]), _at(stats["num_valid"]), _at(workspace),
+            0 if workspace is None else workspace.numel())
     stats["top_k"] = topk_ids.shape[1]
     return stats
 

@@ -611,9 +611,9 @@ int moe_lora_balance_loss(int32_t num_tokens, int32_t num_experts, int32_t top_k
   if (!loss || !counts || !mean_probs || !num_valid || (num_tokens > 0 && (!logits || !topk_ids)) ||
       off_by_element(logits, dtype))
     return MOE_LORA_ERR_INVALID;
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 8 ||
-      workspace_bytes < balance_ws_bytes(num_tokens, num_experts))
-    return MOE_LORA_ERR_WORKSPACE;
+  const size_t need = balance_ws_bytes(num_tokens, num_experts);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_LORA_ERR_WORKSPACE;
+  if (need > 0 && reinterpret_cast<uintptr_t>(workspace) % 8) return MOE_LORA_ERR_INVALID;
   const Balance b = {num_tokens, num_experts, top_k, dtype == MOE_LORA_F32, logits, topk_ids, token_mask};
   return hip_status(launch_balance_loss(b, loss, counts, mean_probs, num_valid, workspace,
                                         static_cast<hipStream_t>(stream)));

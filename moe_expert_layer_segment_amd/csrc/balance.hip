@@ -47,7 +47,7 @@ static BalanceWs balance_ws(void* ws, int64_t E) {
   return w;
 }
 size_t balance_ws_bytes(int64_t T, int64_t E) {
-  return T <= kBalSingle ? 16 : (size_t)kBalBlocks * ((size_t)E * 12 + 4) + kFinishGroups * 8 + 8;
+  return T <= kBalSingle ? 0 : (size_t)kBalBlocks * ((size_t)E * 12 + 4) + kFinishGroups * 8 + 8;
 }
 
 // expert i of a lane

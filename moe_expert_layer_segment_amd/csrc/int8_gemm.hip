@@ -42,9 +42,16 @@ __device__ __forceinline__ float silu_near(float v) {
   const float t = -v * kLog2e;
   const float lo = __builtin_fmaf(-v, kRest, __builtin_fmaf(-v, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t);
-  // behind the range of e the correction would be infinity times lo
-  const float d = 1.0f + (e < 1e38f ? __builtin_fmaf(e, lo * kLn2, e) : e);
-  return v * __builtin_amdgcn_rcpf(d);
+  // (an infinite e stays one: times lo it would not)
+  return v * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(fminf(e, 1e38f), lo * kLn2, e));
+}
+
+// 4 outputs of SiLU(gate) * up
+__device__ __forceinline__ floatx4 silu_mul(floatx4 gate, floatx4 up) {
+  floatx4 v;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = silu_near(gate[q]) * up[q];
+  return v;
 }
 
 // first weight row of 16-column block cb; with silu_mul even blocks are gate
@@ -165,10 +172,7 @@ int8_stream_kernel(Int8Gemm p, int row_groups, int col_groups) {
       for (int nb = 0; nb < NB; nb += 2) {
         if ((mb * NB + nb) / 2 % WV != wave || cb0 + nb + 1 >= ncb || m >= p.M) continue;
         const floatx4 gate = total(mb, nb), up = total(mb, nb + 1);
-        floatx4 v;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = silu_near(gate[q]) * up[q];
-        store_out(p, m * (p.N / 2) + (cb0 + nb) / 2 * 16 + 4 * g, v);
+        store_out(p, m * (p.N / 2) + (cb0 + nb) / 2 * 16 + 4 * g, silu_mul(gate, up));
       }
     } else {
       for (int nb = 0; nb < NB; ++nb) {
@@ -251,14 +255,13 @@ __device__ __forceinline__ void dma16_m0(uint64_t base, uint32_t goff, uint32_t 
       "global_load_lds_dwordx4 %[go], %[gb]"
       :
       : [la] "s"(lds_addr), [go] "v"(goff), [gb] "s"(base)
-      : "memory", "m0");
+      : "memory");
 }
 
-// rows [m0, m0 + TM) of expert e, weight rows from 16 cb0 on; rows before m0 + skip are left to
-// another workgroup, rows from m0 + rows on do not exist
+// rows [m0, m0 + TM) of expert e, weight rows from 16 cb0 on; rows from m0 + rows on do not exist
 template <int TM>
 __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t m0, int64_t cb0,
-                                          int64_t e, int rows, int skip) {
+                                          int64_t e, int rows) {
   constexpr int WN = TM == 64 ? 4 : 2, WM = 4 / WN;             // waves over columns and rows
   constexpr int MB = TM / WM / 16, NB = kTileN / WN / 16;       // 16-row blocks of a wave
   constexpr int XSEG = TM / 8 / 4, WSEG = kTileN / 8 / 4;       // a wave's DMAs of 8 rows for a K tile
@@ -344,10 +347,10 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
   constexpr std::integral_constant<int, 0> first{};
   constexpr std::integral_constant<int, 1> second{};
   // The MFMAs of step H.  Between them, at an even pace, the fragments of the other step are read
-  // from `place` (read), and DMAs go out (send).
+  // from `place`, and DMAs go out (send).
   constexpr int SLOTS = MB * NB, READS = MB + NB;
   static_assert(READS <= SLOTS && DMAS <= SLOTS, "a slot behind each MFMA");
-  auto step = [&](auto H, int place, auto read, auto&& send) {
+  auto step = [&](auto H, int place, auto&& send) {
     constexpr int h = decltype(H)::value;
     std::integral_constant<int, 1 - h> other;
     static_for<SLOTS>([&](auto S) {
@@ -355,7 +358,7 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
       mfma_in_place(acc[i][j], wf[h][j], xf[h][i]);
       // the n-th of READS lies behind MFMA n SLOTS / READS; those of the weights come first
       constexpr int n = (s * READS + SLOTS - 1) / SLOTS;
-      if constexpr (decltype(read)::value && n < READS && n * SLOTS / READS == s) {
+      if constexpr (n < READS && n * SLOTS / READS == s) {
         if constexpr (n < NB) read_w(place, other, std::integral_constant<int, n < NB ? n : 0>{});
         else read_x(place, other, std::integral_constant<int, n < NB ? 0 : n - NB>{});
       }
@@ -363,7 +366,6 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  auto nothing = [](auto) {};
 
   static_for<DMAS>([&](auto D) {
     if (decltype(D)::value == 0 && tiles == 1) last_tile();
@@ -394,13 +396,13 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
 #pragma unroll 1
   for (int t = 0; t < tiles; ++t, place ^= 1) {
     if (t + 1 == tiles) cut(first);
-    step(first, place, std::true_type{}, nothing);
+    step(first, place, [](auto) {});
     wait_all_barrier();
     if (t + 1 == tiles) cut(second);
     if (t + 3 == tiles) last_tile();
     const Bases at = bases_of(t + 2);
     const bool sends = t + 2 < tiles;
-    step(second, place ^ 1, std::true_type{}, [&](auto S) {
+    step(second, place ^ 1, [&](auto S) {
       constexpr int s = decltype(S)::value, d = (s * DMAS + SLOTS - 1) / SLOTS;
       if constexpr (d < DMAS && d * SLOTS / DMAS == s) {
         if (sends) issue(at, place, d);
@@ -442,7 +444,7 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
     const int row = (wm * MB + i) * 16 + r;
-    if (row >= rows || row < skip) continue;
+    if (row >= rows) continue;
     const bool holds = live >> i & 1;
     const int64_t at = (m0 + row) * out_cols + col0;
     auto y = [&](int j) {
@@ -456,14 +458,7 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
       for (int j = 0; j < NB; j += 4) {
         const int col = (wn * NB + j) * 8 + 8 * g;
         if (col0 + col >= out_cols) continue;
-        floatx4 v[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const floatx4 gate = y(j + 2 * h), up = y(j + 2 * h + 1);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[h][q] = silu_near(gate[q]) * up[q];
-        }
-        store_out(p, at + col, v[0], v[1]);
+        store_out(p, at + col, silu_mul(y(j), y(j + 1)), silu_mul(y(j + 2), y(j + 3)));
       }
     } else {
 #pragma unroll
@@ -544,9 +539,9 @@ __global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_til
   for (int row = done + threadIdx.x / 64; row < rows; row += 4)
     if (lane * 4 < width) store_out(p, (m0 + row) * cols + col0 + lane * 4, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
   const int some = min(rows, done);
-  if (TOP == 256 && done == 256) int8_tile<TOP>(p, lds, m0, cb0, e, some, 0);
-  else if (TOP >= 128 && done == 128) int8_tile<TOP >= 128 ? 128 : 64>(p, lds, m0, cb0, e, some, 0);
-  else if (done == 64) int8_tile<64>(p, lds, m0, cb0, e, some, 0);
+  if (TOP == 256 && done == 256) int8_tile<TOP>(p, lds, m0, cb0, e, some);
+  else if (TOP >= 128 && done == 128) int8_tile<TOP >= 128 ? 128 : 64>(p, lds, m0, cb0, e, some);
+  else if (done == 64) int8_tile<64>(p, lds, m0, cb0, e, some);
 }
 
 template <int TM>
