@@ -1155,8 +1155,11 @@ def moe_lora_int8_quantize(x: torch.Tensor, num_rows_used: Optional[torch.Tensor
 def moe_lora_int8_dequantize(codes: torch.Tensor, scales: torch.Tensor,
                              out: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
     """The values [.., K] that codes and scales stand for (bfloat16 unless ``out_dtype``
-    or ``out`` says float32)."""
+    or ``out`` says float32).  There is no gradient: scales that require one are refused
+    where autograd is on."""
     K = _int8_pair(codes, scales, "x")
+    if scales.requires_grad:
+        _requires_grad("moe_lora_int8_dequantize")
     if out is None:
         out = torch.empty_like(codes, dtype=out_dtype or torch.bfloat16)
     else:
@@ -1241,9 +1244,12 @@ def moe_lora_int8_gemm(x: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.T
     the tokens lie, each of which is read for its ``top_k`` pairs.  Rows behind the last used
     tile are left as they are in ``out`` (undefined when it is not given).  With ``pair_rows``
     in align_out, and with ``top_k``, padding rows get zeros, whatever x and the weights hold.
-    ``out`` / ``out_dtype``: bfloat16 (the default) or float32.  There is no gradient."""
+    ``out`` / ``out_dtype``: bfloat16 (the default) or float32.  There is no gradient: scales that
+    require one are refused where autograd is on."""
     K = _int8_pair(w_codes, w_scales, "w")
     dev = w_codes.device
+    if w_scales.requires_grad or x_scales.requires_grad:
+        _requires_grad("moe_lora_int8_gemm")
     if w_codes.dim() != (2 if align_out is None else 3):
         raise ValueError("w_codes must be [N, K], or [E, N, K] with align_out")
     E, N = (1 if align_out is None else w_codes.shape[0]), w_codes.shape[-2]
@@ -1392,6 +1398,7 @@ def moe_lora_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
         workspace = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
     else:
         _need(workspace, "workspace", torch.uint8, dev, wsb)
+        _apart(workspace, logits, topk_ids, token_mask)
     _launch("moe_lora_balance_loss", dev, lib().moe_lora_balance_loss, T, E, topk_ids.shape[1], dt,
             _at(logits), _at(topk_ids), _at(token_mask), _at(stats["loss"]), _at(stats["counts"]),
             _at(stats["mean_probs"]), _at(stats["num_valid"]), _at(workspace),

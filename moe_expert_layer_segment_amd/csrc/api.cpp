@@ -574,7 +574,8 @@ int moe_lora_int8_gemm(const moe_lora_int8_gemm_args* a, void* stream) {
       return MOE_LORA_ERR_UNSUPPORTED;
   }
   if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->out || misaligned(a->x) ||
-      misaligned(a->w) || misaligned(a->out) || off_by_word(a->x_scale) || off_by_word(a->w_scale))
+      misaligned(a->w) || misaligned(a->out) || off_by_word(a->x_scale) || off_by_word(a->w_scale) ||
+      off_by_word(a->tile_expert) || off_by_word(a->sorted_pair_ids))
     return MOE_LORA_ERR_INVALID;
   Int8Gemm p;
   p.M = a->num_rows; p.N = a->out_features; p.K = a->in_features; p.E = a->num_experts;
@@ -609,7 +610,8 @@ int moe_lora_balance_loss(int32_t num_tokens, int32_t num_experts, int32_t top_k
   const int st = balance_shape(num_tokens, num_experts, top_k, dtype);
   if (st != MOE_LORA_OK) return st;
   if (!loss || !counts || !mean_probs || !num_valid || (num_tokens > 0 && (!logits || !topk_ids)) ||
-      off_by_element(logits, dtype))
+      off_by_element(logits, dtype) || off_by_word(topk_ids) || off_by_word(loss) || off_by_word(counts) ||
+      off_by_word(mean_probs) || off_by_word(num_valid))
     return MOE_LORA_ERR_INVALID;
   const size_t need = balance_ws_bytes(num_tokens, num_experts);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_LORA_ERR_WORKSPACE;
@@ -629,7 +631,7 @@ int moe_lora_balance_loss_backward(int32_t num_tokens, int32_t num_experts, int3
   if (!float_dtype(out_dtype)) return MOE_LORA_ERR_UNSUPPORTED;
   if (num_tokens == 0) return MOE_LORA_OK;
   if (!logits || !counts || !num_valid || !d_logits || off_by_element(logits, dtype) ||
-      off_by_element(d_logits, out_dtype))
+      off_by_element(d_logits, out_dtype) || off_by_word(counts) || off_by_word(num_valid) || off_by_word(d_loss))
     return MOE_LORA_ERR_INVALID;
   const Balance b = {num_tokens, num_experts, top_k, dtype == MOE_LORA_F32, logits, nullptr, token_mask};
   return hip_status(launch_balance_loss_backward(b, out_dtype == MOE_LORA_F32, counts, num_valid,

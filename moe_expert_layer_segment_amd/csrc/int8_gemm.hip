@@ -237,7 +237,7 @@ constexpr int tile_lds(int tm) { return 2 * (tm + kTileN) * kStep; }
 __device__ __forceinline__ void mfma_in_place(int4v& c, int4v a, int4v b) {
   asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
-__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 2" ::: "memory"); }
 
 // a uniform address, in scalar registers
 __device__ __forceinline__ uint64_t uniform_address(const void* p) {
@@ -408,9 +408,10 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
         if (sends) issue(at, place, d);
       }
     });
+    // the last products are done before what follows reads them: here, since the compiler may move
+    // the sums as soon as the loop ends
+    settle();
   }
-  // the last products are done before what follows reads them
-  settle();
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
