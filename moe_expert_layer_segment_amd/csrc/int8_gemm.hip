@@ -258,10 +258,12 @@ __device__ __forceinline__ void dma16_m0(uint64_t base, uint32_t goff, uint32_t 
       : "memory");
 }
 
-// rows [m0, m0 + TM) of expert e, weight rows from 16 cb0 on; rows from m0 + rows on do not exist
+// rows [m0, m0 + TM) of expert e, weight rows from 16 cb0 on; rows from m0 + rows on do not exist.
+// ids: with row_ids, those of rows lane, 64 + lane, ...
+struct Ids { int32_t a, b, c, d; };
 template <int TM>
 __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t m0, int64_t cb0,
-                                          int64_t e, int rows) {
+                                          int64_t e, int rows, Ids ids) {
   constexpr int WN = TM == 64 ? 4 : 2, WM = 4 / WN;             // waves over columns and rows
   constexpr int MB = TM / WM / 16, NB = kTileN / WN / 16;       // 16-row blocks of a wave
   constexpr int XSEG = TM / 8 / 4, WSEG = kTileN / 8 / 4;       // a wave's DMAs of 8 rows for a K tile
@@ -284,6 +286,10 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
     return min(col, out_cols - 1 - col0);
   };
   auto is_up = [&](int n) { return p.silu_mul && n / 16 % 2; };
+  const int32_t id0 = ids.a, id1 = ids.b, id2 = ids.c, id3 = ids.d;
+  auto ids_of = [=](int q) { return q == 0 ? id0 : q == 1 ? id1 : q == 2 ? id2 : id3; };
+  // what the others read instead is not used
+  auto token_of = [&](int32_t id) -> int64_t { return id >= 0 && id < p.num_ids ? (uint32_t)id / (uint32_t)p.top_k : 0; };
 
   // This lane's row in each of its DMAs: 8 rows of 128 bytes, lane l the chunk at place l % 8 of
   // row l / 8.  Offsets are 32 bits, of x from its start (where the rows of a pair's tokens lie
@@ -299,11 +305,19 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
   for (int i = 0; i < DMAS; ++i) {
     const int row = lds_row(i) + lane / 8;
     int64_t src = i < XSEG ? min(row, rows - 1) : w_col(row);
-    if (i < XSEG && p.top_k > 0) {
-      const int32_t id = p.row_ids[m0 + src];
-      src = id >= 0 && id < p.num_ids ? (uint32_t)id / (uint32_t)p.top_k : 0;
-    }
+    if (i < XSEG && p.top_k > 0) src = token_of(__builtin_amdgcn_ds_bpermute(4 * (row % 64), ids_of(wave * TM / 256)));
     off[i] = (uint32_t)(src * p.K);
+  }
+  // scale of row threadIdx.x (and whether it holds a pair) and of column threadIdx.x: they arrive
+  // while the products are made
+  float own_xs = 0.0f, own_ws;
+  uint32_t own_holds = 1;
+  {
+    const int row = min((int)threadIdx.x, rows - 1), id = ids_of(min(wave, TM / 64 - 1));
+    if (p.row_ids) own_holds = id >= 0 && id < p.num_ids;
+    if ((int)threadIdx.x < TM) own_xs = p.x_scale[p.top_k > 0 ? token_of(id) : m0 + row];
+    const int n = threadIdx.x;
+    own_ws = p.w_scale[e * p.N + col0 + w_col(n) + (is_up(n) ? out_cols : 0)];
   }
   // its chunk of a K tile, in even and in odd segments
   const uint32_t chunk[2] = {(uint32_t)((lane % 8) ^ swz(lane / 8)) * 16, (uint32_t)((lane % 8) ^ swz(8 + lane / 8)) * 16};
@@ -417,30 +431,24 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
 #pragma unroll
     for (int j = 0; j < NB; ++j) asm volatile("" : "+a"(acc[i][j]));
 
-  // the scales of this lane's rows and columns
+  // the scales go through LDS, where what is still read ahead there is not used
+  struct Row { float scale; uint32_t holds; };
+  Row* const row_lds = reinterpret_cast<Row*>(lds);
+  float* const col_lds = reinterpret_cast<float*>(lds + TM * sizeof(Row));
+  if ((int)threadIdx.x < TM) row_lds[threadIdx.x] = Row{own_xs, own_holds};
+  col_lds[threadIdx.x] = own_ws;
+  __syncthreads();
   float xs[MB];
   floatx4 ws[NB];
   uint32_t live = 0;
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
-    const int row = min((wm * MB + i) * 16 + r, rows - 1);
-    int64_t src = m0 + row;
-    bool holds = true;
-    if (p.row_ids) {
-      const int32_t id = p.row_ids[m0 + row];
-      holds = id >= 0 && id < p.num_ids;
-      if (p.top_k > 0) src = holds ? (uint32_t)id / (uint32_t)p.top_k : 0;
-    }
-    live |= (uint32_t)holds << i;
-    xs[i] = p.x_scale[src];
+    const Row row = row_lds[(wm * MB + i) * 16 + r];
+    live |= row.holds << i;
+    xs[i] = row.scale;
   }
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int n = (wn * NB + j) * 16 + 4 * g;   // 4 columns from there on; N is a multiple of 16
-    const float* at = p.w_scale + e * p.N + col0 + min(w_col(n), out_cols - 4 - col0) + (is_up(n) ? out_cols : 0);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) ws[j][q] = at[q];
-  }
+  for (int j = 0; j < NB; ++j) ws[j] = *reinterpret_cast<const floatx4*>(col_lds + (wn * NB + j) * 16 + 4 * g);
 
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
@@ -524,25 +532,27 @@ __global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_til
   const int rows = (int)min((int64_t)span, p.M - m0);
   if (rows <= 0) return;
   int live = rows;   // up to the last row that holds a pair
+  Ids ids = {};
   if (p.row_ids) {
     live = 0;
-    for (int r0 = (rows - 1) / 64 * 64; r0 >= 0 && live == 0; r0 -= 64) {
-      const int32_t id = p.row_ids[m0 + min(r0 + lane, rows - 1)];
-      const uint64_t has = __ballot(r0 + lane < rows && id >= 0 && id < p.num_ids);
-      if (has) live = r0 + 64 - __clzll(has);
-    }
+    auto id_at = [&](int q) { return 64 * q < TOP ? p.row_ids[m0 + min(q * 64 + lane, rows - 1)] : -1; };
+    ids = {id_at(0), id_at(1), id_at(2), id_at(3)};
+    auto look = [&](int q, int32_t id) {
+      const uint64_t has = __ballot(q * 64 + lane < rows && id >= 0 && id < p.num_ids);
+      live = has ? q * 64 + 64 - __clzll(has) : live;
+    };
+    look(0, ids.a), look(1, ids.b), look(2, ids.c), look(3, ids.d);
     live = __builtin_amdgcn_readfirstlane(live);
   }
+  const int done = live > 128 ? 256 : live > 64 ? 128 : live > 0 ? 64 : 0, some = min(rows, done);
+  if (TOP == 256 && done == 256) int8_tile<TOP>(p, lds, m0, cb0, e, some, ids);
+  else if (TOP >= 128 && done == 128) int8_tile<TOP >= 128 ? 128 : 64>(p, lds, m0, cb0, e, some, ids);
+  else if (done == 64) int8_tile<64>(p, lds, m0, cb0, e, some, ids);
   // the rows behind the tile that these take hold no pair
-  const int done = live > 128 ? 256 : live > 64 ? 128 : live > 0 ? 64 : 0;
   const int cols = (int)(p.silu_mul ? p.N / 2 : p.N), col0 = (int)cb0 * (p.silu_mul ? 8 : 16);
   const int width = min(p.silu_mul ? kTileN / 2 : kTileN, cols - col0);
   for (int row = done + threadIdx.x / 64; row < rows; row += 4)
     if (lane * 4 < width) store_out(p, (m0 + row) * cols + col0 + lane * 4, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
-  const int some = min(rows, done);
-  if (TOP == 256 && done == 256) int8_tile<TOP>(p, lds, m0, cb0, e, some);
-  else if (TOP >= 128 && done == 128) int8_tile<TOP >= 128 ? 128 : 64>(p, lds, m0, cb0, e, some);
-  else if (done == 64) int8_tile<64>(p, lds, m0, cb0, e, some);
 }
 
 template <int TM>
