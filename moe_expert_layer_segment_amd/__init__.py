@@ -6,6 +6,7 @@ The compute runs in hand-written HIP kernels behind a C ABI
 """
 from .binding import (  # noqa: F401
     compute_moe_lora_info,
+    int8_block_m,
     moe_lora_align,
     moe_lora_align_capacity_rows,
     moe_lora_align_workspace_bytes,

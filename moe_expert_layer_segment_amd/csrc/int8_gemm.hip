@@ -480,24 +480,27 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
   }
 }
 
+// Tiles are numbered in bands of kBand rows of them, in patches of kBand x kPatch.  The XCD that
+// workgroup b runs on, b % 8, takes 32 neighbours in that order at a time (one for each of its CUs),
+// which share rows and weights in its L2.  Workgroups without a tile are the last ones alone: with
+// those that the patches at the edges lack left empty, XCDs got unequal shares (65536 x 1536 x
+// 2048 of 128 experts 403 us, so 320), and so did the parts of an XCD that consecutive workgroups
+// go round (512 x 28672 x 4096, two tiles high, 113 us, so 65).  For the latter the tiles of a
+// patch are numbered along its rows, too: rows differ in how many of them hold a pair.
+//
 // Workgroups of the last, incomplete round of 256 (one to a CU) take a half or a quarter of a
 // tile's rows each, where that fills the round no more than once; a workgroup whose rows end
 // early with padding takes a smaller tile.
-//
-// Patches of (32 / pn) x pn tiles go round the eight XCDs (workgroup b runs on XCD b % 8), so
-// the 32 workgroups that an XCD holds share rows and weights in its L2.
-constexpr int kRound = 256;
+constexpr int kRound = 256, kBand = 4, kPatch = 8;
 constexpr int64_t kTailTiles = 16 * kRound;   // with more, a share of a round does not count
 
 // per_entry: tiles of an entry of tile_expert (three of 64 rows for block_m = 192)
 template <int TOP>
-__global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_tiles, int n_tiles, int pn,
-                                                           int n_patches, int per_entry, int tail) {
+__global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_tiles, int n_tiles, int per_entry,
+                                                           int tail) {
   __shared__ __attribute__((aligned(1024))) char lds[tile_lds(TOP)];
   const int lane = threadIdx.x & 63;
-  const int pm = 32 / pn;
-  int patch = (int)(blockIdx.x / 256) * 8 + (int)(blockIdx.x % 8);
-  const int in = (int)(blockIdx.x / 8) % 32;
+  uint32_t tile = blockIdx.x / 256 * 256 + blockIdx.x % 8 * 32 + blockIdx.x / 8 % 32;
   int used = m_tiles, whole = m_tiles, pieces = 1;   // tiles with rows; those taken whole
   if (tail) {
     if (p.tile_expert) {
@@ -510,17 +513,21 @@ __global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_til
       }
       used = __builtin_amdgcn_readfirstlane(used);
     }
-    whole = used * n_tiles / kRound * kRound / n_tiles / pm * pm;
+    whole = used * n_tiles / kRound * kRound / n_tiles;
     const int rest = (used - whole) * n_tiles;
     if (TOP == 256 && 4 * rest <= kRound) pieces = 4;
     else if (TOP >= 128 && 2 * rest <= kRound) pieces = 2;
     else whole = used;
   }
-  const int whole_patches = (whole + pm - 1) / pm * n_patches;
-  const bool part = patch >= whole_patches;
-  if (part) patch -= whole_patches;
-  const int mt = patch / n_patches * pm + in % pm, nt = patch % n_patches * pn + in / pm;
-  if (nt >= n_tiles || mt >= (part ? (used - whole) * pieces : whole)) return;
+  const bool part = tile >= (uint32_t)(whole * n_tiles);
+  if (part) tile -= (uint32_t)(whole * n_tiles);
+  const uint32_t down = part ? (used - whole) * pieces : whole;
+  if (tile >= down * n_tiles) return;
+  const uint32_t band = tile / (kBand * n_tiles), high = min((uint32_t)kBand, down - band * kBand);
+  tile -= band * kBand * n_tiles;
+  const uint32_t patch = tile / (high * kPatch), wide = min((uint32_t)kPatch, n_tiles - patch * kPatch);
+  tile -= patch * high * kPatch;
+  const int mt = band * kBand + tile / wide, nt = patch * kPatch + tile % wide;
   const int span = part ? TOP / pieces : TOP;
   const int64_t m0 = part ? (int64_t)whole * TOP + (int64_t)mt * span : (int64_t)mt * TOP;
   const int64_t cb0 = (int64_t)nt * (kTileN / 16);
@@ -558,16 +565,11 @@ __global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_til
 template <int TM>
 static hipError_t tiled(const Int8Gemm& p, hipStream_t stream) {
   const int64_t m_tiles = ceil_div(p.M, TM), n_tiles = ceil_div(p.N, kTileN);
-  int pn = 8;
-  while (pn > n_tiles) pn /= 2;
-  const int64_t n_patches = ceil_div(n_tiles, pn);
   const bool tail = m_tiles * n_tiles <= kTailTiles;
-  // parts of tiles fill a round at most: 16 patches, and one more for each part of the
-  // columns in which their rows end
-  const int64_t patches = ceil_div(m_tiles, 32 / pn) * n_patches + (tail ? 16 + 2 * n_patches : 0);
-  hipLaunchKernelGGL(int8_tile_kernel<TM>, dim3((unsigned)(ceil_div(patches, 8) * 256)), dim3(256), 0, stream, p,
-                     (int)m_tiles, (int)n_tiles, pn, (int)n_patches,
-                     (int)(p.tile_expert ? p.BM / TM : 1), (int)tail);
+  // where the last tiles are parted, a round of parts takes their place
+  const int64_t blocks = std::max(m_tiles * n_tiles, tail ? (m_tiles - 1) * n_tiles + kRound : 0);
+  hipLaunchKernelGGL(int8_tile_kernel<TM>, dim3((unsigned)(ceil_div(blocks, kRound) * kRound)), dim3(256), 0, stream, p,
+                     (int)m_tiles, (int)n_tiles, (int)(p.tile_expert ? p.BM / TM : 1), (int)tail);
   return hipGetLastError();
 }
 
@@ -580,14 +582,27 @@ static hipError_t few(const Int8Gemm& p, hipStream_t s) {
   return stream<MB, 1, WIDE>(p, s);
 }
 
+// Workgroups of 64 rows, two to a CU, hide each other's beginning and end, those of 256 read less
+// for each product.  16384 x 4096 x 256 51 us by 64 rows, 56 by 256; x 512 67 and 68; x 768 82
+// and 80, x 2048 167 and 140.  384 x 20480 x 7168, 160 tiles of 256 rows: 67 and 97.
+constexpr int64_t kShortK = 512;
+// In blocks of 128 rows, by 64 rows and by 128: 65536 rows of 128 experts x 1536 x 2048 357 and 370
+// us, 8192 of 32 x 8192 x 4096 486 and 511, x 4096 x 7168 475 and 447.
+constexpr int64_t kLongK = 4096;
+
 hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t s) {
   // rows of a workgroup: within one tile_expert entry, or those there are
   const int64_t rows = p.tile_expert ? p.BM : p.M;
   auto takes = [&](int64_t n) { return p.tile_expert ? rows % n == 0 : rows > n / 2; };
   if (takes(64)) {
-    if (ceil_div(p.M, 64) * ceil_div(p.N, kTileN) <= 64) return stream<4, 2, 4>(p, s);
-    if (takes(256)) return tiled<256>(p, s);
-    if (takes(128)) return tiled<128>(p, s);
+    const int64_t n_tiles = ceil_div(p.N, kTileN), of64 = ceil_div(p.M, 64) * n_tiles;
+    if (of64 <= 64) return stream<4, 2, 4>(p, s);
+    // one round of pairs of 64 rows, where those of 256 would be more than half a round, not parted
+    const bool pairs = !p.tile_expert && of64 <= 2 * kRound && 2 * ceil_div(p.M, 256) * n_tiles > kRound;
+    if (p.K > kShortK && !pairs) {
+      if (takes(256)) return tiled<256>(p, s);
+      if (p.K > kLongK && takes(128)) return tiled<128>(p, s);
+    }
     return tiled<64>(p, s);
   }
   if (takes(32)) return stream<2, 4, 4>(p, s);

@@ -338,12 +338,13 @@ MANY = [  # block_m, tiles in use and behind them, N: past 256 workgroups
     (32, 40, 1, 1056)]
 
 
+@pytest.mark.parametrize("K", [208, 528])      # tiles of 64 rows, and those that block_m takes
 @pytest.mark.parametrize("case", MANY, ids=lambda c: f"b{c[0]}t{c[1]}N{c[3]}")
-def test_many_tiles(case):
+def test_many_tiles(case, K):
     """Row tiles with any number of rows in use, with gaps; the others give zeros."""
     bm, tiles, behind, N = case
-    E, K, M = 3, 208, bm * (tiles + behind)
-    say(f"many tiles {case}")
+    E, M = 3, bm * (tiles + behind)
+    say(f"many tiles {case} {K}")
     g = torch.Generator().manual_seed(18)
     experts = torch.cat((torch.randint(0, E, (tiles,), generator=g), torch.full((behind,), -1)))
     fill = torch.randint(0, bm + 1, (tiles + behind,), generator=g)

@@ -368,6 +368,14 @@ def test_what_a_product_is_called_with(recorder):
     assert a.tile_expert is None and (a.num_rows, a.num_experts, a.block_m) == (7, 1, 0)
 
 
+def test_block_m_rule():
+    assert [binding.int8_block_m(*a) for a in ((64, 8, 128), (64, 8, 32), (64, 8, 16), (16384, 1, 32))] == \
+        [16, 32, 64, 256]
+    for T in (0, 1, 100, 10000):
+        for E in (1, 8, 256):
+            assert binding.int8_block_m(T, 2, E) in (16, 32, 64, 256)
+
+
 # ---------------------------------------------------------------------------
 # the oracle
 # ---------------------------------------------------------------------------
