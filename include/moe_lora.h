@@ -613,7 +613,7 @@ int moe_lora_rms_norm_quantize(int64_t num_tokens, int32_t hidden, int32_t dtype
  * order, and out rounds once more to its type.  A row's result depends on that row alone.
  * block_m as for moe_lora_mx4_gemm.  in_features: a multiple of 16, at most 131056 (2^17 -
  * 16); out_features: a multiple of 16 (32 with silu_mul), at most 2^24; num_rows / 16 *
- * out_features / 64 < 2^24 (else MOE_LORA_ERR_UNSUPPORTED).  x, w and out 16-byte aligned.
+ * out_features / 64 <= 2^24 - 256 (else MOE_LORA_ERR_UNSUPPORTED).  x, w and out 16-byte aligned.
  * No workspace.
  */
 typedef struct moe_lora_int8_gemm_args {

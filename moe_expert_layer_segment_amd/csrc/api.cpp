@@ -561,8 +561,9 @@ int moe_lora_int8_gemm(const moe_lora_int8_gemm_args* a, void* stream) {
     return MOE_LORA_ERR_INVALID;   // rows of several experts need their tiles
   }
   if (a->sorted_pair_ids && (!a->tile_expert || a->num_pairs < 0)) return MOE_LORA_ERR_INVALID;
-  // threads of one launch are counted in 32 bits: 256 to 16 rows x 64 columns at the least
-  if ((a->num_rows + 15) / 16 * ((a->out_features + 63) / 64) >= (int64_t(1) << 24))
+  // threads of one launch are counted in 32 bits: 256 to 16 rows x 64 columns at the least, in
+  // rounds of 256 workgroups
+  if ((a->num_rows + 15) / 16 * ((a->out_features + 63) / 64) > (int64_t(1) << 24) - 256)
     return MOE_LORA_ERR_UNSUPPORTED;
   if (a->num_rows == 0) return MOE_LORA_OK;
   if (a->top_k > 0) {

@@ -494,12 +494,16 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
 constexpr int kRound = 256, kBand = 4, kPatch = 8;
 constexpr int64_t kTailTiles = 16 * kRound;   // with more, a share of a round does not count
 
-// per_entry: tiles of an entry of tile_expert (three of 64 rows for block_m = 192)
+// An entry of tile_expert holds several tiles (for block_m = 80 one of 64 rows and one of 16), or
+// (entries of 16, 32 or 48 rows: these are the m_tiles, then) a tile takes as many neighbours of
+// one expert as it has room for, from the expert's first on; the workgroups of the others have
+// nothing to do.
 template <int TOP>
-__global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_tiles, int n_tiles, int per_entry,
-                                                           int tail) {
+__global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_tiles, int n_tiles, int tail) {
   __shared__ __attribute__((aligned(1024))) char lds[tile_lds(TOP)];
   const int lane = threadIdx.x & 63;
+  const bool small = TOP == 64 && p.tile_expert && p.BM < TOP;
+  const uint32_t per_entry = p.tile_expert ? ((uint32_t)p.BM + TOP - 1) / TOP : 1;
   uint32_t tile = blockIdx.x / 256 * 256 + blockIdx.x % 8 * 32 + blockIdx.x / 8 % 32;
   int used = m_tiles, whole = m_tiles, pieces = 1;   // tiles with rows; those taken whole
   if (tail) {
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_til
       used = 0;   // from the end, where the entries without an expert are
       for (int t0 = (m_tiles - 1) / 64 * 64; t0 >= 0 && used == 0; t0 -= 64) {
         const int t = t0 + lane;
-        const int te = t < m_tiles ? p.tile_expert[(uint32_t)t / (uint32_t)per_entry] : -1;
+        const int te = t < m_tiles ? p.tile_expert[(uint32_t)t / per_entry] : -1;
         const uint64_t has = __ballot(te >= 0 && te < p.E);
         if (has) used = t0 + 64 - __clzll(has);
       }
@@ -529,14 +533,33 @@ __global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_til
   tile -= patch * high * kPatch;
   const int mt = band * kBand + tile / wide, nt = patch * kPatch + tile % wide;
   const int span = part ? TOP / pieces : TOP;
-  const int64_t m0 = part ? (int64_t)whole * TOP + (int64_t)mt * span : (int64_t)mt * TOP;
+  int64_t m0 = (int64_t)(part ? whole : mt) * TOP + (part ? mt * span : 0);
+  int rows = (int)min((int64_t)span, p.M - m0);
   const int64_t cb0 = (int64_t)nt * (kTileN / 16);
   int64_t e = 0;
   if (p.tile_expert) {
-    e = __builtin_amdgcn_readfirstlane(p.tile_expert[(uint32_t)(part ? whole + mt / pieces : mt) / (uint32_t)per_entry]);
+    const uint32_t entry = (uint32_t)(part ? whole + mt / pieces : mt) / per_entry;
+    e = __builtin_amdgcn_readfirstlane(p.tile_expert[entry]);
     if (e < 0 || e >= p.E) return;
+    if (TOP == 64) {
+      const int in_entry = (mt - (int)(entry * per_entry)) * TOP;
+      m0 = (int64_t)entry * p.BM + in_entry;
+      rows = min((int)p.BM - in_entry, TOP);
+    }
   }
-  const int rows = (int)min((int64_t)span, p.M - m0);
+  if (small) {
+    int before = 0;   // entries of this expert
+    for (int at = mt - 1; at >= 0; at -= 64) {
+      const uint64_t other = __ballot(at < lane || p.tile_expert[max(at - lane, 0)] != e);
+      before += other ? __ffsll((unsigned long long)other) - 1 : 64;
+      if (other) break;
+    }
+    const int room = TOP / (int)p.BM;
+    if (before % room) return;
+    int entries = 1;
+    while (entries < room && mt + entries < m_tiles && p.tile_expert[mt + entries] == e) ++entries;
+    rows = __builtin_amdgcn_readfirstlane(entries) * (int)p.BM;
+  }
   if (rows <= 0) return;
   int live = rows;   // up to the last row that holds a pair
   Ids ids = {};
@@ -564,12 +587,13 @@ __global__ void __launch_bounds__(256, 1) int8_tile_kernel(Int8Gemm p, int m_til
 
 template <int TM>
 static hipError_t tiled(const Int8Gemm& p, hipStream_t stream) {
-  const int64_t m_tiles = ceil_div(p.M, TM), n_tiles = ceil_div(p.N, kTileN);
+  const int64_t m_tiles = p.tile_expert ? p.M / p.BM * ceil_div(p.BM, TM) : ceil_div(p.M, TM);
+  const int64_t n_tiles = ceil_div(p.N, kTileN);
   const bool tail = m_tiles * n_tiles <= kTailTiles;
   // where the last tiles are parted, a round of parts takes their place
   const int64_t blocks = std::max(m_tiles * n_tiles, tail ? (m_tiles - 1) * n_tiles + kRound : 0);
   hipLaunchKernelGGL(int8_tile_kernel<TM>, dim3((unsigned)(ceil_div(blocks, kRound) * kRound)), dim3(256), 0, stream, p,
-                     (int)m_tiles, (int)n_tiles, (int)(p.tile_expert ? p.BM / TM : 1), (int)tail);
+                     (int)m_tiles, (int)n_tiles, (int)tail);
   return hipGetLastError();
 }
 
@@ -590,13 +614,21 @@ constexpr int64_t kShortK = 512;
 // us, 8192 of 32 x 8192 x 4096 486 and 511, x 4096 x 7168 475 and 447.
 constexpr int64_t kLongK = 4096;
 
+// In blocks of 16 and of 32 rows, with that many rows an expert, weights are streamed for each block;
+// with more, a tile takes 64 rows of an expert.  A layer of 32 experts of 4096 x 2048, streamed and by
+// tiles: 12 rows an expert 217 and 265 us in blocks of 16 rows, 215 and 230 in blocks of 32; 24 rows
+// 301 and 250, 242 and 274; 32 rows 355 and 270, 286 and 278; 64 rows 567 and 271, 408 and 275.
+constexpr int64_t kFewRows = 20;
+
 hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t s) {
   // rows of a workgroup: within one tile_expert entry, or those there are
   const int64_t rows = p.tile_expert ? p.BM : p.M;
   auto takes = [&](int64_t n) { return p.tile_expert ? rows % n == 0 : rows > n / 2; };
-  if (takes(64)) {
-    const int64_t n_tiles = ceil_div(p.N, kTileN), of64 = ceil_div(p.M, 64) * n_tiles;
-    if (of64 <= 64) return stream<4, 2, 4>(p, s);
+  const int64_t n_tiles = ceil_div(p.N, kTileN), of64 = ceil_div(p.M, 64) * n_tiles;
+  // rows that hold a pair, about: without their number half of the blocks' last rows do not
+  const int64_t held = p.row_ids ? p.num_ids : p.M - p.E * p.BM / 2;
+  const bool many = p.tile_expert ? p.BM > 32 || held > kFewRows * p.E : takes(64);
+  if (many && of64 > 64) {
     // one round of pairs of 64 rows, where those of 256 would be more than half a round, not parted
     const bool pairs = !p.tile_expert && of64 <= 2 * kRound && 2 * ceil_div(p.M, 256) * n_tiles > kRound;
     if (p.K > kShortK && !pairs) {
@@ -605,6 +637,7 @@ hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t s) {
     }
     return tiled<64>(p, s);
   }
+  if (takes(64)) return stream<4, 2, 4>(p, s);
   if (takes(32)) return stream<2, 4, 4>(p, s);
   return few<1, 4, 16>(p, s);
 }

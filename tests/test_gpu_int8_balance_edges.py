@@ -153,6 +153,62 @@ def test_experts_and_rows_past_32_bits(bm):
         check_product(y[at], x[at], xs[at], w[e], ws[e], None, False)
 
 
+VARIANTS = [  # block_m (0: one weight for all rows), blocks or rows, N, K, experts
+    (16, 900, 272, 544, 9), (16, 64, 4112, 272, 2), (16, 300, 1040, 96, 40), (32, 301, 528, 800, 5),
+    (32, 33, 4112, 144, 1), (48, 70, 1040, 272, 30), (80, 41, 1040, 528, 7), (96, 50, 800, 544, 3),
+    (112, 40, 1040, 560, 11), (160, 30, 1040, 272, 4), (240, 30, 1040, 528, 4), (64, 130, 1040, 1040, 6),
+    (128, 60, 1040, 4112, 6), (128, 100, 1040, 4112, 3), (128, 60, 1040, 1040, 6), (256, 19, 4352, 528, 4),
+    (256, 70, 1040, 528, 4), (256, 34, 2064, 512, 4), (256, 1, 17 * 256, 1040, 1),
+    (0, 96, 8464, 4112, 1), (0, 384, 11024, 528, 1), (0, 200, 28672, 528, 1), (0, 2049, 8192, 544, 1),
+    (0, 4097, 1040, 256, 1), (0, 65, 16400, 272, 1), (0, 1000, 15888, 528, 1)]
+
+
+@pytest.mark.parametrize("case", VARIANTS, ids=lambda c: "b{}n{}N{}K{}E{}".format(*c))
+def test_variants(case):
+    """Runs of blocks of one expert of any length, blocks without one among them, all sizes of
+    tiles and parts of them: against products in 64 bits, which are exact here."""
+    bm, n, N, K, E = case
+    M = bm * n if bm else n
+    say(f"variant {case}")
+    g = torch.Generator().manual_seed(60)
+    w, ws = device_codes(E, N, K, seed=61), torch.rand(E, N, device="cuda") * 1e-3
+    x, xs = device_codes(M, K, seed=62), torch.rand(M, device="cuda")
+    al = None
+    expert = torch.zeros(M, dtype=torch.long)
+    if bm:
+        runs = torch.randint(1, 7, (n,), generator=g)
+        te = torch.repeat_interleave(torch.randint(-1, E, (n,), generator=g), runs)[:n]
+        te[-1 - n // 8:] = -1
+        al = dict(block_m=bm, tile_expert=te.int().cuda())
+        expert = te.repeat_interleave(bm)
+    expert = expert.cuda()
+    ref = torch.full((M, N), -9.5, dtype=torch.float32, device="cuda")
+    for e in range(E):
+        at = expert == e
+        ref[at] = (x[at].double() @ w[e].double().t()).float() * xs[at, None] * ws[e]
+    mark = torch.full((M, N), -9.5, dtype=torch.float32, device="cuda")
+    wa, wsa = (w, ws) if bm else (w[0], ws[0])
+    y = binding.moe_lora_int8_gemm(x, xs, wa, wsa, align_out=al, out=mark.clone())
+    assert torch.equal(y, ref)
+    if not bm:
+        return
+    # with padding rows: some in between, and every block's end behind a row of its own
+    live = torch.rand(M, generator=g) < 0.9
+    live &= torch.arange(M) % bm < torch.randint(0, bm + 1, (n,), generator=g).repeat_interleave(bm)
+    pairs = int(live.sum())
+    sid = torch.full((M,), pairs, dtype=torch.int32)
+    sid[live] = torch.randperm(pairs, generator=g).int()
+    al.update(sorted_pair_ids=sid.cuda(), pair_rows=torch.empty(pairs, dtype=torch.int32, device="cuda"), capacity=M)
+    ref[((expert >= 0) & ~live.cuda())] = 0.0
+    assert torch.equal(binding.moe_lora_int8_gemm(x, xs, wa, wsa, align_out=al, out=mark.clone()), ref)
+    # the same rows where the tokens lie
+    tok, tok_s = torch.zeros(pairs, K, dtype=torch.int8, device="cuda"), torch.ones(pairs, device="cuda")
+    at = sid[live].long().cuda()
+    tok[at], tok_s[at] = x[live.cuda()], xs[live.cuda()]
+    y = binding.moe_lora_int8_gemm(tok, tok_s, wa, wsa, align_out=al, top_k=1, out=mark.clone())
+    assert torch.equal(y, ref)
+
+
 def test_tokens_of_many_rounds():
     """More tokens than the loss's workgroups take at once."""
     T, E, k = 1 << 20, 5, 2

@@ -130,6 +130,9 @@ def test_gemm_codes():
     assert call(num_rows=0, in_features=(1 << 17) - 16) == OK
     assert call(out_features=(1 << 24) + 16) == UNSUPPORTED
     assert call(num_rows=1 << 30, out_features=1 << 14) == UNSUPPORTED
+    most = 16 * ((1 << 24) - 256)                            # of 64 columns
+    assert call(num_rows=most + 16, out_features=64) == UNSUPPORTED
+    assert call(num_rows=most, out_features=64, out=None) == INVALID
     for bm in (0, -16, 8, 24):
         assert call(block_m=bm) == INVALID, bm
     assert call(num_rows=72) == INVALID                      # not whole tiles
