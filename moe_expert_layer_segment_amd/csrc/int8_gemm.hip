@@ -61,9 +61,9 @@ __device__ __forceinline__ int64_t weight_row(const Int8Gemm& p, int64_t cb) {
 }
 
 // ---- few rows --------------------------------------------------------------
-// The weights are streamed from memory into registers, once, and bound the kernel.  A workgroup
-// holds 16 MB rows and 16 NB columns; its WV waves take every WV-th group of 128 values of K and
-// add their sums through LDS.
+// The weights are streamed from memory into registers, once, and bound the kernel (64 tokens x 8
+// of 128 experts, 1536 x 2048 each: 74 us, 5.3 TB/s).  A workgroup holds 16 MB rows and 16 NB
+// columns; its WV waves take every WV-th group of 128 values of K and add their sums through LDS.
 template <int MB, int NB, int WV>
 __global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2)
 int8_stream_kernel(Int8Gemm p, int row_groups, int col_groups) {
@@ -206,6 +206,10 @@ static hipError_t stream(const Int8Gemm& p, hipStream_t stream) {
 // LDS rows are eight 16-byte chunks.  Lane group g takes chunk 2g + h of its row in step h, from
 // place (2g + h) ^ (bits 3, 1, 2 of the row's number): no two of 16 lanes read one bank, and a
 // DMA's lanes, which fill places in order, still read whole 64-byte pieces.
+//
+// 4096 x 4096 x 7168 takes 99 us (2.4e15 operations a second; 91 without the DMAs, 87 where all
+// values are zero: the clock gives way to the power), of which about 11 are the start and the end
+// of a tile: there is one workgroup to a CU, so nothing runs beside them.
 constexpr int kTileN = 256;
 constexpr int kStep = 128;   // bytes of K in an LDS row
 
@@ -598,10 +602,13 @@ static hipError_t tiled(const Int8Gemm& p, hipStream_t stream) {
 }
 
 // A workgroup of 4 waves and 16 NB columns, or, where those would not fill the chip, of WIDE
-// waves and 16 columns (32 with silu_mul: a gate and an up block).
+// waves and 16 columns (32 with silu_mul: a gate and an up block).  By 4 waves and by WIDE (us): a row x
+// 2112 x 7168 16.3 and 9.4, x 8192 x 2048 (128 workgroups of 4) 9.9 and 9.4, x 16384 x 2048 (256)
+// 10.8 and 12.0, x 28672 x 4096 23 and 28; 30 rows x 2112 x 7168 21.4 and 12.1; 40 rows x 4096 x 4096
+// (128) 13.8 and 11.5, 128 rows x 2112 x 7168 (132) 23.5 and 35.6: more waves read x more often.
 template <int MB, int NB, int WIDE>
 static hipError_t few(const Int8Gemm& p, hipStream_t s) {
-  if (ceil_div(p.M, 16 * MB) * ceil_div(p.N, 16 * NB) >= 512) return stream<MB, NB, 4>(p, s);
+  if (ceil_div(p.M, 16 * MB) * ceil_div(p.N, 16 * NB) > (MB == 1 ? 255 : 128)) return stream<MB, NB, 4>(p, s);
   if (p.silu_mul) return stream<MB, 2, WIDE>(p, s);
   return stream<MB, 1, WIDE>(p, s);
 }
@@ -628,6 +635,8 @@ hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t s) {
   // rows that hold a pair, about: without their number half of the blocks' last rows do not
   const int64_t held = p.row_ids ? p.num_ids : p.M - p.E * p.BM / 2;
   const bool many = p.tile_expert ? p.BM > 32 || held > kFewRows * p.E : takes(64);
+  // (64 workgroups of tiles and fewer: 64 rows x 8192 x 2048 20 us, streamed 11; 256 x 4096 x 4096,
+  // with 64, 30 and 26; 256 x 8192 x 2048, with 128, 19 and 27)
   if (many && of64 > 64) {
     // one round of pairs of 64 rows, where those of 256 would be more than half a round, not parted
     const bool pairs = !p.tile_expert && of64 <= 2 * kRound && 2 * ceil_div(p.M, 256) * n_tiles > kRound;
@@ -637,8 +646,8 @@ hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t s) {
     }
     return tiled<64>(p, s);
   }
-  if (takes(64)) return stream<4, 2, 4>(p, s);
-  if (takes(32)) return stream<2, 4, 4>(p, s);
+  if (takes(64)) return few<4, 2, 8>(p, s);
+  if (takes(32)) return few<2, 4, 8>(p, s);
   return few<1, 4, 16>(p, s);
 }
 
