@@ -199,23 +199,34 @@ static hipError_t stream(const Int8Gemm& p, hipStream_t stream) {
 // fragments (256 bytes a lane) for 64 MFMAs, half the LDS reads of eight waves with 128 x 64.
 //
 // A step multiplies one set of fragments while the other is read for the step that follows, the
-// reads and the DMAs spread over the MFMAs.  After the first step of a K tile all of the tile is
-// in registers: a barrier, ahead of which every wave has waited for its DMAs of the next tile,
-// frees its buffer and admits the next one.
+// reads and the DMAs spread over the MFMAs.  Half way through the first step of a K tile all of it
+// is in registers: a barrier there frees its buffer for the DMAs of the tile after the next, half
+// of which go out in what is left of this step and half in the second.  A barrier between the
+// steps, ahead of which every wave has waited for its DMAs of the next tile, admits that one.
+// (With one barrier for both, behind the first step, DMAs had half a step less to arrive:
+// 2048 x 4096 x 4128 52 us, so 46; 1000 x 4096 x 7168 50 and 44; 8192 rows of 32 experts x 8192 x
+// 4096 425 and 402.)
 //
 // LDS rows are eight 16-byte chunks.  Lane group g takes chunk 2g + h of its row in step h, from
 // place (2g + h) ^ (bits 3, 1, 2 of the row's number): no two of 16 lanes read one bank, and a
 // DMA's lanes, which fill places in order, still read whole 64-byte pieces.
 //
-// 4096 x 4096 x 7168 takes 99 us (2.4e15 operations a second; 91 without the DMAs, 87 where all
-// values are zero: the clock gives way to the power), of which about 11 are the start and the end
-// of a tile: there is one workgroup to a CU, so nothing runs beside them.
+// 4096 x 4096 x 7168 takes 99 us (2.4e15 operations a second; 87 where all values are zero: the
+// clock gives way to the power, from 2.1 GHz to 1.8 where the weights come from memory), of which
+// about 11 are the start and the end of a tile: there is one workgroup to a CU, so nothing runs
+// beside them.  Of 4096 x 4096 x 28672 (380 us, matrix units busy for 58% of its cycles) the DMAs
+// cost a fourth and the LDS reads an eighth; without both they are busy for 81%.
 constexpr int kTileN = 256;
 constexpr int kStep = 128;   // bytes of K in an LDS row
 
-// this wave's DMA and LDS reads are done, then every wave's
-__device__ __forceinline__ void wait_all_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// this wave's DMAs but its last N are done, then every wave's
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+// this wave's LDS reads are done, then every wave's
+__device__ __forceinline__ void read_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // 8 neighbouring columns
@@ -364,23 +375,24 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
   };
   constexpr std::integral_constant<int, 0> first{};
   constexpr std::integral_constant<int, 1> second{};
-  // The MFMAs of step H.  Between them, at an even pace, the fragments of the other step are read
-  // from `place`, and DMAs go out (send).
-  constexpr int SLOTS = MB * NB, READS = MB + NB;
-  static_assert(READS <= SLOTS && DMAS <= SLOTS, "a slot behind each MFMA");
-  auto step = [&](auto H, int place, auto&& send) {
+  // The MFMAs of step H.  Between them the fragments of the other step are read from `place`: in the
+  // second step at an even pace, in the first one behind each of the first MFMAs, and then(slot)
+  // does what else there is.
+  constexpr int SLOTS = MB * NB, READS = MB + NB, FREE = SLOTS / 2, EARLY = DMAS / 2;
+  static_assert(READS <= FREE, "every fragment is read before the buffer is free");
+  auto step = [&](auto H, int place, auto&& then) {
     constexpr int h = decltype(H)::value;
     std::integral_constant<int, 1 - h> other;
     static_for<SLOTS>([&](auto S) {
       constexpr int s = decltype(S)::value, i = s / NB, j = s % NB;
       mfma_in_place(acc[i][j], wf[h][j], xf[h][i]);
-      // the n-th of READS lies behind MFMA n SLOTS / READS; those of the weights come first
-      constexpr int n = (s * READS + SLOTS - 1) / SLOTS;
-      if constexpr (n < READS && n * SLOTS / READS == s) {
+      // the n-th of READS lies behind MFMA n SPAN / READS; those of the weights come first
+      constexpr int SPAN = h == 0 ? READS : SLOTS, n = (s * READS + SPAN - 1) / SPAN;
+      if constexpr (n < READS && n * SPAN / READS == s) {
         if constexpr (n < NB) read_w(place, other, std::integral_constant<int, n < NB ? n : 0>{});
         else read_x(place, other, std::integral_constant<int, n < NB ? 0 : n - NB>{});
       }
-      send(S);
+      then(S);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
@@ -389,7 +401,7 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
     if (decltype(D)::value == 0 && tiles == 1) last_tile();
     issue(bases_of(0), 0, decltype(D)::value);
   });
-  wait_all_barrier();
+  wait_barrier<0>();
   if (tiles > 1) {
     if (tiles == 2) last_tile();
     static_for<DMAS>([&](auto D) { issue(bases_of(1), 1, decltype(D)::value); });
@@ -410,22 +422,33 @@ __device__ __forceinline__ void int8_tile(const Int8Gemm& p, char* lds, int64_t 
   settle();
   // one loop for every tile, the last ones too: where the sums pass from one piece of code to
   // another the compiler moves them.  (What the last tile reads ahead is not used.)
+  constexpr std::integral_constant<int, EARLY> early{};
+  constexpr std::integral_constant<int, DMAS> all{};
   int place = 0;
 #pragma unroll 1
   for (int t = 0; t < tiles; ++t, place ^= 1) {
     if (t + 1 == tiles) cut(first);
-    step(first, place, [](auto) {});
-    wait_all_barrier();
-    if (t + 1 == tiles) cut(second);
     if (t + 3 == tiles) last_tile();
     const Bases at = bases_of(t + 2);
     const bool sends = t + 2 < tiles;
-    step(second, place ^ 1, [&](auto S) {
-      constexpr int s = decltype(S)::value, d = (s * DMAS + SLOTS - 1) / SLOTS;
-      if constexpr (d < DMAS && d * SLOTS / DMAS == s) {
-        if (sends) issue(at, place, d);
-      }
+    // DMAs LO to HI - 1 behind the MFMAs from slot FROM on, at an even pace
+    auto send = [&](auto S, auto FROM, auto LO, auto HI) {
+      constexpr int s = decltype(S)::value - decltype(FROM)::value, span = SLOTS - decltype(FROM)::value;
+      constexpr int lo = decltype(LO)::value, many = decltype(HI)::value - lo;
+      constexpr int d = lo + s * many / span, end = lo + (s + 1) * many / span;
+      static_for<end - d>([&](auto D) {
+        if (sends) issue(at, place, d + decltype(D)::value);
+      });
+    };
+    step(first, place, [&](auto S) {
+      constexpr int s = decltype(S)::value;
+      if constexpr (s == FREE) read_barrier();
+      if constexpr (s >= FREE) send(S, std::integral_constant<int, FREE>{}, first, early);
     });
+    if (sends) wait_barrier<EARLY>();
+    else wait_barrier<0>();
+    if (t + 1 == tiles) cut(second);
+    step(second, place ^ 1, [&](auto S) { send(S, first, early, all); });
     // the last products are done before what follows reads them: here, since the compiler may move
     // the sums as soon as the loop ends
     settle();
