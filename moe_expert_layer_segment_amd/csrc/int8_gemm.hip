@@ -36,11 +36,15 @@ __device__ __forceinline__ void store_out(const Int8Gemm& p, int64_t at, floatx4
 }
 
 // SiLU(v) as silu_f, with what rounding the exponent -v log2(e) to fp32 leaves made good: it
-// would cost e^-v |v| 2^-25 of its value.
+// would cost e^-v |v| 2^-25 of its value.  The exponent is that of a v within [-126, 126], where
+// it and its correction are finite: e^126 is infinite and e^-126 nothing beside 1, so a v beyond
+// gives what it should, v itself (or its infinity) or -0.  Below -88, where SiLU is less than 1e-36,
+// the result is -0.
 __device__ __forceinline__ float silu_near(float v) {
   const float kLog2e = 1.4426950408889634f, kRest = 1.925963033500887e-8f, kLn2 = 0.6931471805599453f;
-  const float t = -v * kLog2e;
-  const float lo = __builtin_fmaf(-v, kRest, __builtin_fmaf(-v, kLog2e, -t));
+  const float x = -__builtin_amdgcn_fmed3f(v, -126.0f, 126.0f);
+  const float t = x * kLog2e;
+  const float lo = __builtin_fmaf(x, kRest, __builtin_fmaf(x, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t);
   // (an infinite e stays one: times lo it would not)
   return v * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(fminf(e, 1e38f), lo * kLn2, e));
