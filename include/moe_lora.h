@@ -645,7 +645,8 @@ int moe_lora_int8_gemm(const moe_lora_int8_gemm_args* args, void* stream);
  *   loss          = num_experts / (n * top_k) * sum_e counts[e] * mean_probs[e]
  *
  *   logits      [num_tokens, num_experts] in dtype (F32 or BF16).  -inf switches an expert
- *               off for a token (probability 0); in a row of -inf alone all are 0.
+ *               off for a token (probability 0); in a row of -inf alone all are 0, in
+ *               one with a NaN or +inf all NaN.
  *   topk_ids    [num_tokens, top_k] int32 (moe_lora_route); ids outside [0, num_experts)
  *               are counted nowhere.
  *   token_mask  [num_tokens] bytes, 0 for tokens that take no part (padding; their logits and

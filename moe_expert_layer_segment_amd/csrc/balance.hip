@@ -6,8 +6,8 @@
 //   loss     = E / (n k) sum_e counts_e P_e       (1 where both are even)
 //   d loss / d logits_te = E / (n^2 k) p_te (counts_e - sum_i p_ti counts_i)
 //
-// counts are constants to the gradient.  A row of logits that are all -inf has p = 0, and with
-// n = 0 everything is 0.  Logits of tokens outside the mask are never read.
+// counts are constants to the gradient.  A row of logits that are all -inf has p = 0, one with a NaN or
+// +inf has p = NaN, and with n = 0 everything is 0.  Logits of tokens outside the mask are never read.
 //
 // One wave per token, V experts to a lane: neighbours where V divides their number, so that a
 // load brings them all, else every 64th.  p is fp32, from the difference to the largest logit
@@ -73,16 +73,22 @@ __device__ __forceinline__ float exp_of(float z, float lo) {
   return __builtin_fmaf(e, rest * kLn2, e);
 }
 
-// logits of a lane, -inf behind the last, to their probabilities
+// logits of a lane, -inf behind the last, to their probabilities: of a row with a NaN all are NaN.
+// (The largest logit is that of the numbers, so that the NaN is met by the sum, or where there is no
+// other number than -inf by a vote.)
 template <int V>
 __device__ __forceinline__ void softmax(float (&v)[V]) {
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-  m = wave_max(m, -INFINITY);
+  m = wave_max(m == m ? m : -INFINITY, -INFINITY);
   if (m == -INFINITY) {
+    bool nan = false;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = v[i] == -INFINITY ? 0.0f : v[i];   // NaN stays
+    for (int i = 0; i < V; ++i) nan |= v[i] != v[i];
+    const float p = __ballot(nan) ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = p;
     return;
   }
   float sum = 0.0f;

@@ -43,7 +43,8 @@ template <typename T>
 __device__ __forceinline__ T wave_sum(T v) {
   return wave_reduce(v, T(0), [](T a, T b) { return a + b; });
 }
-// of values none of which is below `none`
+// of values none of which is below `none`, or NaN: as the first of a pair it would be lost, and as the
+// second take the other's place
 template <typename T>
 __device__ __forceinline__ T wave_max(T v, T none) {
   return wave_reduce(v, none, [](T a, T b) { return a > b ? a : b; });
