@@ -97,7 +97,7 @@ __device__ __forceinline__ void softmax(float (&v)[V]) {
     // z + lo = v - m exactly; far below the largest logit (-inf, which has no lo) p is 0
     const float z = v[i] - m;
     const float back = z + m;
-    const float lo = (v[i] - back) - (z - (back - m));
+    const float lo = (v[i] - back) - (m + (z - back));
     v[i] = z < -200.0f ? 0.0f : exp_of(z, lo);
     sum += v[i];
   }

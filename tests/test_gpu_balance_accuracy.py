@@ -1,10 +1,13 @@
 """The balance loss and its gradient where probabilities, counts or differences are delicate: NaN
-in any lane."""
+in any lane, logits far below the largest."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import int8_balance_oracle as ib
 from gpu_helpers import say
 from moe_expert_layer_segment_amd import binding
+from test_gpu_balance import D, HALF, TINY, np64
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +41,28 @@ def test_nan_at_every_expert(E, off):
     for t in {0, 1, half - 1, half, half + 1, half + half // 2, E - 1}:
         stats = binding.moe_lora_balance_loss(logits[t:t + 1], ids)
         assert bool(stats["mean_probs"].isnan().all()) and bool(stats["loss"].isnan().all()), t
+
+
+# ---------------------------------------------------------------------------
+# logits far below the largest
+# ---------------------------------------------------------------------------
+def far_rows(E, n, seed, below=86.0):
+    """fp32 rows whose largest logit is small or negative, the others far below it."""
+    g = torch.Generator().manual_seed(seed)
+    top = 65 * torch.rand(n, 1, generator=g, dtype=torch.float64) - 60
+    logits = top - 20 - (below - 20) * torch.rand(n, E, generator=g, dtype=torch.float64)
+    at = torch.randint(0, E, (n, 1), generator=g)
+    return logits.scatter(1, at, top).float().cuda()
+
+
+@pytest.mark.parametrize("E", [64, 300, 1024])
+def test_logits_far_below_a_negative_one(E):
+    """Each probability of a token alone is within D of its value: the difference to the largest
+    logit is taken to more digits than fp32 holds of it."""
+    say(f"far below {E}")
+    ids = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    logits = far_rows(E, 40, 2)
+    p = ib.softmax(np64(logits))
+    for t in range(40):
+        mean = np64(binding.moe_lora_balance_loss(logits[t:t + 1], ids)["mean_probs"])
+        assert (np.abs(mean - p[t]) <= (D + HALF[torch.float32]) * p[t] + TINY).all(), t
