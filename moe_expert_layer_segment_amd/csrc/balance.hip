@@ -344,12 +344,20 @@ balance_backward_kernel(Balance b, const int32_t* __restrict__ counts, const int
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * waves;
       if (t >= b.T) break;
+      // sum_i p_i c_i with probabilities that add up to 1: in c_e - dot all of c would stay of what they
+      // lack, beside differences that can be any part of it (every c the same: 0)
       double dot = 0.0;
       if (live[u]) {
+        double sum = 0.0;
         softmax<V>(p[u]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dot = __builtin_fma((double)p[u][i], (double)c[i], dot);
+        for (int i = 0; i < V; ++i) {
+          dot = __builtin_fma((double)p[u][i], (double)c[i], dot);
+          sum += (double)p[u][i];
+        }
         dot = wave_sum(dot);
+        sum = wave_sum(sum);
+        if (sum != 0.0) dot /= sum;
       }
       float d[V];
 #pragma unroll

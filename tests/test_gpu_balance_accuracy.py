@@ -1,5 +1,6 @@
 """The balance loss and its gradient where probabilities, counts or differences are delicate: NaN
-in any lane, logits far below the largest."""
+in any lane, logits far below the largest, one expert far above the others,
+even counts."""
 import numpy as np
 import pytest
 import torch
@@ -18,6 +19,19 @@ def gradient(logits, counts, n=None, k=1, d_loss=None):
     n = logits.shape[0] if n is None else n
     stats = dict(counts=counts, num_valid=torch.tensor([n], dtype=torch.int32).cuda(), top_k=k)
     return binding.moe_lora_balance_loss_backward(d_loss, logits, stats, out_dtype=torch.float32)
+
+
+def differences(logits, counts, n=None, k=1):
+    """(gradient, size): g p_e sum_i p_i (c_e - c_i) and g p_e sum_i p_i |c_e - c_i| in float64.
+    Probabilities that are off by a factor 1 + d each leave the gradient off by 2 |d| of the size."""
+    l64 = np64(logits)
+    p, c = ib.softmax(l64), np.asarray(counts, dtype=np.float64)
+    T, E = l64.shape
+    n = T if n is None else n
+    g = E / (float(n) ** 2 * k)
+    diff = c[:, None] - c[None, :]
+    return g * p * (p @ diff.T), g * p * (p @ np.abs(diff).T)
+
 
 
 # ---------------------------------------------------------------------------
@@ -66,3 +80,46 @@ def test_logits_far_below_a_negative_one(E):
     for t in range(40):
         mean = np64(binding.moe_lora_balance_loss(logits[t:t + 1], ids)["mean_probs"])
         assert (np.abs(mean - p[t]) <= (D + HALF[torch.float32]) * p[t] + TINY).all(), t
+
+
+# ---------------------------------------------------------------------------
+# differences of counts
+# ---------------------------------------------------------------------------
+def peaked_rows(E, n, seed):
+    """Rows with one logit 15 to 30 above the others'."""
+    g = torch.Generator().manual_seed(seed)
+    logits = torch.randn(n, E, generator=g)
+    at = torch.randint(0, E, (n, 1), generator=g)
+    return logits.scatter(1, at, 15 + 15 * torch.rand(n, 1, generator=g)).cuda()
+
+
+# what 64 bits leave of c_e - sum_i p_i c_i / sum_i p_i, of c: two sums of 16 terms in a lane and of six
+# exchanges, a quotient and a difference: 46 half steps of 2^-53
+LAST = 2.0 ** -47
+
+
+@pytest.mark.parametrize("E", [2, 64, 200, 1024])
+def test_gradient_of_peaked_rows(E):
+    """Where one expert has all but a millionth of the probability its gradient is a difference of
+    nearly equal numbers; what the rounding of probabilities leaves is of the size of the
+    differences of counts alone, and rows add up to 0."""
+    say(f"peaked rows {E}")
+    g = torch.Generator().manual_seed(3)
+    counts = torch.randint(1500, 2501, (E,), generator=g)
+    logits = peaked_rows(E, 200, 4)
+    d = np64(gradient(logits, counts))
+    ref, size = differences(logits, counts)
+    noise = LAST * E / 200.0 ** 2 * 2500
+    tol = 2.01 * D * size + HALF[torch.float32] * (np.abs(ref) + 2.01 * D * size) + noise + TINY
+    assert (np.abs(d - ref) <= tol).all()
+    # each element is rounded twice (p, and the result)
+    assert (np.abs(d.sum(1)) <= 2.01 * 2.0 ** -24 * np.abs(d).sum(1) + E * (noise + TINY)).all()
+
+
+@pytest.mark.parametrize("E", [1, 2, 61, 64, 256, 1000])
+def test_gradient_of_even_counts_is_zero(E):
+    say(f"even counts {E}")
+    for logits in (peaked_rows(E, 50, 5), torch.randn(50, E, generator=torch.Generator().manual_seed(6)).cuda()):
+        d = np64(gradient(logits, [12345] * E))
+        p = ib.softmax(np64(logits))
+        assert (np.abs(d) <= LAST * 12345 * E / 50.0 ** 2 * p * (1 + D) + TINY).all()
