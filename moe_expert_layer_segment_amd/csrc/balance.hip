@@ -326,9 +326,9 @@ balance_backward_kernel(Balance b, const int32_t* __restrict__ counts, const int
   const int E = b.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t n = num_valid[0];
   const double g = n > 0 ? (d_loss ? (double)d_loss[0] : 1.0) * (double)E / ((double)n * (double)n * (double)b.k) : 0.0;
-  float c[V];
+  double c[V];   // exactly: their differences may be below what fp32 holds of counts of many ranks
 #pragma unroll
-  for (int i = 0; i < V; ++i) c[i] = expert_of<V, NEXT>(i) < E ? (float)counts[expert_of<V, NEXT>(i)] : 0.0f;
+  for (int i = 0; i < V; ++i) c[i] = expert_of<V, NEXT>(i) < E ? (double)counts[expert_of<V, NEXT>(i)] : 0.0;
   constexpr int U = V <= 4 ? 2 : 1;
   const int64_t waves = (int64_t)gridDim.x * kBackWaves;
   for (int64_t t0 = (int64_t)blockIdx.x * kBackWaves + wave; t0 < b.T; t0 += waves * U) {
@@ -352,7 +352,7 @@ balance_backward_kernel(Balance b, const int32_t* __restrict__ counts, const int
         softmax<V>(p[u]);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          dot = __builtin_fma((double)p[u][i], (double)c[i], dot);
+          dot = __builtin_fma((double)p[u][i], c[i], dot);
           sum += (double)p[u][i];
         }
         dot = wave_sum(dot);
@@ -361,7 +361,7 @@ balance_backward_kernel(Balance b, const int32_t* __restrict__ counts, const int
       }
       float d[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = live[u] ? (float)(g * (double)p[u][i] * ((double)c[i] - dot)) : 0.0f;
+      for (int i = 0; i < V; ++i) d[i] = live[u] ? (float)(g * (double)p[u][i] * (c[i] - dot)) : 0.0f;
       store_logits<O, V, NEXT>(d_logits + t * E, E, d);
     }
   }

@@ -1,6 +1,6 @@
 """The balance loss and its gradient where probabilities, counts or differences are delicate: NaN
 in any lane, logits far below the largest, one expert far above the others,
-even counts."""
+even counts, counts past 2^24."""
 import numpy as np
 import pytest
 import torch
@@ -123,3 +123,19 @@ def test_gradient_of_even_counts_is_zero(E):
         d = np64(gradient(logits, [12345] * E))
         p = ib.softmax(np64(logits))
         assert (np.abs(d) <= LAST * 12345 * E / 50.0 ** 2 * p * (1 + D) + TINY).all()
+
+
+@pytest.mark.parametrize("base", [1 << 24, (1 << 28) + 3, (1 << 31) - 2000])
+@pytest.mark.parametrize("E", [8, 65, 512])
+def test_counts_past_24_bits(E, base):
+    """Counts summed over ranks differ by less than fp32 holds of them."""
+    say(f"counts {E} {base}")
+    g = torch.Generator().manual_seed(7)
+    counts = base + torch.randint(0, 1000, (E,), generator=g)
+    logits = torch.randn(60, E, generator=g).cuda()
+    n = 1 << 26
+    d = np64(gradient(logits, counts, n, 8))
+    ref, size = differences(logits, counts, n, 8)
+    noise = LAST * E / (float(n) ** 2 * 8) * base
+    tol = 2.01 * D * size + HALF[torch.float32] * (np.abs(ref) + 2.01 * D * size) + noise + TINY
+    assert (np.abs(d - ref) <= tol).all()
