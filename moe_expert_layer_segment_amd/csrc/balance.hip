@@ -10,11 +10,11 @@
 // +inf has p = NaN, and with n = 0 everything is 0.  Logits of tokens outside the mask are never read.
 //
 // One wave per token, V experts to a lane: neighbours where V divides their number, so that a
-// load brings them all, else every 64th.  p is fp32, from the difference to the largest logit
-// with its rounding error (two fp32 numbers); a wave adds its tokens up in fp64 registers, a
-// workgroup its waves through LDS, and the workgroups' sums go through memory to others that add
-// them in order: no floating-point atomics, so results do not change from run to run.  Few tokens
-// are one workgroup, and one launch.
+// load brings them all, else every 64th.  p is fp64, and holds more than fp32 would: the gradient is
+// a difference, and an fp32 result lacks little but its own rounding.  A wave adds its tokens up in
+// registers, a workgroup its waves through LDS, and the workgroups' sums go through memory to others
+// that add them in order: no floating-point atomics, so results do not change from run to run.  Few
+// tokens are one workgroup, and one launch.
 //
 // Latency bounds small batches, and the instructions of the softmax large ones: 16384 tokens of 256
 // experts in fp32 take 10 us forward (17 MB: 3 at the rate of reading), 5.5 for the finish, and 12
@@ -64,47 +64,46 @@ __device__ __forceinline__ int expert_of(int i) {
   return NEXT ? lane * V + i : lane + 64 * i;
 }
 
-// 2^x of z + lo, where z log2(e) is rounded once and the rest makes it good
-__device__ __forceinline__ float exp_of(float z, float lo) {
-  const float kLog2e = 1.4426950408889634f, kRest = 1.925963033500887e-8f, kLn2 = 0.6931471805599453f;
-  const float t = z * kLog2e;
-  const float rest = __builtin_fmaf(lo, kLog2e, __builtin_fmaf(z, kRest, __builtin_fmaf(z, kLog2e, -t)));
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, rest * kLn2, e);
+// e^z of z <= 0 (0 below -2000), to 2^-29 of its value: 2^n 2^f of z log2(e) = n + f, |f| <= 1/2, with
+// the series of 2^f to f^8.  Its terms from f^3 on are fp32, rounded at 2^-28 of an eighth of the result,
+// all else fp64.  (It takes no longer than the hardware's exponential with what makes its argument good,
+// and gives 6 bits more.)
+__device__ __forceinline__ double exp_of(double z) {
+  constexpr double kLog2e = 1.4426950408889634;
+  constexpr double kInt = 1.5 * 4503599627370496.0;   // its last bit is 1
+  const double s = __builtin_fma(z, kLog2e, kInt);
+  const double f = __builtin_fma(z, kLog2e, -(s - kInt));
+  const float x = (float)f;
+  float r = 1.3215487e-6f;                            // ln(2)^k / k!, from k = 8 down
+  r = __builtin_fmaf(r, x, 1.5252734e-5f);
+  r = __builtin_fmaf(r, x, 1.5403530e-4f);
+  r = __builtin_fmaf(r, x, 1.3333558e-3f);
+  r = __builtin_fmaf(r, x, 9.6181291e-3f);
+  r = __builtin_fmaf(r, x, 5.5504109e-2f);
+  double e = __builtin_fma(f, (double)r, 0.2402265069591007);
+  e = __builtin_fma(f, e, 0.6931471805599453);
+  e = __builtin_fma(f, e, 1.0);
+  return __builtin_amdgcn_ldexp(e, (int32_t)(uint32_t)__builtin_bit_cast(uint64_t, s));
 }
 
-// logits of a lane, -inf behind the last, to their probabilities: of a row with a NaN all are NaN.
-// (The largest logit is that of the numbers, so that the NaN is met by the sum, or where there is no
-// other number than -inf by a vote.)
+// logits of a lane, -inf behind the last, to e^(logit - the row's largest); all 0 where there is none
+// but -inf.  The largest is that of the numbers, and a NaN stays one.
 template <int V>
-__device__ __forceinline__ void softmax(float (&v)[V]) {
+__device__ __forceinline__ void exponentials(const float (&v)[V], double (&e)[V]) {
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-  m = wave_max(m == m ? m : -INFINITY, -INFINITY);
-  if (m == -INFINITY) {
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) nan |= v[i] != v[i];
-    const float p = __ballot(nan) ? __builtin_nanf("") : 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = p;
-    return;
-  }
-  float sum = 0.0f;
+  m = wave_max(m == m ? m : -INFINITY);
+  const double base = m == -INFINITY ? 0.0 : (double)m;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    // z + lo = v - m exactly; far below the largest logit (-inf, which has no lo) p is 0
-    const float z = v[i] - m;
-    const float back = z + m;
-    const float lo = (v[i] - back) - (m + (z - back));
-    v[i] = z < -200.0f ? 0.0f : exp_of(z, lo);
-    sum += v[i];
+    const double z = (double)v[i] - base;
+    e[i] = exp_of(z < -2000.0 ? -2000.0 : z);   // (for -inf; NaN stays)
   }
-  const float per = __builtin_amdgcn_rcpf(wave_sum(sum));
-#pragma unroll
-  for (int i = 0; i < V; ++i) v[i] *= per;
 }
+
+// what makes exponentials of this sum (at least 1, 0 or NaN) to probabilities
+__device__ __forceinline__ double per_sum(double sum) { return sum == 0.0 ? 0.0 : reciprocal(sum); }
 
 template <typename T, int V, bool NEXT>
 __device__ __forceinline__ void load_logits(const T* row, int E, float (&v)[V]) {
@@ -177,7 +176,7 @@ template <typename T, int V, bool NEXT>
 __global__ void __launch_bounds__(kBalThreads)
 balance_kernel(Balance b, BalanceWs ws, BalanceOut out) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const int E = b.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int E = b.E, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double* const sums = reinterpret_cast<double*>(lds);              // [4][E]
   int32_t* const counts = reinterpret_cast<int32_t*>(sums + 4 * E); // [E]
   __shared__ int32_t valid[kBalWaves];
@@ -214,9 +213,13 @@ balance_kernel(Balance b, BalanceWs ws, BalanceOut out) {
         const int32_t e = b.topk_ids[(t0 + u * waves) * b.k + j];
         if (e >= 0 && e < E) atomicAdd(&counts[e], 1);
       }
-      softmax<V>(v[u]);
+      double e[V], sum = 0.0;
+      exponentials<V>(v[u], e);
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += (double)v[u][i];
+      for (int i = 0; i < V; ++i) sum += e[i];
+      const double per = per_sum(wave_sum(sum));
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = __builtin_fma(e[i], per, acc[i]);
     }
   }
   if (lane == 0) valid[wave] = n;
@@ -323,7 +326,7 @@ template <typename T, typename O, int V, bool NEXT>
 __global__ void __launch_bounds__(kBackThreads)
 balance_backward_kernel(Balance b, const int32_t* __restrict__ counts, const int32_t* __restrict__ num_valid,
                         const float* __restrict__ d_loss, O* __restrict__ d_logits) {
-  const int E = b.E, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int E = b.E, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t n = num_valid[0];
   const double g = n > 0 ? (d_loss ? (double)d_loss[0] : 1.0) * (double)E / ((double)n * (double)n * (double)b.k) : 0.0;
   double c[V];   // exactly: their differences may be below what fp32 holds of counts of many ranks
@@ -333,35 +336,36 @@ balance_backward_kernel(Balance b, const int32_t* __restrict__ counts, const int
   const int64_t waves = (int64_t)gridDim.x * kBackWaves;
   for (int64_t t0 = (int64_t)blockIdx.x * kBackWaves + wave; t0 < b.T; t0 += waves * U) {
     bool live[U];
-    float p[U][V];
+    float v[U][V];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * waves;
       live[u] = t < b.T && (!b.mask || b.mask[t]);
-      if (live[u]) load_logits<T, V, NEXT>(static_cast<const T*>(b.logits) + t * E, E, p[u]);
+      if (live[u]) load_logits<T, V, NEXT>(static_cast<const T*>(b.logits) + t * E, E, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * waves;
       if (t >= b.T) break;
-      // sum_i p_i c_i with probabilities that add up to 1: in c_e - dot all of c would stay of what they
-      // lack, beside differences that can be any part of it (every c the same: 0)
-      double dot = 0.0;
-      if (live[u]) {
-        double sum = 0.0;
-        softmax<V>(p[u]);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          dot = __builtin_fma((double)p[u][i], c[i], dot);
-          sum += (double)p[u][i];
-        }
-        dot = wave_sum(dot);
-        sum = wave_sum(sum);
-        if (sum != 0.0) dot /= sum;
-      }
       float d[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = live[u] ? (float)(g * (double)p[u][i] * (c[i] - dot)) : 0.0f;
+      for (int i = 0; i < V; ++i) d[i] = 0.0f;
+      if (live[u]) {
+        // the sums of e_i and e_i c_i, so that probabilities add up to 1: in c_e - mean all of c would
+        // stay of what they lack, beside differences that can be any part of it (every c the same: 0)
+        double e[V], sum = 0.0, dot = 0.0;
+        exponentials<V>(v[u], e);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          sum += e[i];
+          dot = __builtin_fma(e[i], c[i], dot);
+        }
+        sum = wave_sum(sum);
+        dot = wave_sum(dot);
+        const double per = per_sum(sum), mean = dot * per, scale = g * per;
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = (float)(scale * e[i] * (c[i] - mean));
+      }
       store_logits<O, V, NEXT>(d_logits + t * E, E, d);
     }
   }

@@ -97,6 +97,14 @@ __device__ inline floatx4 fp24_unpack4(u32x3 w) {
   return v;
 }
 
+// 1 / v of a positive normal number, to fp64's last bit or the one before: the hardware's first guess
+// and two steps of Newton's.
+__device__ __forceinline__ double reciprocal(double v) {
+  double r = __builtin_amdgcn_rcp(v);
+  r = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
+}
+
 __device__ inline float silu_f(float v) {
   const float kLog2e = 1.4426950408889634f;
   float e = __builtin_amdgcn_exp2f(-v * kLog2e);

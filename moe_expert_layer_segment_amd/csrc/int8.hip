@@ -27,14 +27,8 @@
 
 namespace moelora {
 
-// 1 / v and 1 / sqrt(v) of a positive normal number, to fp64's last bit or the one before: the
-// hardware's first guess and two steps of Newton's.  (Every wave of a row works them out: as
-// quotients and a root of fp64 they took 16384 x 7168 from 215 to 228 us.)
-__device__ __forceinline__ double reciprocal(double v) {
-  double r = __builtin_amdgcn_rcp(v);
-  r = __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
-  return __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);
-}
+// 1 / sqrt(v), as reciprocal of common.hpp.  (Every wave of a row works them out: as quotients and a
+// root of fp64 they took 16384 x 7168 from 215 to 228 us.)
 __device__ __forceinline__ double reciprocal_root(double v) {
   double r = __builtin_amdgcn_rsq(v);
 #pragma unroll

@@ -139,3 +139,32 @@ def test_counts_past_24_bits(E, base):
     noise = LAST * E / (float(n) ** 2 * 8) * base
     tol = 2.01 * D * size + HALF[torch.float32] * (np.abs(ref) + 2.01 * D * size) + noise + TINY
     assert (np.abs(d - ref) <= tol).all()
+
+
+# ---------------------------------------------------------------------------
+# probabilities
+# ---------------------------------------------------------------------------
+# A probability before it is rounded: in 2^f = 1 + f (ln 2 + f (c + f R(f))) R is fp32, two half steps of a
+# number below 2^-4 and less than another from the steps before, times |f|^3 <= 1/8, of a result above 0.7,
+# and what the series leaves out 2^-31: below 2^-29.  The sum of them is off by as much.
+P = 2.0 ** -28
+
+
+def test_probabilities_have_more_bits_than_fp32():
+    """mean_probs of a token alone, the loss and the gradient are off by little more than their last
+    rounding, down to the last numbers that fp32 has."""
+    say("probabilities")
+    ids = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    half = HALF[torch.float32] * (1 + P)
+    for E in (7, 64, 256, 1024):
+        near = torch.randn(40, E, generator=torch.Generator().manual_seed(8)).cuda()
+        for logits in (near, 4 * near, far_rows(E, 40, 9, 110.0)):
+            p = ib.softmax(np64(logits))
+            for t in range(40):
+                stats = binding.moe_lora_balance_loss(logits[t:t + 1], ids)
+                assert (np.abs(np64(stats["mean_probs"]) - p[t]) <= (P + half) * p[t] + 2.0 ** -150).all()
+                assert abs(float(stats["loss"].cpu()[0]) - E * p[t, 0]) <= (P + half) * E * p[t, 0] + 2.0 ** -150
+            counts = torch.randint(0, 99, (E,), generator=torch.Generator().manual_seed(10))
+            d, (ref, size) = np64(gradient(logits, counts)), differences(logits, counts)
+            noise = LAST * E / 40.0 ** 2 * 99 * p
+            assert (np.abs(d - ref) <= 2.01 * P * size + half * (np.abs(ref) + 2.01 * P * size) + noise + 2.0 ** -150).all()
