@@ -554,7 +554,8 @@ int moe_lora_mx4_gemm(const moe_lora_mx4_gemm_args* args, void* stream);
  * channels of every expert.
  *   num_rows_used  device int32, or NULL: rows from *num_rows_used on are skipped
  *                  and their outputs left as they were (num_rows_padded of align).
- * moe_lora_int8_dequantize: out = code * scale, rounded once to dtype.
+ * moe_lora_int8_dequantize: out = code * scale rounded to fp32, and for BF16 from there (so
+ * that next to the middle of two bf16 numbers it may be the other one).
  * dtype (of x / out): F32 or BF16.  1 <= cols <= 2^24, num_rows * cols <= 2^40.  Any
  * pointer aligned to its element works.
  */
@@ -573,12 +574,16 @@ int moe_lora_int8_dequantize(int64_t num_rows, int32_t cols, int32_t dtype, cons
  *   x, residual   [num_tokens, hidden] in dtype; residual NULL: h = x.
  *   weight        [hidden] in weight_dtype.
  *   codes, scales n in 8-bit integers, as moe_lora_int8_quantize of n: of n unrounded, and
- *                 n is that of h unrounded.
+ *                 n is that of h unrounded, both in fp64.  Its last bits are rounded, so that a
+ *                 scale may be the fp32 number beside that of the formula, and a code the
+ *                 integer beside it where the quotient is within 1e-9 of the middle of two.
+ *                 A scale past fp32's range is infinity, with codes 0.
  *   residual_out  [num_tokens, hidden] out, h in dtype; NULL: not written.  May be
  *                 `residual` or `x` itself; no other output may overlap an input.
  *   y             [num_tokens, hidden] out, n in y_dtype (for the router); NULL: not written.
+ * h and n are rounded to fp32, and for BF16 from there.
  * dtypes: F32 or BF16 each.  1 <= hidden <= 16384 (else MOE_LORA_ERR_UNSUPPORTED),
- * eps >= 0 and finite.  Any pointer aligned to its element works.
+ * eps >= 0 and finite in fp32.  Any pointer aligned to its element works.
  */
 int moe_lora_rms_norm_quantize(int64_t num_tokens, int32_t hidden, int32_t dtype,
                                int32_t weight_dtype, int32_t y_dtype, double eps, const void* x,

@@ -1154,8 +1154,8 @@ def moe_lora_int8_quantize(x: torch.Tensor, num_rows_used: Optional[torch.Tensor
 
 def moe_lora_int8_dequantize(codes: torch.Tensor, scales: torch.Tensor,
                              out: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
-    """The values [.., K] that codes and scales stand for (bfloat16 unless ``out_dtype``
-    or ``out`` says float32).  There is no gradient: scales that require one are refused
+    """The values [.., K] that codes and scales stand for, rounded to float32 and from there to
+    bfloat16, unless ``out_dtype`` or ``out`` says float32.  There is no gradient: scales that require one are refused
     where autograd is on."""
     K = _int8_pair(codes, scales, "x")
     if scales.requires_grad:

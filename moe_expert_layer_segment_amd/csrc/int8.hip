@@ -5,10 +5,11 @@
 //   norm       h = x + residual,  n = h * weight / sqrt(mean(h^2) + eps),  n quantized;
 //              h and n themselves on request
 //
-// The integers are those of the formula to the bit: next to the border of two of them the
-// quotient of fp32 values is not decided by an fp32 quotient, so from the sums of squares on
-// all is fp64, whose units (half the fp32 rate) have time to spare under these kernels, which
-// memory bounds.  A row with an infinity or a NaN gets the scale NaN and codes 0, a row of
+// The integers of a quantisation are those of the formula to the bit: next to the border of two of
+// them the quotient of fp32 values is not decided by an fp32 quotient.  The norm is not a quotient
+// of fp32 values; its integers are those of the formula in fp64, but within 1e-9 of a border.  So all
+// from the sums of squares on is fp64, whose units (half the fp32 rate) have time to spare under
+// these kernels, which memory bounds.  What is stored as bf16 is rounded to fp32 first.  A row with an infinity or a NaN gets the scale NaN and codes 0, a row of
 // zeros (or one whose scale is below fp32) the scale 0 and codes 0.
 //
 // A row is read once: its threads keep it in registers between the maximum and the codes.  In
