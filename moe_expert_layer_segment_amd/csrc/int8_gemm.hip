@@ -648,20 +648,12 @@ constexpr int64_t kShortK = 512;
 // us, 8192 of 32 x 8192 x 4096 486 and 511, x 4096 x 7168 475 and 447.
 constexpr int64_t kLongK = 4096;
 
-// In blocks of 16 and of 32 rows, with that many rows an expert, weights are streamed for each block;
-// with more, a tile takes 64 rows of an expert.  A layer of 32 experts of 4096 x 2048, streamed and by
-// tiles: 12 rows an expert 217 and 265 us in blocks of 16 rows, 215 and 230 in blocks of 32; 24 rows
-// 301 and 250, 242 and 274; 32 rows 355 and 270, 286 and 278; 64 rows 567 and 271, 408 and 275.
-constexpr int64_t kFewRows = 20;
-
 hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t s) {
   // rows of a workgroup: within one tile_expert entry, or those there are
   const int64_t rows = p.tile_expert ? p.BM : p.M;
   auto takes = [&](int64_t n) { return p.tile_expert ? rows % n == 0 : rows > n / 2; };
   const int64_t n_tiles = ceil_div(p.N, kTileN), of64 = ceil_div(p.M, 64) * n_tiles;
-  // rows that hold a pair, about: without their number half of the blocks' last rows do not
-  const int64_t held = p.row_ids ? p.num_ids : p.M - p.E * p.BM / 2;
-  const bool many = p.tile_expert ? p.BM > 32 || held > kFewRows * p.E : takes(64);
+  const bool many = p.tile_expert ? !int8_few_rows(p) : takes(64);
   // (64 workgroups of tiles and fewer: 64 rows x 8192 x 2048 20 us, streamed 11; 256 x 4096 x 4096,
   // with 64, 30 and 26; 256 x 8192 x 2048, with 128, 19 and 27)
   if (many && of64 > 64) {

@@ -133,6 +133,20 @@ struct Int8Gemm {
   void* out;                         // [M, N], or [M, N / 2] with silu_mul
 };
 hipError_t launch_int8_gemm(const Int8Gemm& p, hipStream_t stream);
+// In blocks of 16 rows with up to 14 rows an expert, and of 32 rows with up to 20, weights are streamed
+// for each block; with more, a tile takes 64 rows of an expert.  Layers (run_int8_layer in a graph)
+// streamed and by tiles, us, with 12, 16, 20, 24 and 32 rows an expert:
+//   32 experts of 4096 x 2048   blocks of 16   225, 250, 283, 299, 354   246, 251, 253, 224, 255
+//                               blocks of 32   213, 221, 228, 233, 281   234, 235, 236, 235, 262
+//   128 experts of 2048 x 768   blocks of 16   180, 206, 229, 244, 283   168, 172, 179, 178, 195
+//                               blocks of 32   191, 195, 201, 207, 243   175, 176, 177, 181, 202
+//   16 experts of 4096 x 6144   blocks of 16   305, 354, 412, 438, 509   313, 316, 334, 333, 337
+//                               blocks of 32   295, 307, 315, 321, 399   308, 307, 307, 309, 336
+inline bool int8_few_rows(const Int8Gemm& p) {
+  // rows that hold a pair, about: without their number half of the blocks' last rows do not
+  const int64_t held = p.row_ids ? p.num_ids : p.M - p.E * p.BM / 2;
+  return p.BM <= 32 && held <= (p.BM == 16 ? 14 : 20) * p.E;
+}
 
 // ---- balance loss ----------------------------------------------------------
 struct Balance {
