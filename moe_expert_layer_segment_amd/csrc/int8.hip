@@ -338,8 +338,10 @@ static hipError_t launch_norm(const Int8Rows& p, hipStream_t stream) {
   if (units <= 256) return go_rows(int8_norm_kernel<T, V, 256, 1>, 256, 1, p, stream);
   if (units <= 512) return go_rows(int8_norm_kernel<T, V, 256, 2>, 256, 1, p, stream);
   if (units <= 1024) return go_rows(int8_norm_kernel<T, V, 512, 2>, 512, 1, p, stream);
-  if (V == 8 || units <= 2048) return go_rows(int8_norm_kernel<T, V, 1024, 2>, 1024, 1, p, stream);
-  return go_rows(int8_norm_kernel<float, 4, 1024, 4>, 1024, 1, p, stream);
+  if constexpr (V == 4) {   // eights are 2048 at the most
+    if (units > 2048) return go_rows(int8_norm_kernel<T, V, 1024, 4>, 1024, 1, p, stream);
+  }
+  return go_rows(int8_norm_kernel<T, V, 1024, 2>, 1024, 1, p, stream);
 }
 
 hipError_t launch_int8_rows(const Int8Rows& p, hipStream_t stream) {

@@ -70,7 +70,7 @@ __device__ __forceinline__ int64_t weight_row(const Int8Gemm& p, int64_t cb) {
 // columns; its WV waves take every WV-th group of 128 values of K and add their sums through LDS.
 template <int MB, int NB, int WV>
 __global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2)
-int8_stream_kernel(Int8Gemm p, int row_groups, int col_groups) {
+int8_stream_kernel(Int8Gemm p, int col_groups) {
   constexpr int H = 2;   // 64-value steps of a group
   __shared__ int4v sums[WV][MB * NB][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -192,7 +192,7 @@ static hipError_t stream(const Int8Gemm& p, hipStream_t stream) {
   const int64_t col_groups = ceil_div(p.N / 16, NB), row_groups = ceil_div(p.M, 16 * MB);
   const auto kernel = int8_stream_kernel<MB, NB, WV>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(row_groups * col_groups)), dim3(64 * WV), 0, stream, p,
-                     (int)row_groups, (int)col_groups);
+                     (int)col_groups);
   return hipGetLastError();
 }
 
