@@ -1305,9 +1305,9 @@ def int8_block_m(num_tokens: int, top_k: int, num_experts: int) -> int:
     so that its weights are read few times, without many padding rows.
 
     Blocks of 16, 32 and 64 rows in run_int8_layer with 32 experts of 4096 x 2048, routed at
-    random (us): 8 rows an expert 200, 208, 240; 16 rows 250, 227, 240; 32 rows 356, 282, 246.  Of
-    64, 128 and 256 rows: 128 rows an expert 337, 343, 333; 192 rows 417, 427, 355; 512 rows 815,
-    782, 671.  With experts of 2048 x 768: 16 rows 76, 70, 73; 128 rows 99, 111, 114; 192 rows 124,
+    random (us): 8 rows an expert 202, 208, 243; 16 rows 250, 223, 243; 32 rows 255, 258, 246.  Of
+    64, 128 and 256 rows: 128 rows an expert 302, 315, 310; 192 rows 362, 377, 333; 512 rows 725,
+    755, 609.  With experts of 2048 x 768: 16 rows 76, 70, 73; 128 rows 99, 111, 114; 192 rows 124,
     132, 125; 256 rows 149, 145, 171; 512 rows 260, 246, 236."""
     per = num_tokens * top_k / num_experts
     return 16 if per <= 12 else 32 if per <= 20 else 64 if per <= 160 else 256

@@ -17,7 +17,7 @@
 // tokens are one workgroup, and one launch.
 //
 // Latency bounds small batches, and the instructions of the softmax large ones: 16384 tokens of 256
-// experts in fp32 take 10 us forward (17 MB: 3 at the rate of reading), 5.5 for the finish, and 12
+// experts in fp32 take 11 us forward (17 MB: 3 at the rate of reading), 5.5 for the finish, and 12
 // back (34 MB: 7).
 #include <hip/hip_runtime.h>
 
@@ -33,8 +33,8 @@ static constexpr int kBalBlocks = 256;        // whose sums are added by the fin
 static constexpr int kFinishWide = 32;        // experts of one of its workgroups
 static constexpr int kFinishGroups = (int)kMaxBalanceExperts / kFinishWide;
 // tokens that one workgroup takes alone, without a second launch and its workspace (of 128 experts
-// in a graph: 64 tokens 6.8 us, by two launches 8.1; 128 tokens 9.4 and 8.6; 256 15.1 and 8.6; calls
-// made one by one take longer than that on the host)
+// in a graph: 64 tokens 7.3 us, by two launches 8.5; 96 tokens 9.3 and 8.6; 128 10.6 and 8.3; 192 13.9 and
+// 8.8; calls made one by one take longer than that on the host, and more by two launches)
 static constexpr int kBalSingle = 128;
 
 struct BalanceWs {

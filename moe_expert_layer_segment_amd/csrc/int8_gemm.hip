@@ -65,8 +65,10 @@ __device__ __forceinline__ int64_t weight_row(const Int8Gemm& p, int64_t cb) {
 }
 
 // ---- few rows --------------------------------------------------------------
-// The weights are streamed from memory into registers, once, and bound the kernel (64 tokens x 8
-// of 128 experts, 1536 x 2048 each: 74 us, 5.3 TB/s).  A workgroup holds 16 MB rows and 16 NB
+// The weights are streamed from memory into registers, once for each 16 MB rows, and bound the kernel
+// where that is once for an expert (64 tokens x 8 of 128 experts, 1536 x 2048 each: 74 us, 5.3 TB/s);
+// with more rows the groups read them again, and x once for each of the columns' workgroups (2112 x
+// 7168 with 17 rows 10.7 us, 64 19.4, 128 23.7).  A workgroup holds 16 MB rows and 16 NB
 // columns; its WV waves take every WV-th group of 128 values of K and add their sums through LDS.
 template <int MB, int NB, int WV>
 __global__ void __launch_bounds__(64 * WV, MB == 1 ? 4 : 2)
