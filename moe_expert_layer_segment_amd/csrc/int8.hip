@@ -9,8 +9,9 @@
 // them the quotient of fp32 values is not decided by an fp32 quotient.  The norm is not a quotient
 // of fp32 values; its integers are those of the formula in fp64, but within 1e-9 of a border.  So all
 // from the sums of squares on is fp64, whose units (half the fp32 rate) have time to spare under
-// these kernels, which memory bounds.  What is stored as bf16 is rounded to fp32 first.  A row with an infinity or a NaN gets the scale NaN and codes 0, a row of
-// zeros (or one whose scale is below fp32) the scale 0 and codes 0.
+// these kernels, which memory bounds.  What is stored as bf16 is rounded to fp32 first.  A row with an
+// infinity or a NaN gets the scale NaN and codes 0, a row of zeros (or one whose scale is below fp32)
+// the scale 0 and codes 0.
 //
 // A row is read once: its threads keep it in registers between the maximum and the codes.  In
 // the norm max |n| = max |h weight| / sqrt(..), so one exchange between the threads gives the
